@@ -63,6 +63,7 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
                                    request longer than its block-table row */
 #define PKV_ERR_TIMEOUT 8u      /* a bounded wait inside a kernel gave up */
 #define PKV_ERR_POSITION 16u    /* a position outside [0, max_position) */
+#define PKV_ERR_NO_BLOCKS 32u   /* a device-built step needs more free blocks than there are */
 
 const char* pkv_last_error(void);
 int pkv_version(void);
@@ -361,6 +362,129 @@ int pkv_paged_attention_varlen_noalloc(const void* q, int64_t q_stride, const vo
                                        int32_t block_size, int32_t num_heads,
                                        int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
                                        int32_t max_query_len, uint32_t* error_word, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit paged cache (microscaled e2m1, "MXFP4")  [the same paged layout and
+ * slot rule as above, 4.25 bits a value in place of 16: AI Infra, section "Paged
+ * Attention"]
+ *
+ * One layer's key cache and value cache are each uint8 [num_blocks,
+ * pkv_mxfp4_block_bytes()], contiguous and 16-byte aligned; block_size 16,
+ * head_dim 64 or 128, any number of KV heads.  32 consecutive dimensions of
+ * one (token, KV head) share a scale byte e, and a value is code * 2^(e - 127)
+ * with a 4-bit e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6, and their negatives):
+ *   amax = max |x| over the 32;  e = clamp(floor(log2 amax) - 2 + 127, 1, 254);
+ *   code = x 2^(127 - e), rounded to nearest even, saturating at +-6;
+ * e = 127 where all 32 are zero, and e = 255 with zero codes where one of them
+ * is NaN or infinite: the 32 then read as NaN.
+ *
+ * Block bytes.  KV head h owns bytes [h C, (h + 1) C), C = 17 head_dim / 2: 16
+ * rows (tokens) of head_dim / 2 code bytes, then 16 head_dim / 32 scale bytes.
+ * With D = head_dim and b = d / 32, of dimension d (even d: low nibble)
+ *   the K code is in byte ((d % 32) / 8) D/8 + 4 b + (d % 8) / 2 of its row,
+ *   the V code is in byte ((d % 32) / 4) D/16 + 2 b + (d % 4) / 2 of its row,
+ *   the K scale of row t is scale byte t D/32 + b,
+ *   the V scale of row t is scale byte (t / 2) D/16 + (b / 2) 4 + (t % 2) 2 + b % 2.
+ * A block is self-contained, so pkv_copy_blocks moves blocks of such pools
+ * (block_bytes = pkv_mxfp4_block_bytes()).
+ * ---------------------------------------------------------------------- */
+/* Bytes of one block of one cache, or 0 for a shape that is not supported. */
+int64_t pkv_mxfp4_block_bytes(int32_t block_size, int32_t num_kv_heads, int32_t head_dim);
+
+/* pkv_reshape_and_cache into the 4-bit cache: token t's K and V rows are
+ * quantised and written at slot_mapping[t].  Arguments, padding (a negative
+ * slot) and PKV_ERR_SLOT as there; dtype is the one of key and value
+ * (PKV_BF16 or PKV_F32).  Only the addressed rows' bytes are written.  Slots
+ * must be distinct: of a slot given twice the row is one of its tokens' or a
+ * mix of them. */
+int pkv_reshape_and_cache_mxfp4(const void* key, const void* value, int64_t key_stride,
+                                int64_t value_stride, void* key_cache, void* value_cache,
+                                const int64_t* slot_mapping, int64_t num_tokens,
+                                int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t dtype, uint32_t* error_word,
+                                void* stream);
+
+/* The inverse: key_out[t] and value_out[t] (dtype PKV_BF16 or PKV_F32, token
+ * strides in elements) receive the values at slot_mapping[t], exactly.  A
+ * negative slot leaves the token's output rows as they were; a slot past the
+ * pool gives zeros and sets PKV_ERR_SLOT. */
+int pkv_gather_cache_mxfp4(const void* key_cache, const void* value_cache,
+                           const int64_t* slot_mapping, void* key_out, void* value_out,
+                           int64_t key_out_stride, int64_t value_out_stride, int64_t num_tokens,
+                           int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t dtype, uint32_t* error_word, void* stream);
+
+/* pkv_paged_attention_varlen over 4-bit caches: the same definition with K and
+ * V the values the caches stand for, sums and softmax in float32.  q and out
+ * are bfloat16; num_heads / num_kv_heads may be any integer up to 16; at most
+ * 8192 requests.  A block_table row has max_blocks_per_req <= block_table_stride
+ * entries.  max_query_len as there (1: every row is a decode row; longer
+ * ones are then not computed).  Rows of a request whose metadata fails the
+ * checks (PKV_ERR_METADATA), and rows behind the last request, are left as
+ * they were; a block id outside the pool reads as zeros (PKV_ERR_BLOCK_ID).
+ * Bytes of tokens past a request's end may hold anything.
+ *
+ * The workspace is pkv_mxfp4_attention_workspace_bytes() bytes whatever the
+ * batch, zero-filled before its first use, word 0 the error word; two calls
+ * that overlap on the GPU must not share one.  All arguments, the metadata
+ * among them, are read only after the work before the call on `stream`. */
+size_t pkv_mxfp4_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_dim);
+int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void* key_cache,
+                                     const void* value_cache, const int32_t* block_table,
+                                     int32_t block_table_stride, int32_t max_blocks_per_req,
+                                     const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, const int32_t* num_computed_tokens,
+                                     float scale, void* out, int64_t out_stride,
+                                     int64_t num_tokens, int32_t num_reqs, int64_t num_blocks,
+                                     int32_t block_size, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t max_query_len, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Step metadata (device)  [显存调度, section "分配是词元计划的一部分": delta_i =
+ * ceil((T_i + s_i) / B) - ceil(T_i / B), all of a plan's blocks from the front of
+ * the free list or none; AI Infra, section "Paged Attention": the slot rule]
+ *
+ * What the allocator and the scheduler build on the host for one step, from
+ * lengths that live on the device: request r holds T_r = num_computed_tokens[r]
+ * tokens in the first ceil(T_r / block_size) blocks of its block_table row and
+ * gets s_r = query_lens[r] >= 0 new ones.
+ *   block_table row r (max_blocks_per_req <= block_table_stride entries) gains
+ *     its delta_r new blocks, taken in request order from
+ *     free_ring[head % ring_size], [(head + 1) % ring_size], ...;
+ *   query_start_loc [num_reqs + 1]: exclusive sums of s_r; seq_lens[r] = T_r + s_r;
+ *   positions[t] (may be NULL) and slot_mapping[t] of every new token, requests
+ *     in order; behind the last one, up to num_tokens, position 0 and slot -1
+ *     (padding, which the cache writes skip);
+ *   free_state_out = {head + the blocks taken, tail}.
+ * free_ring is int32 [ring_size], a ring of free block ids; free_state is
+ * int64 [4] = {head, tail, 0, 0}, head and tail counting the blocks ever taken
+ * and ever returned (0 <= head <= tail <= head + ring_size).  To return a block
+ * write it at free_ring[tail % ring_size] and add one to tail.  free_state_out
+ * may be free_state (then words 2 and 3 must be zero, and are left so) or
+ * another int64 [2].
+ *
+ * Nothing is taken and the step is an empty one (query_start_loc all zero,
+ * seq_lens = T, every slot -1, every position 0, block_table and the ring's
+ * state unchanged) if it needs more blocks than are free (PKV_ERR_NO_BLOCKS), or
+ * if a length is negative, a request would outgrow its row, the new tokens do
+ * not fit in num_tokens, or free_state is inconsistent (PKV_ERR_METADATA).  A
+ * held block with a negative id in the table gives its tokens slot -1 and sets
+ * PKV_ERR_BLOCK_ID.
+ *
+ * All pointers are device memory; the outputs must not overlap the inputs
+ * (except free_state_out).  block_size must be 16, num_reqs at most 8192.  The
+ * bf16 and float32 attention entry points above read their metadata early
+ * (see "Ordering" there): let the step's cache write, or any other kernel or
+ * copy, come between this call and them.
+ * ---------------------------------------------------------------------- */
+int pkv_build_step_metadata(const int32_t* query_lens, const int32_t* num_computed_tokens,
+                            int32_t num_reqs, int32_t* block_table, int32_t block_table_stride,
+                            int32_t max_blocks_per_req, const int32_t* free_ring, int64_t ring_size, int64_t* free_state,
+                            int64_t* free_state_out, int32_t block_size, int64_t num_tokens,
+                            int32_t* query_start_loc, int32_t* seq_lens, int64_t* slot_mapping,
+                            int64_t* positions, uint32_t* error_word, void* stream);
 
 /* ------------------------------------------------------------------------
  * Step metadata (host)  [AI Infra, section "Paged Attention": slot_idx =

@@ -12,6 +12,9 @@ It is plain, slow and meant to be read against the pages:
 * `attention` - dense per-request causal GQA softmax attention in float64
 * `rope`      - table-driven rotary embedding of Q and K (a dense rotation
                 matrix per token) and its fusion with the cache scatter
+* `mxfp4`     - the 4-bit cache a value at a time (quantisation in exact
+                fractions, the block layout, reading back) and the step
+                metadata that the device builds, a token at a time
 * `allocator` - a list-based block allocator with reserve / commit / rollback
 * `scheduler` - a list-based continuous-batching scheduler with recompute
                 preemption, and the step metadata built from its plan
@@ -37,6 +40,10 @@ What pins each part (tests/test_oracle_*.py, run with -m "not gpu"):
   rope            - complex multiplication by e^{ia} (numpy), unit-vector
                     closed forms, orthogonality, the relative-position
                     property, pass-through of dimensions >= rotary_dim
+  mxfp4           - the e2m1 grid enumerated, ties and saturation by hand,
+                    every (code, scale) pair against its closed form, layout
+                    places a bijection onto the block's bytes; the step
+                    metadata against the allocator and `paging`
   allocator       - the conservation law and reserve / commit / rollback
                     protocol of "显存与调度" checked after every transition,
                     telescoping of the incremental block demand

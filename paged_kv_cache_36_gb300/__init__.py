@@ -14,14 +14,17 @@ import ctypes as C
 import numpy as np
 
 from . import _ffi
-from ._ffi import (ERR_BLOCK_ID, ERR_METADATA, ERR_POSITION, ERR_SLOT, ERR_TIMEOUT,  # noqa: F401
-                   PKV_BF16, PKV_F32)
+from ._ffi import (ERR_BLOCK_ID, ERR_METADATA, ERR_NO_BLOCKS, ERR_POSITION,  # noqa: F401
+                   ERR_SLOT, ERR_TIMEOUT, PKV_BF16, PKV_F32)
 
 __all__ = [
     "PkvError", "lib", "reshape_and_cache", "rope_reshape_and_cache", "copy_blocks",
     "attention_workspace_bytes", "new_workspace",
     "paged_attention_varlen", "reshape_and_cache_paged_attention", "read_error_word",
     "PreparedCall", "prepare_reshape_and_cache_paged_attention",
+    "mxfp4_block_bytes", "new_cache_mxfp4", "reshape_and_cache_mxfp4", "gather_cache_mxfp4",
+    "mxfp4_attention_workspace_bytes", "new_workspace_mxfp4", "paged_attention_varlen_mxfp4",
+    "build_step_metadata",
     "build_slot_mapping", "Allocator", "Scheduler",
 ]
 
@@ -269,6 +272,224 @@ def prepare_reshape_and_cache_paged_attention(key, value, slot_mapping, q, key_c
             query_start_loc, seq_lens, num_computed_tokens, workspace)
     return PreparedCall(lib().pkv_reshape_and_cache_paged_attention, args, keep,
                         "reshape_and_cache_paged_attention")
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit paged cache and the device-built step metadata
+# ---------------------------------------------------------------------------
+def _one_device(where: str, *tensors):
+    """The CUDA device that all the tensors (None allowed) are on."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError(f"{where}: all tensors must be on one CUDA device")
+    return dev
+
+
+def _expect(where: str, name: str, t, dtype, shape=None) -> None:
+    """t is a contiguous tensor of this dtype (and shape)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _device_call(where: str, fn, device, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"{where}: the stream is on another device than the tensors")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_ptr(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_ptr(stream)), where)
+
+
+def _allocating_on(device, stream):
+    """Context in which a call's own buffers are made: on its stream, so that
+    their memory is neither filled nor reused ahead of it."""
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device)
+
+
+def mxfp4_block_bytes(num_kv_heads: int, head_dim: int, block_size: int = 16) -> int:
+    """Bytes of one block of one 4-bit cache."""
+    n = int(lib().pkv_mxfp4_block_bytes(block_size, num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no 4-bit cache of {num_kv_heads} KV heads of {head_dim} in blocks of "
+                         f"{block_size}: head_dim is 64 or 128, block_size 16")
+    return n
+
+
+def new_cache_mxfp4(num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """(key_cache, value_cache): zeroed 4-bit caches, uint8 [num_blocks, block bytes]."""
+    import torch
+    shape = (num_blocks, mxfp4_block_bytes(num_kv_heads, head_dim))
+    return (torch.zeros(shape, dtype=torch.uint8, device=device),
+            torch.zeros(shape, dtype=torch.uint8, device=device))
+
+
+def _mxfp4_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int) -> int:
+    import torch
+    shape = (key_cache.shape[0], mxfp4_block_bytes(num_kv_heads, head_dim))
+    _expect(where, "key_cache", key_cache, torch.uint8, shape)
+    _expect(where, "value_cache", value_cache, torch.uint8, shape)
+    return shape[0]
+
+
+def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, slot_mapping, error_word=None,
+                            stream=None) -> None:
+    """Quantise key/value [T, Hkv, D] (bfloat16 or float32) into the 4-bit caches
+    (new_cache_mxfp4) at slot_mapping[T] (int64; negative: padding)."""
+    import torch
+    where = "reshape_and_cache_mxfp4"
+    T, hkv, d = key.shape
+    if value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError(f"{where}: key and value must have one shape and dtype")
+    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
+    _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
+    dev = _one_device(where, key, value, key_cache, value_cache, slot_mapping, error_word)
+    _device_call(where, lib().pkv_reshape_and_cache_mxfp4, dev, stream, key.data_ptr(),
+                 value.data_ptr(), _token_stride(key), _token_stride(value), key_cache.data_ptr(),
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d,
+                 _dtype_code(key), error_word.data_ptr() if error_word is not None else None)
+
+
+def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out, error_word=None,
+                       stream=None):
+    """Read the rows at slot_mapping[T] (int64; negative: the row of the outputs
+    is left alone) back from the 4-bit caches into key_out and value_out
+    [T, Hkv, D], bfloat16 or float32; exact.  Returns (key_out, value_out)."""
+    import torch
+    where = "gather_cache_mxfp4"
+    T, hkv, d = key_out.shape
+    if value_out.shape != key_out.shape or value_out.dtype != key_out.dtype:
+        raise ValueError(f"{where}: key_out and value_out must have one shape and dtype")
+    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
+    _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
+    dev = _one_device(where, key_cache, value_cache, slot_mapping, key_out, value_out, error_word)
+    _device_call(where, lib().pkv_gather_cache_mxfp4, dev, stream, key_cache.data_ptr(),
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), key_out.data_ptr(),
+                 value_out.data_ptr(), _token_stride(key_out), _token_stride(value_out), T, nb, 16,
+                 hkv, d, _dtype_code(key_out),
+                 error_word.data_ptr() if error_word is not None else None)
+    return key_out, value_out
+
+
+def mxfp4_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    n = int(lib().pkv_mxfp4_attention_workspace_bytes(num_heads, num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no attention over 4-bit caches of {num_heads}/{num_kv_heads} heads of "
+                         f"{head_dim}: up to 16 whole query heads per KV head, head_dim 64 or 128")
+    return n
+
+
+def new_workspace_mxfp4(num_heads: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A zero-filled workspace of paged_attention_varlen_mxfp4, for any batch."""
+    import torch
+    return torch.zeros(mxfp4_attention_workspace_bytes(num_heads, num_kv_heads, head_dim),
+                       dtype=torch.uint8, device=device)
+
+
+def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_start_loc, seq_lens,
+                                 num_computed_tokens, scale: float, out=None, workspace=None,
+                                 max_query_len: int = 0, stream=None):
+    """paged_attention_varlen over the 4-bit caches: causal GQA attention of the
+    flattened batch q [T, H, D] (bfloat16), up to 16 query heads per KV head.
+    The number of KV heads is the one the caches' block size gives.  Returns
+    out [T, H, D]; rows that belong to no request are left as they were."""
+    import torch
+    where = "paged_attention_varlen_mxfp4"
+    T, H, D = q.shape
+    nb, block_bytes = key_cache.shape
+    hkv = max(1, block_bytes // mxfp4_block_bytes(1, D))
+    _mxfp4_pools(where, key_cache, value_cache, hkv, D)
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"{where}: q must be bfloat16")
+    R = seq_lens.shape[0]
+    if block_table.dtype != torch.int32 or block_table.shape[0] != R:
+        raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
+    _expect(where, "query_start_loc", query_start_loc, torch.int32, (R + 1,))
+    _expect(where, "seq_lens", seq_lens, torch.int32, (R,))
+    _expect(where, "num_computed_tokens", num_computed_tokens, torch.int32, (R,))
+    dev = _one_device(where, q, key_cache, value_cache, block_table, query_start_loc, seq_lens,
+                      num_computed_tokens, workspace, out)
+    if out is None or workspace is None:
+        with _allocating_on(dev, stream):
+            if out is None:
+                out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+            if workspace is None:
+                workspace = new_workspace_mxfp4(H, hkv, D, dev)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"{where}: out must have q's shape and dtype")
+    _device_call(where, lib().pkv_paged_attention_varlen_mxfp4, dev, stream, q.data_ptr(),
+                 _token_stride(q), key_cache.data_ptr(), value_cache.data_ptr(),
+                 block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
+                 query_start_loc.data_ptr(), seq_lens.data_ptr(), num_computed_tokens.data_ptr(),
+                 float(scale), out.data_ptr(), _token_stride(out), T, R, nb, 16, H, hkv, D, int(max_query_len),
+                 workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring, free_state,
+                        num_tokens: int, free_state_out=None, query_start_loc=None, seq_lens=None,
+                        slot_mapping=None, positions=None, error_word=None, block_size: int = 16,
+                        stream=None):
+    """The step's metadata built on the device from request lengths (int32 [R]
+    tensors): takes each request's new blocks from free_ring (int32) in request
+    order, appends them to its row of block_table (int32 [R, max_blocks], in
+    place), and returns (query_start_loc int32 [R + 1], seq_lens int32 [R],
+    slot_mapping int64 [num_tokens], positions int64 [num_tokens]), padded with
+    slot -1 and position 0 behind the last new token.  free_state is int64 [4]
+    = {blocks ever taken, blocks ever returned, 0, 0}; the new counts go to
+    free_state_out (default: free_state, in place).  A step that does not fit is
+    refused whole: an empty step, with the reason's bit in error_word."""
+    import torch
+    where = "build_step_metadata"
+    R, T = query_lens.shape[0], int(num_tokens)
+    i32, i64 = torch.int32, torch.int64
+    _expect(where, "query_lens", query_lens, i32, (R,))
+    _expect(where, "num_computed_tokens", num_computed_tokens, i32, (R,))
+    if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
+    _expect(where, "free_ring", free_ring, i32, (free_ring.numel(),))
+    _expect(where, "free_state", free_state, i64, (4,))
+    dev = _one_device(where, query_lens, num_computed_tokens, block_table, free_ring, free_state,
+                      free_state_out, query_start_loc, seq_lens, slot_mapping, positions,
+                      error_word)
+    if any(t is None for t in (query_start_loc, seq_lens, slot_mapping, positions)):
+        with _allocating_on(dev, stream):
+            new = dict(device=dev)
+            if query_start_loc is None:
+                query_start_loc = torch.empty(R + 1, dtype=i32, **new)
+            if seq_lens is None:
+                seq_lens = torch.empty(R, dtype=i32, **new)
+            if slot_mapping is None:
+                slot_mapping = torch.empty(T, dtype=i64, **new)
+            if positions is None:
+                positions = torch.empty(T, dtype=i64, **new)
+    _expect(where, "query_start_loc", query_start_loc, i32, (R + 1,))
+    _expect(where, "seq_lens", seq_lens, i32, (R,))
+    _expect(where, "slot_mapping", slot_mapping, i64, (T,))
+    _expect(where, "positions", positions, i64, (T,))
+    if free_state_out is None:
+        free_state_out = free_state
+    elif free_state_out.dtype != i64 or free_state_out.numel() < 2 or \
+            not free_state_out.is_contiguous():
+        raise ValueError(f"{where}: free_state_out must be int64 with at least 2 entries")
+    _device_call(where, lib().pkv_build_step_metadata, dev, stream, query_lens.data_ptr(),
+                 num_computed_tokens.data_ptr(), R, block_table.data_ptr(),
+                 _row_stride(block_table), block_table.shape[1], free_ring.data_ptr(),
+                 free_ring.numel(),
+                 free_state.data_ptr(), free_state_out.data_ptr(), block_size, T,
+                 query_start_loc.data_ptr(), seq_lens.data_ptr(), slot_mapping.data_ptr(),
+                 positions.data_ptr(), error_word.data_ptr() if error_word is not None else None)
+    return query_start_loc, seq_lens, slot_mapping, positions
 
 
 # ---------------------------------------------------------------------------

@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "api.h"
 #include "kernels.h"
 #include "pkv_error.h"
 
@@ -20,8 +21,6 @@ constexpr size_t kHeaderBytes = 256;
 constexpr int64_t kMaxTmaRows = 0x7fffffffLL;
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct WorkspaceLayout {
   size_t counters, part_ml, part_o, total;
@@ -149,6 +148,8 @@ int encode_query_map(CUtensorMap* map, const void* q, int64_t q_stride, int64_t 
   return PKV_OK;
 }
 
+}  // namespace
+
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_E_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -157,7 +158,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 // for its stream, reads its device error word (one device-to-host copy) and
 // turns any PKV_ERR_* bit into PKV_E_INVALID.  Off by default, so no call
 // synchronises.
-bool validate_enabled() {
+static bool validate_enabled() {
   const char* v = std::getenv("PKV_VALIDATE");
   return v && v[0] == '1';
 }
@@ -170,11 +171,10 @@ int validate_error_word(const uint32_t* word, cudaStream_t stream, const char* w
   if (e != cudaSuccess) return cuda_fail(e, where);
   if (bits)
     return fail(PKV_E_INVALID, "%s: the kernels reported error bits 0x%x (1 block id, 2 slot, "
-                "4 metadata, 8 timeout, 16 position)", where, bits);
+                "4 metadata, 8 timeout, 16 position, 32 no free blocks)", where, bits);
   return PKV_OK;
 }
 
-}  // namespace
 }  // namespace pkv
 
 using namespace pkv;

@@ -71,6 +71,7 @@ struct AttnArgs {
   int32_t head_dim;
   float scale;
   uint32_t* err;              // device error word
+  int32_t bt_width;           // entries of a block-table row (4-bit caches only)
 };
 
 // Scratch carved out of the caller's workspace for the split-KV decode.
@@ -161,5 +162,53 @@ cudaError_t launch_varlen_bf16(const AttnArgs& a, const CUtensorMap& qmap, const
 // CUDA-core attention, one warp per (query row, head); fp32 path for all rows,
 // or only rows of requests with query length > 1 when skip_decode is set.
 cudaError_t launch_attn_rows(const AttnArgs& a, bool bf16, bool skip_decode, cudaStream_t stream);
+
+// Rows of K and V into (or out of) the 4-bit paged cache; strides in elements.
+// The gather writes through key / value.
+struct MxCacheArgs {
+  const void* key;
+  const void* value;
+  int64_t key_stride;
+  int64_t value_stride;
+  uint8_t* key_cache;
+  uint8_t* value_cache;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  bool bf16;
+  uint32_t* err;
+};
+
+cudaError_t launch_reshape_and_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
+cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
+
+// Attention over the 4-bit paged cache on CUDA cores, one warp per (query
+// row, head).
+cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, bool decode_only, cudaStream_t stream);
+
+// A step's metadata built on the device.
+struct StepMetadataArgs {
+  const int32_t* query_lens;
+  const int32_t* num_computed;
+  int32_t* block_table;
+  int32_t bt_stride;
+  int32_t bt_width;         // entries of a row
+  const int32_t* free_ring;
+  int64_t ring_size;
+  int64_t* free_state;      // head, tail, ticket (zero between calls), unused
+  int64_t* free_state_out;  // may be free_state itself
+  int32_t* query_start_loc;
+  int32_t* seq_lens;
+  int64_t* slot_mapping;
+  int64_t* positions;       // may be null
+  int64_t num_tokens;
+  int32_t num_reqs;
+  uint32_t* err;            // may be null
+};
+
+int step_metadata_max_reqs();
+cudaError_t launch_step_metadata(const StepMetadataArgs& a, cudaStream_t stream);
 
 }  // namespace pkv
