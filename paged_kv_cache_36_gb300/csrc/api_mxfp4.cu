@@ -72,6 +72,29 @@ int cache_args(const char* where, const void* rows_k, const void* rows_v, int64_
   return PKV_OK;
 }
 
+struct MxWorkspace {
+  size_t count1, count2, ml, o, total;
+};
+
+// The error word's 256 bytes, then the decode's counters and partials.
+MxWorkspace mx_workspace(int64_t workers, int32_t group, int32_t head_dim) {
+  const size_t slots = 2 * static_cast<size_t>(workers);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  MxWorkspace w;
+  w.count1 = 256;
+  w.count2 = w.count1 + up(slots * 4);
+  w.ml = w.count2 + up(slots * 4);
+  w.o = w.ml + up(slots * group * 8);
+  w.total = w.o + up(slots * group * head_dim * 4);
+  return w;
+}
+
+int current_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  return decode_grid_size(dev);
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -124,7 +147,7 @@ size_t pkv_mxfp4_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_hea
   if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       num_heads / num_kv_heads > kMaxGroup || (head_dim != 64 && head_dim != 128))
     return 0;
-  return 256;  // the error word
+  return mx_workspace(decode_mxfp4_workers(current_sms()), num_heads / num_kv_heads, head_dim).total;
 }
 
 int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void* key_cache,
@@ -149,10 +172,11 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
     return fail(PKV_E_UNSUPPORTED, "%s: at most %d requests and 2^31 - 1 tokens", where,
                 step_metadata_max_reqs());
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
-  const size_t need = pkv_mxfp4_attention_workspace_bytes(num_heads, num_kv_heads, head_dim);
-  if (workspace_bytes < need || !aligned16(workspace))
+  const int sms = current_sms();
+  const MxWorkspace w = mx_workspace(decode_mxfp4_workers(sms), num_heads / num_kv_heads, head_dim);
+  if (workspace_bytes < w.total || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,
-                workspace_bytes, need);
+                workspace_bytes, w.total);
   if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
   if (!q || !key_cache || !value_cache || !block_table || !query_start_loc || !seq_lens ||
       !num_computed_tokens || !out)
@@ -166,6 +190,8 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   if (max_blocks_per_req <= 0 || (num_reqs > 1 && block_table_stride < max_blocks_per_req))
     return fail(PKV_E_INVALID, "%s: block_table rows of %d entries, %d apart", where,
                 max_blocks_per_req, block_table_stride);
+  if (static_cast<int64_t>(num_reqs) * max_blocks_per_req > 0x7fffffffLL)
+    return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
   AttnArgs a;
   a.q = q;
   a.q_stride = q_stride;
@@ -189,7 +215,14 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   a.scale = scale;
   a.err = static_cast<uint32_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_attn_rows_mxfp4(a, max_query_len == 1, st);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxDecodeScratch ds;
+  ds.count1 = reinterpret_cast<int32_t*>(ws + w.count1);
+  ds.count2 = reinterpret_cast<int32_t*>(ws + w.count2);
+  ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  ds.part_o = reinterpret_cast<float*>(ws + w.o);
+  cudaError_t e = launch_decode_mxfp4(a, ds, sms, st);
+  if (e == cudaSuccess && max_query_len != 1) e = launch_attn_rows_mxfp4(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_mxfp4 launch");
   return validate_error_word(a.err, st, "paged_attention_varlen_mxfp4");
 }

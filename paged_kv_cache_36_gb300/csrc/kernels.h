@@ -185,8 +185,24 @@ cudaError_t launch_reshape_and_cache_mxfp4(const MxCacheArgs& a, cudaStream_t st
 cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 
 // Attention over the 4-bit paged cache on CUDA cores, one warp per (query
-// row, head).
-cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, bool decode_only, cudaStream_t stream);
+// row, head), of the rows of requests with query length > 1.
+cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, cudaStream_t stream);
+
+// Scratch of the 4-bit decode: two slots per worker (one warp of an SM), each
+// with a partial of all heads of a KV head and two counters, zero between calls.
+struct MxDecodeScratch {
+  int32_t* count1;            // [2 * workers]
+  int32_t* count2;            // [2 * workers]
+  float* part_ml;             // [2 * workers][group][2]
+  float* part_o;              // [2 * workers][group][head_dim]
+};
+
+// Workers of the 4-bit decode on a device of `sms` SMs.
+int64_t decode_mxfp4_workers(int sms);
+
+// Split-KV decode over the 4-bit cache of the rows of requests with query length 1.
+cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, int sms,
+                                cudaStream_t stream);
 
 // A step's metadata built on the device.
 struct StepMetadataArgs {

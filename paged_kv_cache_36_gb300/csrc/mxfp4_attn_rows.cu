@@ -38,7 +38,7 @@ __device__ __forceinline__ void read_dims(const uint8_t* chunk, int t, int d0,
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) attn_rows_mxfp4_kernel(const AttnArgs a, int decode_only, float scale_log2) {
+__global__ void __launch_bounds__(256) attn_rows_mxfp4_kernel(const AttnArgs a, float scale_log2) {
   grid_dependency_wait();
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) attn_rows_mxfp4_kernel(const AttnArgs a, 
   const int qlen = __ldg(a.qsl + r + 1) - q0;
   const int nc = __ldg(a.num_computed + r);
   const int seq = __ldg(a.seq_lens + r);
-  if (t - q0 >= qlen || (decode_only && qlen != 1)) return;  // also: rows behind the last request
+  if (t - q0 >= qlen || qlen <= 1) return;  // rows behind the last request, decode rows
   if (nc < 0 || seq != nc + qlen || (seq - 1) / kMxBlock >= a.bt_width) {
     if (lane == 0) atomicOr(a.err, PKV_ERR_METADATA);
     return;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) attn_rows_mxfp4_kernel(const AttnArgs a, 
 
 }  // namespace
 
-cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, bool decode_only, cudaStream_t stream) {
+cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, cudaStream_t stream) {
   const int64_t warps = a.num_tokens * a.num_heads;
   if (warps == 0) return cudaSuccess;
   const int64_t blocks = (warps + 7) / 8;
@@ -114,9 +114,9 @@ cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, bool decode_only, cudaStre
   const float scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const dim3 grid(static_cast<unsigned>(blocks));
   if (a.head_dim == 128)
-    return launch_programmatic(attn_rows_mxfp4_kernel<128>, grid, dim3(256), 0, stream, a, decode_only ? 1 : 0, scale_log2);
+    return launch_programmatic(attn_rows_mxfp4_kernel<128>, grid, dim3(256), 0, stream, a, scale_log2);
   if (a.head_dim == 64)
-    return launch_programmatic(attn_rows_mxfp4_kernel<64>, grid, dim3(256), 0, stream, a, decode_only ? 1 : 0, scale_log2);
+    return launch_programmatic(attn_rows_mxfp4_kernel<64>, grid, dim3(256), 0, stream, a, scale_log2);
   return cudaErrorNotSupported;
 }
 
