@@ -73,17 +73,18 @@ int cache_args(const char* where, const void* rows_k, const void* rows_v, int64_
 }
 
 struct MxWorkspace {
-  size_t count1, count2, ml, o, total;
+  size_t plan, ml, o, total;
 };
 
-// The error word's 256 bytes, then the decode's counters and partials.
-MxWorkspace mx_workspace(int64_t workers, int32_t group, int32_t head_dim) {
-  const size_t slots = 2 * static_cast<size_t>(workers);
+// The error word's 256 bytes, then the decode's plan (for the largest batch)
+// and partials.
+MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const size_t slots = static_cast<size_t>(decode_mxfp4_slots(sms, num_kv_heads));
+  const size_t group = static_cast<size_t>(num_heads / num_kv_heads);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   MxWorkspace w;
-  w.count1 = 256;
-  w.count2 = w.count1 + up(slots * 4);
-  w.ml = w.count2 + up(slots * 4);
+  w.plan = 256;
+  w.ml = w.plan + up((static_cast<size_t>(step_metadata_max_reqs()) + 2) * 4);
   w.o = w.ml + up(slots * group * 8);
   w.total = w.o + up(slots * group * head_dim * 4);
   return w;
@@ -147,7 +148,7 @@ size_t pkv_mxfp4_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_hea
   if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       num_heads / num_kv_heads > kMaxGroup || (head_dim != 64 && head_dim != 128))
     return 0;
-  return mx_workspace(decode_mxfp4_workers(current_sms()), num_heads / num_kv_heads, head_dim).total;
+  return mx_workspace(current_sms(), num_heads, num_kv_heads, head_dim).total;
 }
 
 int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void* key_cache,
@@ -173,7 +174,7 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
                 step_metadata_max_reqs());
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
   const int sms = current_sms();
-  const MxWorkspace w = mx_workspace(decode_mxfp4_workers(sms), num_heads / num_kv_heads, head_dim);
+  const MxWorkspace w = mx_workspace(sms, num_heads, num_kv_heads, head_dim);
   if (workspace_bytes < w.total || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,
                 workspace_bytes, w.total);
@@ -217,8 +218,7 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MxDecodeScratch ds;
-  ds.count1 = reinterpret_cast<int32_t*>(ws + w.count1);
-  ds.count2 = reinterpret_cast<int32_t*>(ws + w.count2);
+  ds.plan = reinterpret_cast<int32_t*>(ws + w.plan);
   ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
   ds.part_o = reinterpret_cast<float*>(ws + w.o);
   cudaError_t e = launch_decode_mxfp4(a, ds, sms, st);

@@ -188,17 +188,16 @@ cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream)
 // row, head), of the rows of requests with query length > 1.
 cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, cudaStream_t stream);
 
-// Scratch of the 4-bit decode: two slots per worker (one warp of an SM), each
-// with a partial of all heads of a KV head and two counters, zero between calls.
+// Scratch of the 4-bit decode: the plan that its join follows, and slots that
+// hold one range's partial of the query heads of one KV head.
 struct MxDecodeScratch {
-  int32_t* count1;            // [2 * workers]
-  int32_t* count2;            // [2 * workers]
-  float* part_ml;             // [2 * workers][group][2]
-  float* part_o;              // [2 * workers][group][head_dim]
+  int32_t* plan;              // [num_reqs + 2]
+  float* part_ml;             // [slots][group][2]
+  float* part_o;              // [slots][group][head_dim]
 };
 
-// Workers of the 4-bit decode on a device of `sms` SMs.
-int64_t decode_mxfp4_workers(int sms);
+// Slots of the 4-bit decode on a device of `sms` SMs.
+int64_t decode_mxfp4_slots(int sms, int num_kv_heads);
 
 // Split-KV decode over the 4-bit cache of the rows of requests with query length 1.
 cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, int sms,

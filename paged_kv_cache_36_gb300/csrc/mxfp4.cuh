@@ -48,6 +48,17 @@ __device__ __forceinline__ int mx_vscale_off(int t, int b) {
   return mx_scale_off(D) + (t >> 1) * (D / 16) + (b >> 1) * 4 + (t & 1) * 2 + (b & 1);
 }
 
+// Two scale bytes as bfloat16 powers of two, NaN for 255.
+__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %1;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
 // The two codes of one byte as f16 values (even position in the low half).
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
   uint32_t r;

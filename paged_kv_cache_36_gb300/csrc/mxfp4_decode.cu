@@ -4,20 +4,23 @@
 //   out = sum_j softmax_j(scale <q, K_j>) V_j,
 // K and V the values that codes and power-of-two scales stand for (mxfp4.cuh).
 //
-// Work split.  A unit is one 16-token block of one KV head.  Units are ordered
-// by request, KV head and block, and worker w of W (a worker is one warp) takes
-// units [wN/W, (w+1)N/W): every warp streams the same bytes whatever the
-// context lengths, and no warp waits for another.  A (request, KV head) run
-// that crosses workers leaves one partial (m, l, o) per worker in the
-// workspace; the warp whose count completes a group of kFan partials merges
-// them, and the one that completes the groups merges those, so that even a
-// run of thousands of workers costs two short merges.  The order of every sum
-// is fixed by the split, not by who comes last.
+// Work split.  The decode requests' blocks form one sequence of N blocks, cut
+// into Q ranges [qN/Q, (q+1)N/Q); a range is walked by one warp per KV head,
+// the warps of a range side by side in one CTA, so that every warp streams the
+// same bytes whatever the context lengths, no warp waits for another, and a
+// block's heads are fetched together.  A request that crosses ranges leaves one
+// partial (m, l, o) per range and head in the workspace, and a second kernel
+// joins them,
+//   M = max_s m_s,  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
+// with one thread per four outputs, in the order of the ranges: no counters, no
+// atomics, the same bits every time.  (Joining in this kernel, by the warp that
+// came last, took about 18 us of a 230 us call: one warp reads the partials of
+// a request at the latency of L2.)
 //
-// Data movement.  A warp keeps its own ring of stages, each two units (4.3 KiB
-// at head_dim 128), filled by 16-byte cp.async: a head's chunk of a block is
-// contiguous, K and V.  The fetch cursor runs ahead of the compute over
-// request boundaries, so a new request costs no bubble.
+// Data movement.  A warp keeps its own ring of stages, each two blocks' worth of
+// its head (4.3 KiB at head_dim 128), filled by 16-byte cp.async: a head's
+// chunk of a block is contiguous, K and V.  The fetch cursor runs ahead of the
+// compute over request boundaries, so a new request costs no bubble.
 //
 // Compute.  S^T = K Q^T and O^T += V^T P^T are m16n8k16 f16 products with the
 // query heads of the KV head as N, float32 accumulators.
@@ -30,11 +33,11 @@
 //     float32: any scale is exact.
 //   - V scales go onto the weights: P^T (f16, 11 bits) times 2^(e - base) for
 //     each group of dimensions, `base` a running exponent per group.  Scales
-//     within 2^7 of it, which is nearly always, cost one f16x2 product per
-//     group; a tile outside the window takes the slow path below, which moves
-//     the base and splits the tile into windows so that no weight leaves f16's
-//     range.
-//   - The running maximum moves only when a score exceeds it by 2^8: the common
+//     in the 16 binades from it up, which is nearly always, cost one f16x2
+//     product per group; a tile outside the window takes the slow path below,
+//     which moves the base and splits the tile into windows so that no weight
+//     leaves f16's range.
+//   - The running maximum moves only when a score exceeds it by 2^3: the common
 //     tile needs a vote, and no shuffle.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,12 +53,23 @@ namespace pkv {
 
 namespace {
 
-constexpr int kFan = 16;         // partials per first-level merge, at least
-constexpr int kMinUnits = 8;     // units a worker takes at least (128 tokens of one KV head)
-constexpr float kMaxSlack = 8.f; // log2 units a score may exceed the running maximum by
+constexpr int kMinBlocks = 8;    // blocks in a range at least (128 tokens)
+// Weights stay below 2^kMaxSlack (the running maximum moves when a score
+// exceeds it by more), and a V scale multiplies them by 2^(e - base + kLow) with
+// e - base in [0, 15]: at most 2^(3 + 12), inside f16, and at the window's lower
+// end a weight of 1 still has 11 bits and all weights a resolution of 2^-21.
+constexpr float kMaxSlack = 3.f;
+constexpr int kLow = -3;
+constexpr int kBelow = 11;       // where a new base goes below the largest scale of its tile
+constexpr int kTopBase = 239;
 
 template <int NT>
 constexpr int warps_per_cta() { return NT == 1 ? 16 : 8; }
+// Ranges that a CTA of `warps` warps walks at once; with more KV heads than
+// warps, a warp walks its one range once per head it has.
+__host__ __device__ constexpr int ranges_per_cta(int warps, int hkv) {
+  return warps > hkv ? warps / hkv : 1;
+}
 
 struct Params {
   const __nv_bfloat16* q;
@@ -77,10 +91,9 @@ struct Params {
   int32_t group;
   float scale_log2;
   uint32_t* err;
-  int32_t* count1;   // [2 * workers] arrivals of a first-level group, at its first slot
-  int32_t* count2;   // [2 * workers] completed groups of a run, at its first slot
-  float2* part_ml;   // [2 * workers][group]
-  float* part_o;     // [2 * workers][group][D]
+  int32_t* plan;     // [num_reqs + 2]: block sums and the number of ranges, for the join
+  float2* part_ml;   // [2 * ranges][hkv][group]
+  float* part_o;     // [2 * ranges][hkv][group][D]
   int32_t stages;
 };
 
@@ -98,14 +111,27 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// D = A B + C, m16n8k16, f16 inputs, float32 accumulators.
+// D += A B, m16n8k16, f16 inputs, float32 accumulators.  Not volatile, so that
+// the compiler may interleave independent products.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D = A B.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -121,26 +147,25 @@ __device__ __forceinline__ float pow2(int k) {
   return k < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// A worker's position in the ordered units: block j of nb of (request r, KV
-// head h), `left` units to go.
+// The partial of range q of a request: slot 2q, except that a request which
+// starts inside the range (after its first block) has slot 2q + 1.  A range
+// leaves two partials at most, of the request it begins in and of the one it
+// ends in.
+__device__ __forceinline__ int64_t slot_of(int64_t q, bool starts_inside) {
+  return 2 * q + (starts_inside ? 1 : 0);
+}
+
+// A position in a range: block j of nb of request r; `run` blocks of it are in
+// the range, then `rest` more of later requests.
 struct Cursor {
-  int r, h, j, nb;
-  int64_t left;
-  __device__ __forceinline__ int pair() const {  // units of the next stage: 1 or 2
-    int n = nb - j < 2 ? nb - j : 2;
-    return left < n ? static_cast<int>(left) : n;
-  }
-  __device__ __forceinline__ void advance(int n, const int32_t* prefix, int hkv) {
-    j += n;
-    left -= n;
-    if (j == nb && left > 0) {
-      j = 0;
-      if (++h == hkv) {
-        h = 0;
-        do ++r; while (prefix[r + 1] == prefix[r]);
-        nb = prefix[r + 1] - prefix[r];
-      }
-    }
+  int r, j, nb;
+  int run, rest;
+  __device__ __forceinline__ void next_run(const int32_t* prefix) {
+    do ++r; while (prefix[r + 1] == prefix[r]);
+    nb = prefix[r + 1] - prefix[r];
+    j = 0;
+    run = rest < nb ? rest : nb;
+    rest -= run;
   }
 };
 
@@ -185,89 +210,112 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   __syncthreads();
   block_inclusive_scan(prefix + 1, R, scan_tmp);
   __syncthreads();
-  const int64_t N = static_cast<int64_t>(prefix[R]) * p.hkv;
-  if (N == 0) return;
-  const int64_t most = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t want = (N + kMinUnits - 1) / kMinUnits;
-  const int64_t W = want < most ? want : most;
-  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // spread over the SMs first
-  if (me >= W) return;
-  const int64_t u0 = me * N / W, u1 = (me + 1) * N / W;
-  auto worker_of = [&](int64_t unit) -> int64_t { return ((unit + 1) * W - 1) / N; };
+  const int64_t N = prefix[R];
+  const int per_cta = ranges_per_cta(kWarps, p.hkv);
+  const int64_t most = static_cast<int64_t>(gridDim.x) * per_cta;
+  const int64_t want = (N + kMinBlocks - 1) / kMinBlocks;
+  const int64_t Q = want < most ? want : most;
+  if (blockIdx.x == 0) {
+    for (int r = threadIdx.x; r <= R; r += blockDim.x) p.plan[r] = prefix[r];
+    if (threadIdx.x == 0) p.plan[R + 1] = static_cast<int32_t>(Q);
+  }
+  // few ranges: one per SM first
+  const int64_t me = static_cast<int64_t>(warp / p.hkv) * gridDim.x + blockIdx.x;
+  if (warp / p.hkv >= per_cta || me >= Q) return;
+  const int64_t u0 = me * N / Q, u1 = (me + 1) * N / Q;
 
-  Cursor at;
+  Cursor start;
   {
-    int lo = 0, hi = R;  // prefix[lo] hkv <= u0 < prefix[hi] hkv
+    int lo = 0, hi = R;  // prefix[lo] <= u0 < prefix[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(prefix[mid]) * p.hkv <= u0) lo = mid; else hi = mid;
+      if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
-    at.r = lo;
-    at.nb = prefix[lo + 1] - prefix[lo];
-    const int64_t off = u0 - static_cast<int64_t>(prefix[lo]) * p.hkv;
-    at.h = static_cast<int>(off / at.nb);
-    at.j = static_cast<int>(off - static_cast<int64_t>(at.h) * at.nb);
-    at.left = u1 - u0;
+    start.r = lo;
+    start.nb = prefix[lo + 1] - prefix[lo];
+    start.j = static_cast<int>(u0) - prefix[lo];
+    start.rest = static_cast<int>(u1 - u0);
+    start.run = min(start.rest, start.nb - start.j);
+    start.rest -= start.run;
   }
 
   // ---- the ring: fetch cursor, ids of its next stage already loaded ----
-  const int64_t block_bytes = static_cast<int64_t>(p.hkv) * kChunk;
+  // A lane copies the same 16-byte pieces of every unit: NW of the K codes, NW
+  // of the V codes, and (lanes below 2 NB) one of the scales.  V codes of two
+  // tokens (128 or 64 bytes) are XOR-swizzled by 16-byte pieces, so that the
+  // four token pairs that a quad reads at once hit different banks.
+  const uint32_t block_bytes = static_cast<uint32_t>(p.hkv) * kChunk;
   const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * p.stages * kStage;
-  Cursor next = at;
-  int id0 = 0, id1 = -1;
-  auto load_ids = [&]() {
-    if (next.left <= 0) return;
-    const int32_t* row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride + next.j;
-    id0 = __ldg(row);
-    id1 = next.pair() == 2 ? __ldg(row + 1) : -1;
+  const bool scale_v = lane >= NB;
+  const uint32_t k_dst = ring + lane * 16;
+  const uint32_t v_dst =
+      ring + kChunk +
+      (D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * ((lane >> 3) & 3))) << 4)
+                : (lane ^ (((lane >> 3) & 1) << 1)) << 4);
+  const uint32_t s_dst = ring + kScale + (scale_v ? kChunk + (lane - NB) * 16 : lane * 16);
+  int h = warp < p.hkv ? warp : warp % p.hkv;
+  Cursor next = start;
+  const int32_t* row;               // the next stage's entries of the block table
+  const uint8_t *k_src, *v_src, *s_src;
+  auto enter_run = [&]() {
+    row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride + next.j;
+    const int64_t head = static_cast<int64_t>(h) * kChunk;
+    k_src = p.key_cache + head + lane * 16;
+    v_src = p.value_cache + head + lane * 16;
+    s_src = (scale_v ? p.value_cache + (lane - NB) * 16 : p.key_cache + lane * 16) + head + kScale;
   };
-  // V codes of two tokens (128 or 64 bytes) are XOR-swizzled by 16-byte chunks
-  // so that the four token pairs that a quad row reads at once hit different
-  // banks.
-  const uint32_t v_dst = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * ((lane >> 3) & 3))) << 4)
-                                  : (lane ^ (((lane >> 3) & 1) << 1)) << 4;
+  uint32_t id0, id1;
+  auto load_ids = [&]() {
+    id0 = static_cast<uint32_t>(__ldg(row));
+    id1 = next.run > 1 ? static_cast<uint32_t>(__ldg(row + 1)) : 0u;
+  };
+  const uint32_t num_blocks = static_cast<uint32_t>(p.num_blocks);
   auto fetch = [&](int slot) {
-    if (next.left > 0) {
-      const int n = next.pair();
-      const uint32_t dst = ring + slot * kStage;
+    if (next.run > 0) {
+      if ((id0 >= num_blocks || id1 >= num_blocks) && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
+      const uint32_t at_slot = slot * kStage;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int id = u == 0 ? id0 : id1;
-        const bool real = id >= 0 && id < p.num_blocks;
-        if (u < n && !real && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
-        const int64_t off = (real ? id : 0) * block_bytes + static_cast<int64_t>(next.h) * kChunk;
-        const uint8_t* k = p.key_cache + off + lane * 16;
-        const uint8_t* v = p.value_cache + off + lane * 16;
-        const uint32_t kd = dst + u * kUnit + lane * 16, vd = dst + u * kUnit + kChunk + v_dst;
+        if (u == 1 && next.run < 2) break;
+        const bool real = (u == 0 ? id0 : id1) < num_blocks;  // else zeros
+        const uint64_t off = static_cast<uint64_t>(real ? (u == 0 ? id0 : id1) : 0u) * block_bytes;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-          cp_async16(kd + i * 512, k + i * 512, real);
-          cp_async16(vd + i * 512, v + i * 512, real);
+          cp_async16(k_dst + at_slot + u * kUnit + i * 512, k_src + off + i * 512, real);
+          cp_async16(v_dst + at_slot + u * kUnit + i * 512, v_src + off + i * 512, real);
         }
-        // scales: NB chunks of 16 bytes each for K and V
-        if (lane < 2 * NB) {
-          const bool is_v = lane >= NB;
-          const int c = is_v ? lane - NB : lane;
-          cp_async16(dst + u * kUnit + (is_v ? kChunk : 0) + kScale + c * 16,
-                     (is_v ? p.value_cache : p.key_cache) + off + kScale + c * 16, real);
-        }
+        if (lane < 2 * NB) cp_async16(s_dst + at_slot + u * kUnit, s_src + off, real);
       }
-      next.advance(n, prefix, p.hkv);
-      load_ids();
+      row += 2;
+      next.run -= 2;
+      if (next.run <= 0 && next.rest > 0) {
+        next.next_run(prefix);
+        enter_run();
+      }
+      if (next.run > 0) load_ids();
     }
     cp_async_commit();
   };
-  load_ids();
   const int stages = p.stages;
-  for (int s = 0; s < stages - 1; ++s) fetch(s);
-
+  // where this lane finds the V codes of tokens 2 tid and 2 tid + 1 (2 tid + 8
+  // and + 9: four pairs on)
+  int v_at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v_at[i] = D == 128 ? tid * 128 + (((4 * i + (gid >> 1)) ^ (2 * tid)) << 4) + (gid & 1) * 8
+                       : tid * 64 + ((i ^ (tid >> 1)) << 5) + gid * 4;
   const int G = p.group;
+  // one pass, or with more KV heads than warps one for each head of this warp
+  for (; h < p.hkv; h += kWarps) {
+  Cursor at = next = start;
+  enter_run();
+  load_ids();
+  for (int s = 0; s < stages - 1; ++s) fetch(s);
   int slot = 0;
-  while (at.left > 0) {
-    // ======================= one run of this worker =======================
-    const int r = at.r, h = at.h;
-    const int64_t run0 = static_cast<int64_t>(prefix[r]) * p.hkv + static_cast<int64_t>(h) * at.nb;
-    const int64_t run1 = run0 + at.nb;
+  while (true) {
+    // ======================= the range's part of one request =======================
+    const int r = at.r;
+    const int64_t run0 = prefix[r], run1 = prefix[r + 1];
     const int64_t tok = __ldg(p.qsl + r);
     const int seq = __ldg(p.seq_lens + r);
 
@@ -326,15 +374,16 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
     for (int w = 0; w < NW; ++w) base[w] = top[w] = 0u;
 
-    bool more = true;
-    while (more) {
-      const int n = at.pair();
-      const int j = at.j;
+    int left = at.run;             // units of the run to go
+    int valid = seq - at.j * kMxBlock;  // tokens the request has from the stage's first on
+    for (; left > 0; left -= 2, valid -= 32) {
       // at the fewest stages one fetch may still be in flight, else two
       if (stages == 2) cp_async_wait<0>(); else cp_async_wait<1>();
       __syncwarp();
       fetch(slot == 0 ? stages - 1 : slot - 1);
       const uint8_t* st = smem + (static_cast<size_t>(warp) * stages + slot) * kStage;
+      // tokens of this stage: below 32 in a run's last one only
+      const int tokens = min(valid, left * kMxBlock);
 
       // ---- S^T = K Q^T of both units, in log2 units ----
       float s[2][NT][4];
@@ -357,6 +406,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           slo = *reinterpret_cast<const uint16_t*>(k + kScale + gid * 2);
           shi = *reinterpret_cast<const uint16_t*>(k + kScale + gid * 2 + 16);
         }
+        uint32_t ks[2][NW];  // K scales as bfloat16 pairs, NaN for 255
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          ks[0][w] = e8m0x2_to_bf16x2(slo >> (16 * w));
+          ks[1][w] = e8m0x2_to_bf16x2(shi >> (16 * w));
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -366,15 +421,14 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           uint32_t x[4], y[4];
           e2m1x8_to_f16(lo[b], x);
           e2m1x8_to_f16(hi[b], y);
-          // 2^(e - 127): the scale byte in a float's exponent field (NaN's 255
-          // gives infinity, and times its zero codes NaN; 0 reads as zero, below
-          // the smallest scale that the cache write makes)
-          const float fl = __uint_as_float((b < 3 ? slo << (23 - 8 * b) : slo >> 1) & 0x7f800000u);
-          const float fh = __uint_as_float((b < 3 ? shi << (23 - 8 * b) : shi >> 1) & 0x7f800000u);
+          const float fl = (b & 1) ? __uint_as_float(ks[0][b >> 1] & 0xffff0000u)
+                                   : __uint_as_float(ks[0][b >> 1] << 16);
+          const float fh = (b & 1) ? __uint_as_float(ks[1][b >> 1] & 0xffff0000u)
+                                   : __uint_as_float(ks[1][b >> 1] << 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(d, x[0], y[0], x[1], y[1], qb[nt][2 * b][0], qb[nt][2 * b][1]);
+            float d[4];
+            mma_f16_first(d, x[0], y[0], x[1], y[1], qb[nt][2 * b][0], qb[nt][2 * b][1]);
             mma_f16(d, x[2], y[2], x[3], y[3], qb[nt][2 * b + 1][0], qb[nt][2 * b + 1][1]);
             s[u][nt][0] = fmaf(d[0], fl, s[u][nt][0]);
             s[u][nt][1] = fmaf(d[1], fl, s[u][nt][1]);
@@ -387,16 +441,50 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[u][nt][c] *= qs[nt][c & 1];
       }
-      // tokens of this stage that the request has (a full stage: 32)
-      const int valid = min(seq - j * kMxBlock, n * kMxBlock);
-      if (valid < 32) {
+      if (tokens < 32) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (u * 16 + gid + (c >> 1) * 8 >= valid) s[u][nt][c] = -INFINITY;
+              if (u * 16 + gid + (c >> 1) * 8 >= tokens) s[u][nt][c] = -INFINITY;
+      }
+
+      // ---- V scales of token pairs tid and tid + 4 of each unit ----
+      uint32_t sw[2][2][NW];
+      uint32_t far[2] = {0u, 0u};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* v = st + u * kUnit + kChunk + kScale;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v + i * 32 + tid * 8);
+            sw[u][i][0] = x.x;
+            sw[u][i][1] = x.y;
+          } else {
+            sw[u][i][0] = *reinterpret_cast<const uint32_t*>(v + i * 16 + tid * 4);
+          }
+        }
+        if (tokens < 32) {
+          // bytes of tokens past the end may be anything: any scale inside the window
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = u * 16 + 2 * tid + 8 * i;
+            const uint32_t keep = (t < tokens ? 0x0000ffffu : 0u) | (t + 1 < tokens ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) sw[u][i][w] = (sw[u][i][w] & keep) | (base[w] & ~keep);
+          }
+        }
+        // All scales within [base, base + 15]?  If so no byte borrows, and every
+        // difference fits its low four bits.  A byte below base by 1 .. 239
+        // leaves one of the tested bits set (base is at most 239, and NaN's 255
+        // is above every base by 16 or more).
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) far[u] |= sw[u][i][w] - base[w];
       }
 
       // ---- online softmax per head column ----
@@ -410,7 +498,43 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                              fmaxf(s[1][nt][cc], s[1][nt][2 + cc]));
           grow |= mx[nt][cc] > m[nt][cc] + kMaxSlack;
         }
-      if (__any_sync(0xffffffffu, grow)) {
+      bool slow[2] = {false, false};
+      // one vote for everything that is rare
+      if (__any_sync(0xffffffffu, grow || ((far[0] | far[1]) & 0xf0f0f0f0u) != 0u)) {
+        if (left == at.run) {
+          // the first stage: nothing is summed up yet, so the base is free to go
+          // where this stage's largest scales want it
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            uint32_t x = __vmaxu4(__vmaxu4(sw[0][0][w], sw[0][1][w]), __vmaxu4(sw[1][0][w], sw[1][1][w]));
+            x = __vmaxu4(x, __byte_perm(x, 0u, 0x1032));  // both tokens of a pair
+            x = __vmaxu4(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = __vmaxu4(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            const uint32_t to = __vminu4(__vsubus4(x, kBelow * 0x01010101u), kTopBase * 0x01010101u);
+            if (tokens < 32) {  // bytes past the end follow the base
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int t = u * 16 + 2 * tid + 8 * i;
+                  const uint32_t keep = (t < tokens ? 0x0000ffffu : 0u) | (t + 1 < tokens ? 0xffff0000u : 0u);
+                  sw[u][i][w] = (sw[u][i][w] & keep) | (to & ~keep);
+                }
+            }
+            base[w] = top[w] = to;
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            far[u] = 0u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int w = 0; w < NW; ++w) far[u] |= sw[u][i][w] - base[w];
+          }
+        }
+        slow[0] = __any_sync(0xffffffffu, (far[0] & 0xf0f0f0f0u) != 0u);
+        // the first unit's slow path moves the base: the second goes with it
+        slow[1] = slow[0] || __any_sync(0xffffffffu, (far[1] & 0xf0f0f0f0u) != 0u);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -433,7 +557,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (u == 1 && valid <= 16) break;
+        if (u == 1 && tokens <= 16) break;
         // P^T fragments: tokens 2 tid, + 1 (and + 8) of head gid
         uint32_t pt[NT][2];
 #pragma unroll
@@ -443,57 +567,23 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           for (int c = 0; c < 4; ++c) e[c] = exp2_approx(s[u][nt][c] - m[nt][c & 1]);
           l[nt][0] += e[0] + e[2];
           l[nt][1] += e[1] + e[3];
-          pt[nt][0] = movmatrix_trans(pack_f16(e[0], e[1]));
-          pt[nt][1] = movmatrix_trans(pack_f16(e[2], e[3]));
+          pt[nt][0] = transpose_8x8(pack_f16(e[0], e[1]));
+          pt[nt][1] = transpose_8x8(pack_f16(e[2], e[3]));
         }
 
-        // ---- V codes and scales of tokens 2 tid, + 1, + 8, + 9 ----
+        // ---- V codes of tokens 2 tid, + 1, + 8, + 9 ----
         const uint8_t* v = st + u * kUnit + kChunk;
-        uint32_t vw[4][NW], sw[2][NW];
-        if constexpr (D == 128) {
-          // pair tid, halves: chunk (token parity 4 + gid / 2) ^ 2 tid, 8 bytes at gid % 2
+        uint32_t vw[4][NW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 x = *reinterpret_cast<const uint2*>(
-                v + (i >> 1) * 512 + tid * 128 + (((((i & 1) << 2) + (gid >> 1)) ^ (2 * tid)) << 4) +
-                (gid & 1) * 8);
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v + (i >> 1) * 512 + v_at[i & 1]);
             vw[i][0] = x.x;
             vw[i][1] = x.y;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 x = *reinterpret_cast<const uint2*>(v + kScale + i * 32 + tid * 8);
-            sw[i][0] = x.x;
-            sw[i][1] = x.y;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(
-                v + (i >> 1) * 256 + tid * 64 + (((i & 1) ^ (tid >> 1)) << 5) + gid * 4);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            sw[i][0] = *reinterpret_cast<const uint32_t*>(v + kScale + i * 16 + tid * 4);
-        }
-        if (valid - u * 16 < 16) {
-          // bytes of tokens past the end may be anything: any scale inside the window
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = u * 16 + 2 * tid + 8 * i;
-            const uint32_t keep = (t < valid ? 0x0000ffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) sw[i][w] = (sw[i][w] & keep) | (base[w] & ~keep);
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(v + (i >> 1) * 256 + v_at[i & 1]);
           }
         }
-        // All scales within [base, base + 7]?  If so no byte borrows, and every
-        // difference fits its low three bits.  A byte below base by 1 .. 247
-        // leaves one of the tested bits set (base is at most 247, and NaN's 255
-        // is above every base by 8 or more).
-        uint32_t far = 0u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int w = 0; w < NW; ++w) far |= sw[i][w] - base[w];
         // codes of a token pair side by side: byte k holds position 2k (even) or
         // 2k + 1 (odd) of both tokens
         uint32_t ev[2][NW], od[2][NW];
@@ -506,12 +596,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
             od[i][w] = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
           }
 
-        if (!__any_sync(0xffffffffu, (far & 0xf8f8f8f8u) != 0u)) {
+        if (!slow[u]) {
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
-            // 2^(e - base) as f16: exponent field e - base + 15 in each half
-            const uint32_t c = 0x3c3c3c3cu - 4u * base[w];
-            const uint32_t x0 = sw[0][w] * 4u + c, x1 = sw[1][w] * 4u + c;
+            // 2^(e - base + kLow) as f16: the exponent field in each half's high byte
+            const uint32_t c = 4u * (15 + kLow) * 0x01010101u - 4u * base[w];
+            const uint32_t x0 = sw[u][0][w] * 4u + c, x1 = sw[u][1][w] * 4u + c;
             uint32_t e0[4], e1[4], o0[4], o1[4];
             e2m1x8_to_f16(ev[0][w], e0);
             e2m1x8_to_f16(od[0][w], o0);
@@ -552,8 +642,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
               bool nan = false;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                e[i] = (sw[i >> 1][w] >> (16 * (i & 1) + 8 * b)) & 0xff;
-                const bool in = u * 16 + 2 * tid + (i & 1) + 8 * (i >> 1) < valid;
+                e[i] = (sw[u][i >> 1][w] >> (16 * (i & 1) + 8 * b)) & 0xff;
+                const bool in = u * 16 + 2 * tid + (i & 1) + 8 * (i >> 1) < tokens;
                 nan |= in && e[i] == 255;
                 if (!in || e[i] == 255 || !((live >> i) & 1u)) e[i] = -1;
                 hi = max(hi, e[i]);
@@ -561,10 +651,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
               hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
               hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
               nan = __any_sync(0xffffffffu, nan);
-              // the base follows the largest scale, five below it; down again
-              // only while what is summed up stays far from overflow
+              // the base follows the largest scale; down again only while what is
+              // summed up stays far from overflow
               int bs = (base[w] >> (8 * b)) & 0xff, tp = (top[w] >> (8 * b)) & 0xff;
-              const int to = min(max(hi - 5, 0), 247);
+              const int to = min(max(hi - kBelow, 0), kTopBase);
               if (hi >= 0 && (to > bs || (hi < bs && tp - to <= 60))) {
                 const float f = bs > to ? pow2(bs - to) : pow2(max(bs - to, -127));
 #pragma unroll
@@ -579,14 +669,15 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                 top[w] = (top[w] & hold) | (static_cast<uint32_t>(tp) * 0x00010001u) << (8 * b);
                 bs = to;
               }
-              // windows of eight binades, from the base down
-              for (int below = 0; below < 256; below += 8) {
+              // windows of 16 binades, from the base down
+              for (int below = 0; below < 256; below += 16) {
                 uint32_t f[2] = {0u, 0u};
                 bool rest = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int d = e[i] < 0 ? -1000 : e[i] - bs + below;
-                  if (d >= 0 && d < 8) f[i >> 1] |= static_cast<uint32_t>(d + 15) << (10 + 16 * (i & 1));
+                  if (d >= 0 && d < 16)
+                    f[i >> 1] |= static_cast<uint32_t>(d + kLow + 15) << (10 + 16 * (i & 1));
                   rest |= e[i] >= 0 && d < 0;
                 }
                 const float back = pow2(-below);
@@ -604,8 +695,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                   const uint32_t b0 = mul_f16x2(pt[nt][0], f[0]), b1 = mul_f16x2(pt[nt][1], f[1]);
 #pragma unroll
                   for (int k = 0; k < 2; ++k) {
-                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(t, a[k][0], a[k][1], a[k][2], a[k][3], b0, b1);
+                    float t[4];
+                    mma_f16_first(t, a[k][0], a[k][1], a[k][2], a[k][3], b0, b1);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                       o[4 * w + 2 * b + k][nt][c] = fmaf(t[c], back, o[4 * w + 2 * b + k][nt][c]);
@@ -627,11 +718,9 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         }
       }
       if (++slot == stages) slot = 0;
-      at.advance(n, prefix, p.hkv);
-      more = at.left > 0 && at.r == r && at.h == h;
     }
 
-    // ======================= end of this worker's part of the run =======================
+    // ======================= end of the range's part of the request =======================
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -642,13 +731,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         l[nt][cc] = x;
       }
-    const int64_t wf = worker_of(run0);
-    const int splits = static_cast<int>(worker_of(run1 - 1) - wf) + 1;
-    // slot of split k: a worker's own, except that a run which starts inside
-    // the first worker's range has that worker's second slot
-    const bool inside = run0 > wf * N / W;
-    auto slot_of = [&](int k) -> int64_t { return 2 * (wf + k) + (k == 0 && inside ? 1 : 0); };
-    const int mine = static_cast<int>(me - wf);
+    const bool whole = run0 >= u0 && run1 <= u1;
+    const int64_t mine = slot_of(me, run0 > u0) * p.hkv + h;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -656,111 +740,94 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         const int g = nt * 8 + 2 * tid + cc;
         if (g >= G) continue;
         // o[2 b + s]: dims 32 b + 4 gid + 2 s (elements 0, 1) and + 1 (2, 3)
-        const float inv = splits == 1 ? 1.f / l[nt][cc] : 1.f;
+        const float inv = 1.f / l[nt][cc];
         __nv_bfloat16* dst = p.out + tok * p.out_stride + static_cast<int64_t>(h * G + g) * D + 4 * gid;
-        float* po = p.part_o + (slot_of(mine) * G + g) * D + 4 * gid;
+        float* po = p.part_o + (mine * G + g) * D + 4 * gid;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint32_t e = (base[b >> 1] >> (8 * (b & 1))) & 0xffu;
-          const float f = mx_scale(e);
+          // what the weights' scales left out: 2^(base - kLow - 127)
+          const float f = mx_scale((base[b >> 1] >> (8 * (b & 1))) & 0xffu) * pow2(-kLow);
           float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = o[2 * b + (i >> 1)][nt][2 * (i & 1) + cc] * f;
-          if (splits == 1)
+          if (whole)
             *reinterpret_cast<uint2*>(dst + 32 * b) =
                 make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
           else
             *reinterpret_cast<float4*>(po + 32 * b) = make_float4(x[0], x[1], x[2], x[3]);
         }
-        if (splits > 1 && gid == 0)
-          p.part_ml[slot_of(mine) * G + g] = make_float2(m[nt][cc], l[nt][cc]);
+        if (!whole && gid == 0) p.part_ml[mine * G + g] = make_float2(m[nt][cc], l[nt][cc]);
       }
-    if (splits == 1) continue;
+    if (at.rest == 0) break;
+    at.next_run(prefix);
+  }
+  // every copy of this pass has been waited for by its stage; none is in flight
+  }
+}
 
-    // ---- join: groups of `fan` splits, then the groups ----
-    int fan = kFan;
-    while (fan * fan < splits) fan += 8;
-    int first = mine / fan * fan, step = 1, count = min(fan, splits - first);
-    int32_t* ctr = p.count1 + slot_of(first);
-    const int groups = (splits + fan - 1) / fan;
-    bool top_level = groups == 1;
-    while (true) {
-      __threadfence();
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) last = atomicAdd(ctr, 1) == count - 1;
-      if (!__shfl_sync(0xffffffffu, last, 0)) break;
-      __threadfence();
-      if (lane == 0) *ctr = 0;  // complete: ready for the next call
-      // every lane takes whole float4s of the G x D partials, four at a time
-      const int vecs = G * (D / 4);
-      for (int v0 = lane; v0 < vecs; v0 += 128) {
-        float4 acc[4];
-        float big[4], den[4];
+// Joins the partials of every request that crosses ranges: a thread sums four
+// dimensions of one (request, query head) over its ranges, kBatch loads in
+// flight.
+template <int D>
+__global__ void __launch_bounds__(256) join_mxfp4_kernel(const Params p) {
+  grid_dependency_wait();  // the decode's partials
+  if (threadIdx.x == 0) grid_launch_dependents();
+  constexpr int kBatch = 8;
+  const int G = p.group, H = p.hkv * G;
+  const int64_t N = __ldcg(p.plan + p.num_reqs), Q = __ldcg(p.plan + p.num_reqs + 1);
+  const int64_t total = static_cast<int64_t>(p.num_reqs) * H * (D / 4);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int r = static_cast<int>(i / (H * (D / 4)));
+    const int rem = static_cast<int>(i - static_cast<int64_t>(r) * (H * (D / 4)));
+    const int head = rem / (D / 4), d4 = rem % (D / 4);
+    const int64_t run0 = __ldcg(p.plan + r), run1 = __ldcg(p.plan + r + 1);
+    if (run0 == run1) continue;  // not a decode row
+    // ranges of a block x: the largest q with floor(qN/Q) <= x
+    const int64_t qf = ((run0 + 1) * Q - 1) / N, ql = (run1 * Q - 1) / N;
+    if (qf == ql) continue;  // written by the decode itself
+    const int h = head / G, g = head - h * G;
+    const bool inside = run0 > qf * N / Q;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float big = -INFINITY, den = 0.f;
+    for (int64_t q = qf; q <= ql; q += kBatch) {
+      float2 ml[kBatch];
+      float4 x[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          big[i] = -INFINITY;
-          den[i] = 0.f;
-        }
-        for (int k = 0; k < count; k += 2) {
-          float4 x[2][4];
-          float2 ml[2][4];
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int v = v0 + 32 * i;
-              ml[kk][i] = make_float2(-INFINITY, 0.f);
-              x[kk][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (v < vecs && k + kk < count) {
-                const int64_t row = slot_of(first + (k + kk) * step) * G + v / (D / 4);
-                ml[kk][i] = __ldcg(p.part_ml + row);
-                x[kk][i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D) + v % (D / 4));
-              }
-            }
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float mn = fmaxf(big[i], ml[kk][i].x);
-              const float wa = big[i] == mn ? 1.f : exp2_approx(big[i] - mn);
-              const float wb = ml[kk][i].x == mn ? 1.f : exp2_approx(ml[kk][i].x - mn);
-              big[i] = mn;
-              den[i] = den[i] * wa + ml[kk][i].y * wb;
-              acc[i].x = acc[i].x * wa + x[kk][i].x * wb;
-              acc[i].y = acc[i].y * wa + x[kk][i].y * wb;
-              acc[i].z = acc[i].z * wa + x[kk][i].z * wb;
-              acc[i].w = acc[i].w * wa + x[kk][i].w * wb;
-            }
-        }
-        __syncwarp();  // the first split's slot, read above by every lane, takes the group's sum
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int v = v0 + 32 * i;
-          if (v >= vecs) continue;
-          const int g = v / (D / 4), d4 = v % (D / 4);
-          if (top_level) {
-            const float inv = 1.f / den[i];
-            *reinterpret_cast<uint2*>(p.out + tok * p.out_stride +
-                                      static_cast<int64_t>(h * G + g) * D + 4 * d4) =
-                make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
-                           pack_bf16(acc[i].z * inv, acc[i].w * inv));
-          } else {
-            const int64_t row = slot_of(first) * G + g;
-            reinterpret_cast<float4*>(p.part_o + row * D)[d4] = acc[i];
-            if (d4 == 0) p.part_ml[row] = make_float2(big[i], den[i]);
-          }
+      for (int k = 0; k < kBatch; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q + k <= ql) {
+          const int64_t at = (slot_of(q + k, q + k == qf && inside) * p.hkv + h) * G + g;
+          ml[k] = __ldcg(p.part_ml + at);
+          x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + d4);
         }
       }
-      if (top_level) break;
-      // this warp's group is done: the groups' own count
-      top_level = true;
-      first = 0;
-      step = fan;
-      count = groups;
-      ctr = p.count2 + slot_of(0);
+      float mx = big;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, ml[k].x);
+      const float keep = big == mx ? 1.f : exp2_approx(big - mx);
+      big = mx;
+      den *= keep;
+      acc.x *= keep;
+      acc.y *= keep;
+      acc.z *= keep;
+      acc.w *= keep;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (q + k > ql) break;
+        const float w = ml[k].x == mx ? 1.f : exp2_approx(ml[k].x - mx);
+        den = fmaf(ml[k].y, w, den);
+        acc.x = fmaf(x[k].x, w, acc.x);
+        acc.y = fmaf(x[k].y, w, acc.y);
+        acc.z = fmaf(x[k].z, w, acc.z);
+        acc.w = fmaf(x[k].w, w, acc.w);
+      }
     }
+    const float inv = 1.f / den;
+    const int64_t tok = __ldg(p.qsl + r);
+    *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + static_cast<int64_t>(head) * D + 4 * d4) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
 }
 
@@ -776,13 +843,21 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   const size_t smem = p.stages * kRing + plan;
   cudaError_t e = raise_smem_limit_once<decode_mxfp4_kernel<D, NT>>(kLimit);
   if (e != cudaSuccess) return e;
-  return launch_programmatic(decode_mxfp4_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
-                             dim3(kWarps * 32), smem, stream, p);
+  e = launch_programmatic(decode_mxfp4_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
+                          dim3(kWarps * 32), smem, stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t threads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group * (D / 4);
+  int64_t grid = (threads + 255) / 256;
+  if (grid > 8 * static_cast<int64_t>(sms)) grid = 8 * static_cast<int64_t>(sms);
+  return launch_programmatic(join_mxfp4_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
+                             stream, p);
 }
 
 }  // namespace
 
-int64_t decode_mxfp4_workers(int sms) { return static_cast<int64_t>(sms) * warps_per_cta<1>(); }
+int64_t decode_mxfp4_slots(int sms, int num_kv_heads) {
+  return 2 * static_cast<int64_t>(sms) * ranges_per_cta(warps_per_cta<1>(), num_kv_heads) * num_kv_heads;
+}
 
 cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, int sms,
                                 cudaStream_t stream) {
@@ -806,8 +881,7 @@ cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, in
   p.group = a.num_heads / a.num_kv_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
-  p.count1 = ws.count1;
-  p.count2 = ws.count2;
+  p.plan = ws.plan;
   p.part_ml = reinterpret_cast<float2*>(ws.part_ml);
   p.part_o = ws.part_o;
   p.stages = 0;

@@ -97,7 +97,8 @@ class Step:
             a weight is off by 2 (D + 32) u S (log2 e folded in), numerator and
             denominator both;
           weight: f16 rounds at 2^-11 (and an exponential at 2^-21) of A, or by
-            2^-25 of |v_j| where p_j is below the normal f16 range;
+            2^-22 of |v_j| where p_j is below the normal f16 range (its least
+            step is 2^-24; a weight may have been scaled by 2^-3 before);
           sums: 2 n u of A for n keys, at worst;
           the result: half a bfloat16 step, 2^-8 |out|.
         """
@@ -128,7 +129,7 @@ class Step:
                 tol[a:b, h] = (2.0 ** -8 * ref[a:b, h].abs()
                                + mean[:, h] * (2.0 ** -11 + 2.0 ** -20 + 4 * (self.d + 32) * u * s
                                                + 2 * n * u)
-                               + 2.0 ** -25 * total)
+                               + 2.0 ** -22 * total)
         return ref, tol
 
 
