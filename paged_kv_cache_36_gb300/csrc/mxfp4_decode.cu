@@ -155,19 +155,24 @@ __device__ __forceinline__ int64_t slot_of(int64_t q, bool starts_inside) {
   return 2 * q + (starts_inside ? 1 : 0);
 }
 
-// A position in a range: block j of nb of request r; `run` blocks of it are in
-// the range, then `rest` more of later requests.
+// A position in a range: `run` blocks of request r to go, then `rest` more of
+// later requests.
 struct Cursor {
-  int r, j, nb;
-  int run, rest;
+  int r, run, rest;
   __device__ __forceinline__ void next_run(const int32_t* prefix) {
     do ++r; while (prefix[r + 1] == prefix[r]);
-    nb = prefix[r + 1] - prefix[r];
-    j = 0;
+    const int nb = prefix[r + 1] - prefix[r];
     run = rest < nb ? rest : nb;
     rest -= run;
   }
 };
+
+// base + a b, 64-bit.
+__device__ __forceinline__ const uint8_t* at_offset(const uint8_t* base, uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(base));
+  return reinterpret_cast<const uint8_t*>(r);
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
@@ -210,42 +215,29 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   __syncthreads();
   block_inclusive_scan(prefix + 1, R, scan_tmp);
   __syncthreads();
-  const int64_t N = prefix[R];
+  const int N = prefix[R];
   const int per_cta = ranges_per_cta(kWarps, p.hkv);
-  const int64_t most = static_cast<int64_t>(gridDim.x) * per_cta;
-  const int64_t want = (N + kMinBlocks - 1) / kMinBlocks;
-  const int64_t Q = want < most ? want : most;
+  const int Q = min((N + kMinBlocks - 1) / kMinBlocks, static_cast<int>(gridDim.x) * per_cta);
   if (blockIdx.x == 0) {
     for (int r = threadIdx.x; r <= R; r += blockDim.x) p.plan[r] = prefix[r];
-    if (threadIdx.x == 0) p.plan[R + 1] = static_cast<int32_t>(Q);
+    if (threadIdx.x == 0) p.plan[R + 1] = Q;
   }
   // few ranges: one per SM first
-  const int64_t me = static_cast<int64_t>(warp / p.hkv) * gridDim.x + blockIdx.x;
-  if (warp / p.hkv >= per_cta || me >= Q) return;
-  const int64_t u0 = me * N / Q, u1 = (me + 1) * N / Q;
+  const int sub = warp / p.hkv;
+  const int me = sub * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  if (sub >= per_cta || me >= Q) return;
+  const int u0 = static_cast<int>(static_cast<int64_t>(me) * N / Q);
+  const int u1 = static_cast<int>(static_cast<int64_t>(me + 1) * N / Q);
 
-  Cursor start;
-  {
-    int lo = 0, hi = R;  // prefix[lo] <= u0 < prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= u0) lo = mid; else hi = mid;
-    }
-    start.r = lo;
-    start.nb = prefix[lo + 1] - prefix[lo];
-    start.j = static_cast<int>(u0) - prefix[lo];
-    start.rest = static_cast<int>(u1 - u0);
-    start.run = min(start.rest, start.nb - start.j);
-    start.rest -= start.run;
-  }
-
-  // ---- the ring: fetch cursor, ids of its next stage already loaded ----
+  // ---- the ring ----
   // A lane copies the same 16-byte pieces of every unit: NW of the K codes, NW
   // of the V codes, and (lanes below 2 NB) one of the scales.  V codes of two
   // tokens (128 or 64 bytes) are XOR-swizzled by 16-byte pieces, so that the
   // four token pairs that a quad reads at once hit different banks.
   const uint32_t block_bytes = static_cast<uint32_t>(p.hkv) * kChunk;
-  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * p.stages * kStage;
+  const int stages = p.stages;
+  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * stages * kStage;
+  const uint32_t ring_end = stages * kStage;
   const bool scale_v = lane >= NB;
   const uint32_t k_dst = ring + lane * 16;
   const uint32_t v_dst =
@@ -253,50 +245,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       (D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (2 * ((lane >> 3) & 3))) << 4)
                 : (lane ^ (((lane >> 3) & 1) << 1)) << 4);
   const uint32_t s_dst = ring + kScale + (scale_v ? kChunk + (lane - NB) * 16 : lane * 16);
-  int h = warp < p.hkv ? warp : warp % p.hkv;
-  Cursor next = start;
-  const int32_t* row;               // the next stage's entries of the block table
-  const uint8_t *k_src, *v_src, *s_src;
-  auto enter_run = [&]() {
-    row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride + next.j;
-    const int64_t head = static_cast<int64_t>(h) * kChunk;
-    k_src = p.key_cache + head + lane * 16;
-    v_src = p.value_cache + head + lane * 16;
-    s_src = (scale_v ? p.value_cache + (lane - NB) * 16 : p.key_cache + lane * 16) + head + kScale;
-  };
-  uint32_t id0, id1;
-  auto load_ids = [&]() {
-    id0 = static_cast<uint32_t>(__ldg(row));
-    id1 = next.run > 1 ? static_cast<uint32_t>(__ldg(row + 1)) : 0u;
-  };
   const uint32_t num_blocks = static_cast<uint32_t>(p.num_blocks);
-  auto fetch = [&](int slot) {
-    if (next.run > 0) {
-      if ((id0 >= num_blocks || id1 >= num_blocks) && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
-      const uint32_t at_slot = slot * kStage;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u == 1 && next.run < 2) break;
-        const bool real = (u == 0 ? id0 : id1) < num_blocks;  // else zeros
-        const uint64_t off = static_cast<uint64_t>(real ? (u == 0 ? id0 : id1) : 0u) * block_bytes;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          cp_async16(k_dst + at_slot + u * kUnit + i * 512, k_src + off + i * 512, real);
-          cp_async16(v_dst + at_slot + u * kUnit + i * 512, v_src + off + i * 512, real);
-        }
-        if (lane < 2 * NB) cp_async16(s_dst + at_slot + u * kUnit, s_src + off, real);
-      }
-      row += 2;
-      next.run -= 2;
-      if (next.run <= 0 && next.rest > 0) {
-        next.next_run(prefix);
-        enter_run();
-      }
-      if (next.run > 0) load_ids();
-    }
-    cp_async_commit();
-  };
-  const int stages = p.stages;
   // where this lane finds the V codes of tokens 2 tid and 2 tid + 1 (2 tid + 8
   // and + 9: four pairs on)
   int v_at[2];
@@ -306,18 +255,69 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                        : tid * 64 + ((i ^ (tid >> 1)) << 5) + gid * 4;
   const int G = p.group;
   // one pass, or with more KV heads than warps one for each head of this warp
-  for (; h < p.hkv; h += kWarps) {
-  Cursor at = next = start;
-  enter_run();
+  for (int h = warp - sub * p.hkv; h < p.hkv; h += kWarps) {
+  const int64_t head_off = static_cast<int64_t>(h) * kChunk;
+  const uint8_t* k_src = p.key_cache + head_off + lane * 16;
+  const uint8_t* v_src = p.value_cache + head_off + lane * 16;
+  const uint8_t* s_src =
+      (scale_v ? p.value_cache + (lane - NB) * 16 : p.key_cache + lane * 16) + head_off + kScale;
+  // the fetch cursor, the table entries after it, and the next stage's two ids
+  Cursor next;
+  const int32_t* row;
+  uint32_t id0 = 0u, id1 = 0u;
+  {
+    int lo = 0, hi = R;  // prefix[lo] <= u0 < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= u0) lo = mid; else hi = mid;
+    }
+    next.r = lo;
+    next.run = min(u1, prefix[lo + 1]) - u0;
+    next.rest = u1 - u0 - next.run;
+    row = p.block_table + static_cast<int64_t>(lo) * p.bt_stride + (u0 - prefix[lo]);
+  }
+  Cursor at = next;
+  auto load_ids = [&]() {
+    id0 = static_cast<uint32_t>(__ldg(row));
+    id1 = next.run > 1 ? static_cast<uint32_t>(__ldg(row + 1)) : 0u;
+  };
+  auto fetch = [&](uint32_t stage) {
+    if (next.run > 0) {
+      if ((id0 >= num_blocks || id1 >= num_blocks) && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
+      const uint32_t kd = k_dst + stage, vd = v_dst + stage, sd = s_dst + stage;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u == 1 && next.run < 2) break;
+        uint32_t id = u == 0 ? id0 : id1;
+        const bool real = id < num_blocks;  // else zeros
+        id = real ? id : 0u;
+        const uint8_t* k = at_offset(k_src, id, block_bytes);
+        const uint8_t* v = at_offset(v_src, id, block_bytes);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          cp_async16(kd + u * kUnit + i * 512, k + i * 512, real);
+          cp_async16(vd + u * kUnit + i * 512, v + i * 512, real);
+        }
+        if (lane < 2 * NB) cp_async16(sd + u * kUnit, at_offset(s_src, id, block_bytes), real);
+      }
+      row += 2;
+      next.run -= 2;
+      if (next.run <= 0 && next.rest > 0) {
+        next.next_run(prefix);
+        row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride;
+      }
+      if (next.run > 0) load_ids();
+    }
+    cp_async_commit();
+  };
   load_ids();
-  for (int s = 0; s < stages - 1; ++s) fetch(s);
-  int slot = 0;
+  for (int s = 0; s < stages - 1; ++s) fetch(s * kStage);
+  uint32_t stage = 0;                          // the stage to compute on
+  uint32_t refill = (stages - 1) * kStage;     // the one it takes the next fetch
+  int first_j = u0 - prefix[at.r];
   while (true) {
     // ======================= the range's part of one request =======================
     const int r = at.r;
-    const int64_t run0 = prefix[r], run1 = prefix[r + 1];
-    const int64_t tok = __ldg(p.qsl + r);
-    const int seq = __ldg(p.seq_lens + r);
 
     // B fragments of Q^T in f16: k-step 2b + s of lane tid holds dims 32 b + 8
     // tid + 4 s .. + 3, the order of the K codes
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     for (int nt = 0; nt < NT; ++nt) {
       const int head = nt * 8 + gid;
       const __nv_bfloat16* qrow =
-          p.q + tok * p.q_stride + static_cast<int64_t>(h * G + (head < G ? head : 0)) * D;
+          p.q + static_cast<int64_t>(__ldg(p.qsl + r)) * p.q_stride + static_cast<int64_t>(h * G + (head < G ? head : 0)) * D;
       uint4 w[NB];
       uint32_t mx = 0u;
 #pragma unroll
@@ -342,8 +342,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       // largest element to [2^14, 2^15)
       const uint32_t ex = min(max(mx >> 7, 15u), 254u);
       const int up = 141 - static_cast<int>(ex);  // in [-113, 126]
-      const float f = pow2(up);
-      const float undo = p.scale_log2 * pow2(-up);
+      const float f = copysignf(pow2(up), p.scale_log2);
+      // the scale's sign is Q's; never zero, for the masked scores' infinities
+      float undo = fabsf(p.scale_log2) * pow2(-up);
+      undo = undo < 1.17549435e-38f ? 1.17549435e-38f : undo;
       qs[nt][0] = __shfl_sync(0xffffffffu, undo, 8 * tid);
       qs[nt][1] = __shfl_sync(0xffffffffu, undo, 8 * tid + 4);
 #pragma unroll
@@ -375,17 +377,19 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     for (int w = 0; w < NW; ++w) base[w] = top[w] = 0u;
 
     int left = at.run;             // units of the run to go
-    int valid = seq - at.j * kMxBlock;  // tokens the request has from the stage's first on
+    // tokens the request has from the stage's first on
+    int valid = __ldg(p.seq_lens + r) - first_j * kMxBlock;
     for (; left > 0; left -= 2, valid -= 32) {
       // at the fewest stages one fetch may still be in flight, else two
       if (stages == 2) cp_async_wait<0>(); else cp_async_wait<1>();
       __syncwarp();
-      fetch(slot == 0 ? stages - 1 : slot - 1);
-      const uint8_t* st = smem + (static_cast<size_t>(warp) * stages + slot) * kStage;
+      fetch(refill);
+      const uint8_t* st = smem + static_cast<uint32_t>(warp) * ring_end + stage;
+      refill = stage;
       // tokens of this stage: below 32 in a run's last one only
       const int tokens = min(valid, left * kMxBlock);
 
-      // ---- S^T = K Q^T of both units, in log2 units ----
+      // ---- S^T = K Q^T of both units; times qs they are in log2 units ----
       float s[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -436,10 +440,6 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
             s[u][nt][3] = fmaf(d[3], fh, s[u][nt][3]);
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[u][nt][c] *= qs[nt][c & 1];
       }
       if (tokens < 32) {
 #pragma unroll
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           mx[nt][cc] = fmaxf(fmaxf(s[0][nt][cc], s[0][nt][2 + cc]),
-                             fmaxf(s[1][nt][cc], s[1][nt][2 + cc]));
+                             fmaxf(s[1][nt][cc], s[1][nt][2 + cc])) * qs[nt][cc];
           grow |= mx[nt][cc] > m[nt][cc] + kMaxSlack;
         }
       bool slow[2] = {false, false};
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = exp2_approx(s[u][nt][c] - m[nt][c & 1]);
+          for (int c = 0; c < 4; ++c) e[c] = exp2_approx(fmaf(s[u][nt][c], qs[nt][c & 1], -m[nt][c & 1]));
           l[nt][0] += e[0] + e[2];
           l[nt][1] += e[1] + e[3];
           pt[nt][0] = transpose_8x8(pack_f16(e[0], e[1]));
@@ -609,8 +609,9 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
             e2m1x8_to_f16(od[1][w], o1);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {  // groups 2w and 2w + 1
-              const uint32_t f0 = (b == 0 ? x0 << 8 : x0) & 0xff00ff00u;
-              const uint32_t f1 = (b == 0 ? x1 << 8 : x1) & 0xff00ff00u;
+              // bytes b and b + 2 to the halves' high bytes
+              const uint32_t f0 = __byte_perm(x0, 0u, b == 0 ? 0x2404 : 0x3414);
+              const uint32_t f1 = __byte_perm(x1, 0u, b == 0 ? 0x2404 : 0x3414);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint32_t b0 = mul_f16x2(pt[nt][0], f0), b1 = mul_f16x2(pt[nt][1], f1);
@@ -717,7 +718,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           }
         }
       }
-      if (++slot == stages) slot = 0;
+      stage += kStage;
+      if (stage == ring_end) stage = 0;
     }
 
     // ======================= end of the range's part of the request =======================
@@ -731,8 +733,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         l[nt][cc] = x;
       }
-    const bool whole = run0 >= u0 && run1 <= u1;
-    const int64_t mine = slot_of(me, run0 > u0) * p.hkv + h;
+    const bool inside = prefix[r] > u0;
+    const bool whole = prefix[r] >= u0 && prefix[r + 1] <= u1;
+    const int64_t mine = slot_of(me, inside) * p.hkv + h;
+    const int64_t tok = __ldg(p.qsl + r);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -760,6 +764,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       }
     if (at.rest == 0) break;
     at.next_run(prefix);
+    first_j = 0;
   }
   // every copy of this pass has been waited for by its stage; none is in flight
   }

@@ -121,7 +121,7 @@ class Step:
             n = len(k)
             seen = torch.arange(n) <= self.past[r] + torch.arange(b - a)[:, None]
             for h in range(self.H):
-                s = q[:, h].abs() @ k[:, h // G].abs().T * self.scale
+                s = q[:, h].abs() @ k[:, h // G].abs().T * abs(self.scale)
                 s = s.masked_fill(~seen, 0).amax(1, keepdim=True)
                 total = torch.stack([v[:self.past[r] + i + 1, h // G].abs().sum(0)
                                      for i in (range(b - a) if r in self.nan else [b - a - 1])])

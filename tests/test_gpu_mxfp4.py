@@ -223,6 +223,17 @@ def test_queries_far_from_one(factor, reqs):
     check(got, *s.reference())
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30, 2.0])
+@pytest.mark.parametrize("reqs", [[(1, 90), (1, 40)], [(20, 70)]])
+def test_scales_of_the_scores(scale, reqs):
+    pkv = _pkv()
+    s = Step(12, reqs, 4, 2, 64)
+    s.scale = scale
+    s.upload()
+    got = pkv.paged_attention_varlen_mxfp4(*s.args(), max_query_len=max(s.q_len))
+    check(got, *s.reference())
+
+
 @pytest.mark.parametrize("is_key", [True, False])
 @pytest.mark.parametrize("reqs", [[(1, 90), (1, 40)], [(20, 70), (1, 40)]])
 def test_a_nan_group_stays_with_its_rows(reqs, is_key):
