@@ -97,10 +97,18 @@ struct Params {
   int32_t stages;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  // `real` false: 16 zero bytes, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
+// 16 bytes from src + kSrc to shared dst + kDst; with `bytes` 0 nothing is read
+// and zeros are written.
+template <int kDst, int kSrc>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst),
+               "n"(kSrc)
+               : "memory");
+}
+template <int kDst, int kSrc>
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16, %4;" ::"r"(dst), "l"(src),
+               "n"(kDst), "n"(kSrc), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   const int stages = p.stages;
   const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * stages * kStage;
   const uint32_t ring_end = stages * kStage;
-  const bool scale_v = lane >= NB;
+  const bool scale_v = lane >= NB, has_scale = lane < 2 * NB;
   const uint32_t k_dst = ring + lane * 16;
   const uint32_t v_dst =
       ring + kChunk +
@@ -283,22 +291,44 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   };
   auto fetch = [&](uint32_t stage) {
     if (next.run > 0) {
-      if ((id0 >= num_blocks || id1 >= num_blocks) && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
       const uint32_t kd = k_dst + stage, vd = v_dst + stage, sd = s_dst + stage;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u == 1 && next.run < 2) break;
-        uint32_t id = u == 0 ? id0 : id1;
-        const bool real = id < num_blocks;  // else zeros
-        id = real ? id : 0u;
-        const uint8_t* k = at_offset(k_src, id, block_bytes);
-        const uint8_t* v = at_offset(v_src, id, block_bytes);
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          cp_async16(kd + u * kUnit + i * 512, k + i * 512, real);
-          cp_async16(vd + u * kUnit + i * 512, v + i * 512, real);
+      const bool two = next.run > 1;
+      if (id0 < num_blocks && id1 < num_blocks) {
+        const uint8_t* k = at_offset(k_src, id0, block_bytes);
+        const uint8_t* v = at_offset(v_src, id0, block_bytes);
+        cp_async16<0, 0>(kd, k);
+        cp_async16<0, 0>(vd, v);
+        if constexpr (NW == 2) {
+          cp_async16<512, 512>(kd, k);
+          cp_async16<512, 512>(vd, v);
         }
-        if (lane < 2 * NB) cp_async16(sd + u * kUnit, at_offset(s_src, id, block_bytes), real);
+        if (has_scale) cp_async16<0, 0>(sd, at_offset(s_src, id0, block_bytes));
+        if (two) {
+          k = at_offset(k_src, id1, block_bytes);
+          v = at_offset(v_src, id1, block_bytes);
+          cp_async16<kUnit, 0>(kd, k);
+          cp_async16<kUnit, 0>(vd, v);
+          if constexpr (NW == 2) {
+            cp_async16<kUnit + 512, 512>(kd, k);
+            cp_async16<kUnit + 512, 512>(vd, v);
+          }
+          if (has_scale) cp_async16<kUnit, 0>(sd, at_offset(s_src, id1, block_bytes));
+        }
+      } else {
+        // a block id outside the pool: its block reads as zeros
+        if (lane == 0) atomicOr(p.err, PKV_ERR_BLOCK_ID);
+        for (int u = 0; u < (two ? 2 : 1); ++u) {
+          const uint32_t id = u == 0 ? id0 : id1;
+          const int n = id < num_blocks ? 16 : 0;
+          const uint64_t off = static_cast<uint64_t>(n ? id : 0u) * block_bytes;
+          cp_async16_or_zero<0, 0>(kd + u * kUnit, k_src + off, n);
+          cp_async16_or_zero<0, 0>(vd + u * kUnit, v_src + off, n);
+          if constexpr (NW == 2) {
+            cp_async16_or_zero<512, 512>(kd + u * kUnit, k_src + off, n);
+            cp_async16_or_zero<512, 512>(vd + u * kUnit, v_src + off, n);
+          }
+          if (has_scale) cp_async16_or_zero<0, 0>(sd + u * kUnit, s_src + off, n);
+        }
       }
       row += 2;
       next.run -= 2;
@@ -379,7 +409,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     int left = at.run;             // units of the run to go
     // tokens the request has from the stage's first on
     int valid = __ldg(p.seq_lens + r) - first_j * kMxBlock;
-    for (; left > 0; left -= 2, valid -= 32) {
+    for (; left > 0; left -= 2, valid -= 32,
+                     stage = stage + kStage == ring_end ? 0u : stage + kStage) {
       // at the fewest stages one fetch may still be in flight, else two
       if (stages == 2) cp_async_wait<0>(); else cp_async_wait<1>();
       __syncwarp();
@@ -498,7 +529,44 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                              fmaxf(s[1][nt][cc], s[1][nt][2 + cc])) * qs[nt][cc];
           grow |= mx[nt][cc] > m[nt][cc] + kMaxSlack;
         }
-      bool slow[2] = {false, false};
+      // P^T fragments of a unit: the weights of tokens 2 tid, + 1 (and + 8) for
+      // head gid, and their sums
+      auto weights = [&](int u, uint32_t (&pt)[NT][2]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = exp2_approx(fmaf(s[u][nt][c], qs[nt][c & 1], -m[nt][c & 1]));
+          l[nt][0] += e[0] + e[2];
+          l[nt][1] += e[1] + e[3];
+          pt[nt][0] = transpose_8x8(pack_f16(e[0], e[1]));
+          pt[nt][1] = transpose_8x8(pack_f16(e[2], e[3]));
+        }
+      };
+      // V codes of tokens 2 tid, + 1 (index 0), + 8, + 9 (index 1), a token pair
+      // side by side: byte k holds position 2k (ev) or 2k + 1 (od) of both
+      auto codes = [&](int u, uint32_t (&ev)[2][NW], uint32_t (&od)[2][NW]) {
+        const uint8_t* v = st + u * kUnit + kChunk;
+        uint32_t vw[4][NW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v + (i >> 1) * 512 + v_at[i & 1]);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(v + (i >> 1) * 256 + v_at[i & 1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const uint32_t x = vw[2 * i][w], y = vw[2 * i + 1][w];
+            ev[i][w] = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+            od[i][w] = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+          }
+      };
       // one vote for everything that is rare
       if (__any_sync(0xffffffffu, grow || ((far[0] | far[1]) & 0xf0f0f0f0u) != 0u)) {
         if (left == at.run) {
@@ -532,9 +600,6 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
               for (int w = 0; w < NW; ++w) far[u] |= sw[u][i][w] - base[w];
           }
         }
-        slow[0] = __any_sync(0xffffffffu, (far[0] & 0xf0f0f0f0u) != 0u);
-        // the first unit's slow path moves the base: the second goes with it
-        slow[1] = slow[0] || __any_sync(0xffffffffu, (far[1] & 0xf0f0f0f0u) != 0u);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -553,173 +618,143 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
               o[i][nt][2 + cc] *= alpha;
             }
           }
+        if (__any_sync(0xffffffffu, ((far[0] | far[1]) & 0xf0f0f0f0u) != 0u)) {
+          // ---- slow path: scales outside the window ----
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (u == 1 && tokens <= 16) break;
+            uint32_t pt[NT][2], ev[2][NW], od[2][NW];
+            weights(u, pt);
+            codes(u, ev, od);
+                      // Tokens with no weight left in f16 (for every head) count for nothing
+                      // here, as they do in the product.
+                      uint32_t live = 0u;  // bit i: token 2 tid + (i & 1) + 8 (i >> 1)
+#pragma unroll
+                      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                          if ((pt[nt][i >> 1] >> (16 * (i & 1))) & 0x7fffu) live |= 1u << i;
+#pragma unroll
+                      for (int x = 4; x < 32; x <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, x);
+#pragma unroll
+                      for (int w = 0; w < NW; ++w) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                          int e[4];       // scale bytes of this lane's tokens in group 2 w + b
+                          int hi = -1;
+                          bool nan = false;
+#pragma unroll
+                          for (int i = 0; i < 4; ++i) {
+                            e[i] = (sw[u][i >> 1][w] >> (16 * (i & 1) + 8 * b)) & 0xff;
+                            const bool in = u * 16 + 2 * tid + (i & 1) + 8 * (i >> 1) < tokens;
+                            nan |= in && e[i] == 255;
+                            if (!in || e[i] == 255 || !((live >> i) & 1u)) e[i] = -1;
+                            hi = max(hi, e[i]);
+                          }
+                          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+                          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+                          nan = __any_sync(0xffffffffu, nan);
+                          // the base follows the largest scale; down again only while what is
+                          // summed up stays far from overflow
+                          int bs = (base[w] >> (8 * b)) & 0xff, tp = (top[w] >> (8 * b)) & 0xff;
+                          const int to = min(max(hi - kBelow, 0), kTopBase);
+                          if (hi >= 0 && (to > bs || (hi < bs && tp - to <= 60))) {
+                            const float f = bs > to ? pow2(bs - to) : pow2(max(bs - to, -127));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[4 * w + 2 * b + k][nt][c] *= f;
+                            const uint32_t hold = ~(0x00ff00ffu << (8 * b));
+                            base[w] = (base[w] & hold) | (static_cast<uint32_t>(to) * 0x00010001u) << (8 * b);
+                            tp = max(tp, to);
+                            top[w] = (top[w] & hold) | (static_cast<uint32_t>(tp) * 0x00010001u) << (8 * b);
+                            bs = to;
+                          }
+                          // windows of 16 binades, from the base down
+                          for (int below = 0; below < 256; below += 16) {
+                            uint32_t f[2] = {0u, 0u};
+                            bool rest = false;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                              const int d = e[i] < 0 ? -1000 : e[i] - bs + below;
+                              if (d >= 0 && d < 16)
+                                f[i >> 1] |= static_cast<uint32_t>(d + kLow + 15) << (10 + 16 * (i & 1));
+                              rest |= e[i] >= 0 && d < 0;
+                            }
+                            const float back = pow2(-below);
+                            uint32_t a[2][4];  // fragments of the group's two m-tiles
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                              const int at8 = 8 * (2 * b + k);
+                              a[k][0] = e2m1x2_to_f16x2(ev[0][w] >> at8);
+                              a[k][1] = e2m1x2_to_f16x2(od[0][w] >> at8);
+                              a[k][2] = e2m1x2_to_f16x2(ev[1][w] >> at8);
+                              a[k][3] = e2m1x2_to_f16x2(od[1][w] >> at8);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                              const uint32_t b0 = mul_f16x2(pt[nt][0], f[0]), b1 = mul_f16x2(pt[nt][1], f[1]);
+#pragma unroll
+                              for (int k = 0; k < 2; ++k) {
+                                float t[4];
+                                mma_f16_first(t, a[k][0], a[k][1], a[k][2], a[k][3], b0, b1);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                  o[4 * w + 2 * b + k][nt][c] = fmaf(t[c], back, o[4 * w + 2 * b + k][nt][c]);
+                              }
+                            }
+                            if (!__any_sync(0xffffffffu, rest)) break;
+                          }
+                          if (nan) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                  o[4 * w + 2 * b + k][nt][c] = __uint_as_float(0x7fffffffu);
+                          }
+                        }
+                      }
+          }
+          continue;
+        }
       }
 
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (u == 1 && tokens <= 16) break;
-        // P^T fragments: tokens 2 tid, + 1 (and + 8) of head gid
-        uint32_t pt[NT][2];
+        uint32_t pt[NT][2], ev[2][NW], od[2][NW];
+        weights(u, pt);
+        codes(u, ev, od);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
+        for (int w = 0; w < NW; ++w) {
+          // 2^(e - base + kLow) as f16: the exponent field in each half's high byte
+          const uint32_t c = 4u * (15 + kLow) * 0x01010101u - 4u * base[w];
+          const uint32_t x0 = sw[u][0][w] * 4u + c, x1 = sw[u][1][w] * 4u + c;
+          uint32_t e0[4], e1[4], o0[4], o1[4];
+          e2m1x8_to_f16(ev[0][w], e0);
+          e2m1x8_to_f16(od[0][w], o0);
+          e2m1x8_to_f16(ev[1][w], e1);
+          e2m1x8_to_f16(od[1][w], o1);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = exp2_approx(fmaf(s[u][nt][c], qs[nt][c & 1], -m[nt][c & 1]));
-          l[nt][0] += e[0] + e[2];
-          l[nt][1] += e[1] + e[3];
-          pt[nt][0] = transpose_8x8(pack_f16(e[0], e[1]));
-          pt[nt][1] = transpose_8x8(pack_f16(e[2], e[3]));
-        }
-
-        // ---- V codes of tokens 2 tid, + 1, + 8, + 9 ----
-        const uint8_t* v = st + u * kUnit + kChunk;
-        uint32_t vw[4][NW];
+          for (int b = 0; b < 2; ++b) {  // groups 2w and 2w + 1
+            // bytes b and b + 2 to the halves' high bytes
+            const uint32_t f0 = __byte_perm(x0, 0u, b == 0 ? 0x2404 : 0x3414);
+            const uint32_t f1 = __byte_perm(x1, 0u, b == 0 ? 0x2404 : 0x3414);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(v + (i >> 1) * 512 + v_at[i & 1]);
-            vw[i][0] = x.x;
-            vw[i][1] = x.y;
-          } else {
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(v + (i >> 1) * 256 + v_at[i & 1]);
-          }
-        }
-        // codes of a token pair side by side: byte k holds position 2k (even) or
-        // 2k + 1 (odd) of both tokens
-        uint32_t ev[2][NW], od[2][NW];
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = mul_f16x2(pt[nt][0], f0), b1 = mul_f16x2(pt[nt][1], f1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const uint32_t x = vw[2 * i][w], y = vw[2 * i + 1][w];
-            ev[i][w] = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
-            od[i][w] = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
-          }
-
-        if (!slow[u]) {
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            // 2^(e - base + kLow) as f16: the exponent field in each half's high byte
-            const uint32_t c = 4u * (15 + kLow) * 0x01010101u - 4u * base[w];
-            const uint32_t x0 = sw[u][0][w] * 4u + c, x1 = sw[u][1][w] * 4u + c;
-            uint32_t e0[4], e1[4], o0[4], o1[4];
-            e2m1x8_to_f16(ev[0][w], e0);
-            e2m1x8_to_f16(od[0][w], o0);
-            e2m1x8_to_f16(ev[1][w], e1);
-            e2m1x8_to_f16(od[1][w], o1);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {  // groups 2w and 2w + 1
-              // bytes b and b + 2 to the halves' high bytes
-              const uint32_t f0 = __byte_perm(x0, 0u, b == 0 ? 0x2404 : 0x3414);
-              const uint32_t f1 = __byte_perm(x1, 0u, b == 0 ? 0x2404 : 0x3414);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = mul_f16x2(pt[nt][0], f0), b1 = mul_f16x2(pt[nt][1], f1);
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  mma_f16(o[4 * w + 2 * b + k][nt], e0[2 * b + k], o0[2 * b + k], e1[2 * b + k],
-                          o1[2 * b + k], b0, b1);
-              }
-            }
-          }
-        } else {
-          // ---- slow path: scales outside the window ----
-          // Tokens with no weight left in f16 (for every head) count for nothing
-          // here, as they do in the product.
-          uint32_t live = 0u;  // bit i: token 2 tid + (i & 1) + 8 (i >> 1)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((pt[nt][i >> 1] >> (16 * (i & 1))) & 0x7fffu) live |= 1u << i;
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, x);
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              int e[4];       // scale bytes of this lane's tokens in group 2 w + b
-              int hi = -1;
-              bool nan = false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                e[i] = (sw[u][i >> 1][w] >> (16 * (i & 1) + 8 * b)) & 0xff;
-                const bool in = u * 16 + 2 * tid + (i & 1) + 8 * (i >> 1) < tokens;
-                nan |= in && e[i] == 255;
-                if (!in || e[i] == 255 || !((live >> i) & 1u)) e[i] = -1;
-                hi = max(hi, e[i]);
-              }
-              hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-              hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
-              nan = __any_sync(0xffffffffu, nan);
-              // the base follows the largest scale; down again only while what is
-              // summed up stays far from overflow
-              int bs = (base[w] >> (8 * b)) & 0xff, tp = (top[w] >> (8 * b)) & 0xff;
-              const int to = min(max(hi - kBelow, 0), kTopBase);
-              if (hi >= 0 && (to > bs || (hi < bs && tp - to <= 60))) {
-                const float f = bs > to ? pow2(bs - to) : pow2(max(bs - to, -127));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) o[4 * w + 2 * b + k][nt][c] *= f;
-                const uint32_t hold = ~(0x00ff00ffu << (8 * b));
-                base[w] = (base[w] & hold) | (static_cast<uint32_t>(to) * 0x00010001u) << (8 * b);
-                tp = max(tp, to);
-                top[w] = (top[w] & hold) | (static_cast<uint32_t>(tp) * 0x00010001u) << (8 * b);
-                bs = to;
-              }
-              // windows of 16 binades, from the base down
-              for (int below = 0; below < 256; below += 16) {
-                uint32_t f[2] = {0u, 0u};
-                bool rest = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int d = e[i] < 0 ? -1000 : e[i] - bs + below;
-                  if (d >= 0 && d < 16)
-                    f[i >> 1] |= static_cast<uint32_t>(d + kLow + 15) << (10 + 16 * (i & 1));
-                  rest |= e[i] >= 0 && d < 0;
-                }
-                const float back = pow2(-below);
-                uint32_t a[2][4];  // fragments of the group's two m-tiles
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int at8 = 8 * (2 * b + k);
-                  a[k][0] = e2m1x2_to_f16x2(ev[0][w] >> at8);
-                  a[k][1] = e2m1x2_to_f16x2(od[0][w] >> at8);
-                  a[k][2] = e2m1x2_to_f16x2(ev[1][w] >> at8);
-                  a[k][3] = e2m1x2_to_f16x2(od[1][w] >> at8);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint32_t b0 = mul_f16x2(pt[nt][0], f[0]), b1 = mul_f16x2(pt[nt][1], f[1]);
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    float t[4];
-                    mma_f16_first(t, a[k][0], a[k][1], a[k][2], a[k][3], b0, b1);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                      o[4 * w + 2 * b + k][nt][c] = fmaf(t[c], back, o[4 * w + 2 * b + k][nt][c]);
-                  }
-                }
-                if (!__any_sync(0xffffffffu, rest)) break;
-              }
-              if (nan) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                      o[4 * w + 2 * b + k][nt][c] = __uint_as_float(0x7fffffffu);
-              }
+              for (int k = 0; k < 2; ++k)
+                mma_f16(o[4 * w + 2 * b + k][nt], e0[2 * b + k], o0[2 * b + k], e1[2 * b + k],
+                        o1[2 * b + k], b0, b1);
             }
           }
         }
       }
-      stage += kStage;
-      if (stage == ring_end) stage = 0;
     }
 
     // ======================= end of the range's part of the request =======================
