@@ -277,44 +277,54 @@ def prepare_reshape_and_cache_paged_attention(key, value, slot_mapping, q, key_c
 # ---------------------------------------------------------------------------
 # the 4-bit paged cache and the device-built step metadata
 # ---------------------------------------------------------------------------
-def _one_device(where: str, *tensors):
-    """The CUDA device that all the tensors (None allowed) are on."""
-    dev = tensors[0].device
+# The checks below run on every call, beside launches of a few microseconds: they
+# compare device indices and dtype objects and make no temporary objects.
+def _check_device(where: str, index: int, *tensors) -> None:
+    """The tensors (None allowed) are on CUDA device `index`."""
     for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
-            raise ValueError(f"{where}: all tensors must be on one CUDA device")
-    return dev
+        if t is not None and t.get_device() != index:
+            index = -1
+    if index < 0:
+        raise ValueError(f"{where}: all tensors must be on one CUDA device")
 
 
-def _expect(where: str, name: str, t, dtype, shape=None) -> None:
-    """t is a contiguous tensor of this dtype (and shape)."""
-    if t.dtype != dtype:
+def _expect(where: str, name: str, t, dtype, shape) -> None:
+    """t is a contiguous tensor of this dtype and shape."""
+    if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _device_call(where: str, fn, device, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current."""
+def _device_call(where: str, fn, index: int, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current, on its current stream
+    if none is given."""
     import torch
-    if stream is not None and getattr(stream, "device", device) != device:
-        raise ValueError(f"{where}: the stream is on another device than the tensors")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream_ptr(stream)), where)
+    if stream is None:
+        ptr = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_ptr(stream)), where)
+        device = getattr(stream, "device", None)
+        if device is not None and device.index != index:
+            raise ValueError(f"{where}: the stream is on another device than the tensors")
+        ptr = stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, ptr)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, ptr)
+    if code < 0:
+        raise PkvError(code, where)
 
 
-def _allocating_on(device, stream):
+def _allocating_on(index: int, stream):
     """Context in which a call's own buffers are made: on its stream, so that
     their memory is neither filled nor reused ahead of it."""
     import torch
     if stream is not None:
         return torch.cuda.stream(stream)
-    return torch.cuda.device(device)
+    return torch.cuda.device(index)
 
 
 def mxfp4_block_bytes(num_kv_heads: int, head_dim: int, block_size: int = 16) -> int:
@@ -336,7 +346,10 @@ def new_cache_mxfp4(num_blocks: int, num_kv_heads: int, head_dim: int, device="c
 
 def _mxfp4_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int) -> int:
     import torch
-    shape = (key_cache.shape[0], mxfp4_block_bytes(num_kv_heads, head_dim))
+    if head_dim != 64 and head_dim != 128:
+        raise ValueError(f"{where}: head_dim must be 64 or 128, not {head_dim}")
+    # 16 tokens of head_dim / 2 code bytes and head_dim / 32 scale bytes per KV head
+    shape = (key_cache.shape[0], num_kv_heads * head_dim * 17 // 2)
     _expect(where, "key_cache", key_cache, torch.uint8, shape)
     _expect(where, "value_cache", value_cache, torch.uint8, shape)
     return shape[0]
@@ -353,7 +366,8 @@ def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, slot_mapping, er
         raise ValueError(f"{where}: key and value must have one shape and dtype")
     nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
     _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
-    dev = _one_device(where, key, value, key_cache, value_cache, slot_mapping, error_word)
+    dev = key.get_device()
+    _check_device(where, dev, value, key_cache, value_cache, slot_mapping, error_word)
     _device_call(where, lib().pkv_reshape_and_cache_mxfp4, dev, stream, key.data_ptr(),
                  value.data_ptr(), _token_stride(key), _token_stride(value), key_cache.data_ptr(),
                  value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d,
@@ -372,7 +386,8 @@ def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out,
         raise ValueError(f"{where}: key_out and value_out must have one shape and dtype")
     nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
     _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
-    dev = _one_device(where, key_cache, value_cache, slot_mapping, key_out, value_out, error_word)
+    dev = key_out.get_device()
+    _check_device(where, dev, key_cache, value_cache, slot_mapping, value_out, error_word)
     _device_call(where, lib().pkv_gather_cache_mxfp4, dev, stream, key_cache.data_ptr(),
                  value_cache.data_ptr(), slot_mapping.data_ptr(), key_out.data_ptr(),
                  value_out.data_ptr(), _token_stride(key_out), _token_stride(value_out), T, nb, 16,
@@ -406,27 +421,29 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
     import torch
     where = "paged_attention_varlen_mxfp4"
     T, H, D = q.shape
-    nb, block_bytes = key_cache.shape
-    hkv = max(1, block_bytes // mxfp4_block_bytes(1, D))
-    _mxfp4_pools(where, key_cache, value_cache, hkv, D)
-    if q.dtype != torch.bfloat16:
+    hkv = max(1, key_cache.shape[1] * 2 // (17 * D))
+    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, D)
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"{where}: q must be bfloat16")
     R = seq_lens.shape[0]
-    if block_table.dtype != torch.int32 or block_table.shape[0] != R:
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
     _expect(where, "query_start_loc", query_start_loc, torch.int32, (R + 1,))
     _expect(where, "seq_lens", seq_lens, torch.int32, (R,))
     _expect(where, "num_computed_tokens", num_computed_tokens, torch.int32, (R,))
-    dev = _one_device(where, q, key_cache, value_cache, block_table, query_start_loc, seq_lens,
-                      num_computed_tokens, workspace, out)
+    dev = q.get_device()
+    _check_device(where, dev, key_cache, value_cache, block_table, query_start_loc, seq_lens,
+                  num_computed_tokens, workspace, out)
     if out is None or workspace is None:
         with _allocating_on(dev, stream):
             if out is None:
-                out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+                out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
             if workspace is None:
-                workspace = new_workspace_mxfp4(H, hkv, D, dev)
-    if out.shape != q.shape or out.dtype != q.dtype:
+                workspace = new_workspace_mxfp4(H, hkv, D, q.device)
+    if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError(f"{where}: out must have q's shape and dtype")
+    if not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous")
     _device_call(where, lib().pkv_paged_attention_varlen_mxfp4, dev, stream, q.data_ptr(),
                  _token_stride(q), key_cache.data_ptr(), value_cache.data_ptr(),
                  block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
@@ -455,16 +472,22 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
     i32, i64 = torch.int32, torch.int64
     _expect(where, "query_lens", query_lens, i32, (R,))
     _expect(where, "num_computed_tokens", num_computed_tokens, i32, (R,))
-    if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != R:
+    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
-    _expect(where, "free_ring", free_ring, i32, (free_ring.numel(),))
+    if free_ring.dtype is not i32 or free_ring.dim() != 1 or not free_ring.is_contiguous():
+        raise ValueError(f"{where}: free_ring must be a contiguous int32 [ring size]")
     _expect(where, "free_state", free_state, i64, (4,))
-    dev = _one_device(where, query_lens, num_computed_tokens, block_table, free_ring, free_state,
-                      free_state_out, query_start_loc, seq_lens, slot_mapping, positions,
-                      error_word)
-    if any(t is None for t in (query_start_loc, seq_lens, slot_mapping, positions)):
+    if free_state_out is None:
+        free_state_out = free_state
+    elif free_state_out.dtype is not i64 or free_state_out.numel() < 2 or \
+            not free_state_out.is_contiguous():
+        raise ValueError(f"{where}: free_state_out must be int64 with at least 2 entries")
+    dev = query_lens.get_device()
+    _check_device(where, dev, num_computed_tokens, block_table, free_ring, free_state,
+                  free_state_out, query_start_loc, seq_lens, slot_mapping, positions, error_word)
+    if query_start_loc is None or seq_lens is None or slot_mapping is None or positions is None:
         with _allocating_on(dev, stream):
-            new = dict(device=dev)
+            new = dict(device=query_lens.device)
             if query_start_loc is None:
                 query_start_loc = torch.empty(R + 1, dtype=i32, **new)
             if seq_lens is None:
@@ -477,11 +500,6 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
     _expect(where, "seq_lens", seq_lens, i32, (R,))
     _expect(where, "slot_mapping", slot_mapping, i64, (T,))
     _expect(where, "positions", positions, i64, (T,))
-    if free_state_out is None:
-        free_state_out = free_state
-    elif free_state_out.dtype != i64 or free_state_out.numel() < 2 or \
-            not free_state_out.is_contiguous():
-        raise ValueError(f"{where}: free_state_out must be int64 with at least 2 entries")
     _device_call(where, lib().pkv_build_step_metadata, dev, stream, query_lens.data_ptr(),
                  num_computed_tokens.data_ptr(), R, block_table.data_ptr(),
                  _row_stride(block_table), block_table.shape[1], free_ring.data_ptr(),

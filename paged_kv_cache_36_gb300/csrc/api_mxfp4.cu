@@ -84,7 +84,7 @@ MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   MxWorkspace w;
   w.plan = 256;
-  w.ml = w.plan + up((static_cast<size_t>(step_metadata_max_reqs()) + 2) * 4);
+  w.ml = w.plan + up(static_cast<size_t>(step_metadata_max_reqs()) * 8);
   w.o = w.ml + up(slots * group * 8);
   w.total = w.o + up(slots * group * head_dim * 4);
   return w;

@@ -191,7 +191,7 @@ cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, cudaStream_t stream);
 // Scratch of the 4-bit decode: the plan that its join follows, and slots that
 // hold one range's partial of the query heads of one KV head.
 struct MxDecodeScratch {
-  int32_t* plan;              // [num_reqs + 2]
+  int32_t* plan;              // [num_reqs][2]
   float* part_ml;             // [slots][group][2]
   float* part_o;              // [slots][group][head_dim]
 };

@@ -12,8 +12,8 @@
 // partial (m, l, o) per range and head in the workspace, and a second kernel
 // joins them,
 //   M = max_s m_s,  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
-// with one thread per four outputs, in the order of the ranges: no counters, no
-// atomics, the same bits every time.  (Joining in this kernel, by the warp that
+// in an order that the ranges fix: no counters, no atomics, the same bits every
+// time.  (Joining in this kernel, by the warp that
 // came last, took about 18 us of a 230 us call: one warp reads the partials of
 // a request at the latency of L2.)
 //
@@ -91,7 +91,7 @@ struct Params {
   int32_t group;
   float scale_log2;
   uint32_t* err;
-  int32_t* plan;     // [num_reqs + 2]: block sums and the number of ranges, for the join
+  int2* plan;        // [num_reqs]: what there is to join (see slot_of)
   float2* part_ml;   // [2 * ranges][hkv][group]
   float* part_o;     // [2 * ranges][hkv][group][D]
   int32_t stages;
@@ -159,7 +159,7 @@ __device__ __forceinline__ float pow2(int k) {
 // starts inside the range (after its first block) has slot 2q + 1.  A range
 // leaves two partials at most, of the request it begins in and of the one it
 // ends in.
-__device__ __forceinline__ int64_t slot_of(int64_t q, bool starts_inside) {
+__device__ __forceinline__ int slot_of(int q, bool starts_inside) {
   return 2 * q + (starts_inside ? 1 : 0);
 }
 
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   constexpr uint32_t kStage = 2 * kUnit;           // two units
   constexpr int kWarps = warps_per_cta<NT>();
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int32_t scan_tmp[32];
+  __shared__ int32_t warp_sum[kWarps];
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(p.stages) * kWarps * kStage);
 
   // the kernel before may write q, the cache, out or the metadata
@@ -205,7 +205,6 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   const int R = p.num_reqs;
 
   // ---- plan: blocks of every decode request and their prefix sum ----
-  if (threadIdx.x == 0) prefix[0] = 0;
   for (int r = threadIdx.x; r < R; r += blockDim.x) {
     const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
     const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
@@ -221,14 +220,45 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     prefix[r + 1] = nb;
   }
   __syncthreads();
-  block_inclusive_scan(prefix + 1, R, scan_tmp);
-  __syncthreads();
+  {
+    // each thread sums its own run of requests, then the CTA scans
+    const int per = (R + kWarps * 32 - 1) / (kWarps * 32);
+    const int first = min(R, static_cast<int>(threadIdx.x) * per), last = min(R, first + per);
+    int sum = 0;
+    for (int r = first; r < last; ++r) sum += prefix[r + 1];
+    int inc = sum;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    inc -= sum;
+    for (int w = 0; w < warp; ++w) inc += warp_sum[w];
+    if (threadIdx.x == 0) prefix[0] = 0;
+    for (int r = first; r < last; ++r) {
+      inc += prefix[r + 1];
+      prefix[r + 1] = inc;
+    }
+    __syncthreads();
+  }
   const int N = prefix[R];
   const int per_cta = ranges_per_cta(kWarps, p.hkv);
   const int Q = min((N + kMinBlocks - 1) / kMinBlocks, static_cast<int>(gridDim.x) * per_cta);
-  if (blockIdx.x == 0) {
-    for (int r = threadIdx.x; r <= R; r += blockDim.x) p.plan[r] = prefix[r];
-    if (threadIdx.x == 0) p.plan[R + 1] = Q;
+  // what the join has to do for each request: its first range, and twice the
+  // number of its ranges plus whether it starts inside the first; 0: nothing
+  for (int r = threadIdx.x * gridDim.x + blockIdx.x; r < R; r += blockDim.x * gridDim.x) {
+    const int run0 = prefix[r], run1 = prefix[r + 1];
+    int2 to_join = make_int2(0, 0);
+    if (run1 > run0) {
+      // the range of block x: the largest q with floor(qN/Q) <= x
+      const int qf = static_cast<int>(((static_cast<int64_t>(run0) + 1) * Q - 1) / N);
+      const int ql = static_cast<int>((static_cast<int64_t>(run1) * Q - 1) / N);
+      const bool inside = run0 > static_cast<int>(static_cast<int64_t>(qf) * N / Q);
+      if (ql > qf) to_join = make_int2(qf, 2 * (ql - qf + 1) + (inside ? 1 : 0));
+    }
+    p.plan[r] = to_join;
   }
   // few ranges: one per SM first
   const int sub = warp / p.hkv;
@@ -770,7 +800,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       }
     const bool inside = prefix[r] > u0;
     const bool whole = prefix[r] >= u0 && prefix[r + 1] <= u1;
-    const int64_t mine = slot_of(me, inside) * p.hkv + h;
+    const int64_t mine = static_cast<int64_t>(slot_of(me, inside)) * p.hkv + h;
     const int64_t tok = __ldg(p.qsl + r);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -805,40 +835,41 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   }
 }
 
-// Joins the partials of every request that crosses ranges: a thread sums four
-// dimensions of one (request, query head) over its ranges, kBatch loads in
-// flight.
+// Joins the partials of every request that crosses ranges.  Eight lanes take 32
+// dimensions of one (request, query head); the four eights of a warp take every
+// fourth range, kBatch loads of a lane in flight, and add up at the end.
 template <int D>
-__global__ void __launch_bounds__(256) join_mxfp4_kernel(const Params p) {
+__global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
   grid_dependency_wait();  // the decode's partials
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   const int G = p.group, H = p.hkv * G;
-  const int64_t N = __ldcg(p.plan + p.num_reqs), Q = __ldcg(p.plan + p.num_reqs + 1);
-  const int64_t total = static_cast<int64_t>(p.num_reqs) * H * (D / 4);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int r = static_cast<int>(i / (H * (D / 4)));
-    const int rem = static_cast<int>(i - static_cast<int64_t>(r) * (H * (D / 4)));
-    const int head = rem / (D / 4), d4 = rem % (D / 4);
-    const int64_t run0 = __ldcg(p.plan + r), run1 = __ldcg(p.plan + r + 1);
-    if (run0 == run1) continue;  // not a decode row
-    // ranges of a block x: the largest q with floor(qN/Q) <= x
-    const int64_t qf = ((run0 + 1) * Q - 1) / N, ql = (run1 * Q - 1) / N;
-    if (qf == ql) continue;  // written by the decode itself
+  const int lane = threadIdx.x & 31, part = lane >> 3;
+  const int per_req = H * (D / 32);  // warps' items of a request
+  const int64_t total = static_cast<int64_t>(p.num_reqs) * per_req;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < total;
+       i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
+    const int r = static_cast<int>(i / per_req);
+    const int item = static_cast<int>(i - static_cast<int64_t>(r) * per_req);
+    const int2 to_join = __ldcg(p.plan + r);
+    if (to_join.y == 0) continue;  // written by the decode itself, or no decode row
+    const int splits = to_join.y >> 1;
+    const bool inside = to_join.y & 1;
+    const int head = item / (D / 32), d4 = (item % (D / 32)) * 8 + (lane & 7);
     const int h = head / G, g = head - h * G;
-    const bool inside = run0 > qf * N / Q;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float big = -INFINITY, den = 0.f;
-    for (int64_t q = qf; q <= ql; q += kBatch) {
+    for (int k0 = part; k0 < splits; k0 += 4 * kBatch) {
       float2 ml[kBatch];
       float4 x[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
+        const int q = k0 + 4 * k;
         ml[k] = make_float2(-INFINITY, 0.f);
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q + k <= ql) {
-          const int64_t at = (slot_of(q + k, q + k == qf && inside) * p.hkv + h) * G + g;
+        if (q < splits) {
+          const int64_t at =
+              (static_cast<int64_t>(slot_of(to_join.x + q, q == 0 && inside)) * p.hkv + h) * G + g;
           ml[k] = __ldcg(p.part_ml + at);
           x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + d4);
         }
@@ -855,7 +886,7 @@ __global__ void __launch_bounds__(256) join_mxfp4_kernel(const Params p) {
       acc.w *= keep;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (q + k > ql) break;
+        if (k0 + 4 * k >= splits) break;
         const float w = ml[k].x == mx ? 1.f : exp2_approx(ml[k].x - mx);
         den = fmaf(ml[k].y, w, den);
         acc.x = fmaf(x[k].x, w, acc.x);
@@ -864,10 +895,26 @@ __global__ void __launch_bounds__(256) join_mxfp4_kernel(const Params p) {
         acc.w = fmaf(x[k].w, w, acc.w);
       }
     }
-    const float inv = 1.f / den;
-    const int64_t tok = __ldg(p.qsl + r);
-    *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + static_cast<int64_t>(head) * D + 4 * d4) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+#pragma unroll
+    for (int x = 8; x < 32; x <<= 1) {
+      const float mx = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+      const float w = big == mx ? 1.f : exp2_approx(big - mx);
+      big = mx;
+      den *= w;
+      den += __shfl_xor_sync(0xffffffffu, den, x);
+      float* a = &acc.x;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        a[c] *= w;
+        a[c] += __shfl_xor_sync(0xffffffffu, a[c], x);
+      }
+    }
+    if (part == 0) {
+      const float inv = 1.f / den;
+      const int64_t tok = __ldg(p.qsl + r);
+      *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + static_cast<int64_t>(head) * D + 4 * d4) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
   }
 }
 
@@ -886,8 +933,8 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   e = launch_programmatic(decode_mxfp4_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
                           dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  const int64_t threads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group * (D / 4);
-  int64_t grid = (threads + 255) / 256;
+  const int64_t items = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group * (D / 32);
+  int64_t grid = (items + 7) / 8;
   if (grid > 8 * static_cast<int64_t>(sms)) grid = 8 * static_cast<int64_t>(sms);
   return launch_programmatic(join_mxfp4_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
                              stream, p);
@@ -921,7 +968,7 @@ cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, in
   p.group = a.num_heads / a.num_kv_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
-  p.plan = ws.plan;
+  p.plan = reinterpret_cast<int2*>(ws.plan);
   p.part_ml = reinterpret_cast<float2*>(ws.part_ml);
   p.part_o = ws.part_o;
   p.stages = 0;
