@@ -221,8 +221,9 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   ds.plan = reinterpret_cast<int32_t*>(ws + w.plan);
   ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
   ds.part_o = reinterpret_cast<float*>(ws + w.o);
-  cudaError_t e = launch_decode_mxfp4(a, ds, sms, st);
-  if (e == cudaSuccess && max_query_len != 1) e = launch_attn_rows_mxfp4(a, st);
+  cudaError_t e = cudaSuccess;
+  if (max_query_len != 1) e = launch_prefill_mxfp4(a, sms, st);
+  if (e == cudaSuccess) e = launch_decode_mxfp4(a, ds, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_mxfp4 launch");
   return validate_error_word(a.err, st, "paged_attention_varlen_mxfp4");
 }

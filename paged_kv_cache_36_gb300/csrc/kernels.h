@@ -184,9 +184,9 @@ struct MxCacheArgs {
 cudaError_t launch_reshape_and_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 
-// Attention over the 4-bit paged cache on CUDA cores, one warp per (query
-// row, head), of the rows of requests with query length > 1.
-cudaError_t launch_attn_rows_mxfp4(const AttnArgs& a, cudaStream_t stream);
+// Chunked-prefill attention over the 4-bit cache (tcgen05) of the rows of
+// requests with query length > 1, on a device of `sms` SMs.
+cudaError_t launch_prefill_mxfp4(const AttnArgs& a, int sms, cudaStream_t stream);
 
 // Scratch of the 4-bit decode: the plan that its join follows, and slots that
 // hold one range's partial of the query heads of one KV head.

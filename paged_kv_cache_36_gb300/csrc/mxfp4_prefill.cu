@@ -1,0 +1,875 @@
+// Chunked-prefill attention over the 4-bit paged cache on the 5th-generation
+// tensor cores: rows of requests with query length > 1.
+//
+// For a query row at position p and KV head g, out = softmax_{j <= p}(scale
+// <q, K_j>) V_j with K, V the values that codes and power-of-two scales stand
+// for (mxfp4.cuh).
+//
+// Tiling is that of the bfloat16 prefill: 128 rows = floor(128 / G) query tokens
+// x the G query heads of a KV head against key tiles of 128, S = Q K^T and O += P
+// V as tcgen05 products, S and O in tensor memory, P written over S.  The operands
+// are f16, and the copies are made by four warps that convert:
+//   - Thread t of the four takes key t of every key tile, 64 code bytes of K and
+//     of V (head_dim 128): one conversion a pair, one f16x2 product by its
+//     group's scale, one 16-byte store per 8 dimensions, in the 128-byte
+//     swizzled layout that both operands read.  Codes of the next tile are
+//     loaded while this one is converted.
+//   - Scales.  A warp's 32 keys share a base exponent for K and one for V: a value
+//     is code 2^(e - base + 12) in f16, exact for scales down to 2^-26 of the
+//     base's and then rounded at f16's 2^-25.  The softmax puts the bases back
+//     for free: x = s f + (v - M), with f = 2^(K base) times the query's factor
+//     and v the V base in log2 units, so that P carries 2^v, the running
+//     maximum M is one of s + v, and l sums P 2^(vref - v).  Where the keys of
+//     the 32 differ by more than 2^14 (an outlier, perhaps one that the row may
+//     not even see), every key gets a base of its own, and the softmax a factor
+//     and an offset per column: no key's precision depends on another's.
+//   - Q is brought to f16 by a power of two per row, as in the decode.
+//   - A V group that is NaN is stored as zeros, and its position noted; a row at
+//     or behind it gets NaN in that group's dimensions.  (0 times NaN would
+//     poison the rows before it.)
+//
+// What bounds it: the softmax's exponentials and the conversion share the SM's
+// issue slots beside the tensor core; K and V come from L2 at a quarter of the
+// bytes.
+//
+// Warp roles (16 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1
+// issues P V; warps 4-11 run the softmax and the epilogue, two per 32-lane quadrant
+// of tensor memory, each with half of the key tile's columns; warps 12-15 convert.
+// Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that
+// stops all roles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "pkv_device.cuh"
+#include "prefill_common.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kKeys = 128;
+constexpr uint32_t kRegion = 16384;  // 128 rows x 128 bytes
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kSBufs = 3;
+constexpr int kMetas = 4;            // key tiles whose scales are in flight
+constexpr int kThreads = 512;
+constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;
+constexpr uint32_t kColO = kSBufs * kKeys;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kUp = 12;              // a base's scale becomes 2^kUp: 6 2^12 is inside f16
+constexpr int kWide = 14;            // binades between the keys of a warp before each has its base
+constexpr size_t kSmemLimit = 232448;
+
+enum Bar {
+  kQFull, kQEmpty,
+  kKFull0, kKEmpty0 = kKFull0 + kKStages,
+  kVFull0 = kKEmpty0 + kKStages, kVEmpty0 = kVFull0 + kVStages,
+  kSFull0 = kVEmpty0 + kVStages, kSFree0 = kSFull0 + kSBufs,
+  kPFull0 = kSFree0 + kSBufs, kODone0 = kPFull0 + kSBufs,
+  kOFinal = kODone0 + kSBufs, kPair0,
+  kMFull0 = kPair0 + 4, kMFree0 = kMFull0 + kMetas,
+  kNumBars = kMFree0 + kMetas
+};
+
+struct Params {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const uint8_t* key_cache;
+  const uint8_t* value_cache;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  int32_t bt_width;
+  const int32_t* qsl;
+  const int32_t* seq_lens;
+  const int32_t* num_computed;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  int64_t num_tokens;
+  int32_t num_reqs;
+  int32_t num_blocks;
+  int32_t hkv;
+  int32_t group;
+  float scale_log2;
+  uint32_t* err;
+  int32_t entry_shift;  // requests per plan entry, as a power of two
+};
+
+// What the softmax has to know of one key tile: by converting warp (32 keys), and
+// by key where a warp's keys are far apart.
+struct Meta {
+  float kf[4];           // K base: 2^(base - 127 - kUp)
+  float vb[4];           // V base: base - 127 - kUp, log2 units
+  uint32_t flags[4];     // 1: K by key, 2: V by key, 4: NaN in V
+  int32_t nan_pos[4][4]; // first key position with a NaN V group, by warp and group
+  float key_kf[kKeys];
+  float key_vb[kKeys];
+  float qf[kRows];       // per row, with the query tile's first key tile
+};
+
+template <int D>
+struct Layout {
+  static constexpr int NDH = D / 64;
+  static constexpr uint32_t kHalf = NDH * kRegion;  // one K (or V or Q) tile
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + kHalf;
+  static constexpr uint32_t kV = kK + kKStages * kHalf;
+  static constexpr uint32_t kBars = kV + kVStages * kHalf;
+  static constexpr uint32_t kXch = kBars + 8 * kNumBars;     // [2 parity][2 half][128 rows] floats
+  static constexpr uint32_t kMeta = kXch + 2 * 2 * 128 * 4;
+  static constexpr uint32_t kMisc = kMeta + kMetas * sizeof(Meta);  // tensor memory slot, abort flag
+  static constexpr uint32_t kPrefix = kMisc + 16;
+};
+
+struct Tile {
+  int r, h, u0, ntok;
+  int nkeys;   // keys any of the tile's rows sees
+  int nkt;     // key tiles
+  int64_t qs;
+  int nc;
+};
+
+// Query tiles of request r (all KV heads); 0 where it has no rows here or its
+// metadata is wrong (*bad).
+__device__ __forceinline__ int request_tiles(const Params& p, int r, int tpt, bool* bad) {
+  const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
+  const int qlen = q1 - q0;
+  if (qlen <= 1) return 0;
+  const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || nc < 0 || nc > 0x7fffffff - qlen ||
+      seq != nc + qlen || (seq - 1) / kMxBlock >= p.bt_width) {
+    *bad = true;
+    return 0;
+  }
+  return (qlen + tpt - 1) / tpt * p.hkv;
+}
+
+// Tile `ct` -> (request, KV head, query rows).  prefix[i] counts the tiles before
+// plan entry i; within a request tiles run KV head fastest, then query tiles.
+__device__ __forceinline__ Tile find_tile(int ct, const int32_t* prefix, int entries,
+                                          const Params& p, int tpt) {
+  int lo = 0, hi = entries;  // prefix[lo] <= ct < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= ct) lo = mid; else hi = mid;
+  }
+  Tile t;
+  t.r = lo << p.entry_shift;
+  int rem = ct - prefix[lo];
+  if (p.entry_shift > 0) {  // an entry of several requests
+    bool bad = false;
+    for (int n = request_tiles(p, t.r, tpt, &bad); rem >= n; n = request_tiles(p, t.r, tpt, &bad)) {
+      rem -= n;
+      ++t.r;
+    }
+  }
+  const int qt = rem / p.hkv;
+  t.h = rem - qt * p.hkv;
+  t.qs = __ldg(p.qsl + t.r);
+  const int qlen = __ldg(p.qsl + t.r + 1) - static_cast<int>(t.qs);
+  t.nc = __ldg(p.num_computed + t.r);
+  t.u0 = qt * tpt;
+  t.ntok = min(tpt, qlen - t.u0);
+  t.nkeys = t.nc + t.u0 + t.ntok;
+  t.nkt = (t.nkeys + kKeys - 1) / kKeys;
+  return t;
+}
+
+// 2^k, subnormal or zero below 2^-126.
+__device__ __forceinline__ float pow2(int k) {
+  if (k >= -126) return __uint_as_float(static_cast<uint32_t>(min(k, 127) + 127) << 23);
+  return k < -149 ? 0.f : __uint_as_float(1u << (k + 149));
+}
+
+// 2^x as a pair of f16, gradually down to 2^-24, then 0.
+__device__ __forceinline__ uint32_t f16x2_pow2(int x) {
+  const uint32_t h = x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+  return h * 0x00010001u;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Instruction descriptor of kind::f16 with f16 A and B, float32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_major) {
+  return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// The codes of one key's row, and the scale bytes of its groups in order.
+template <int D>
+struct KeyRow {
+  uint4 c[D / 32];
+  uint32_t e;
+};
+
+// Eight codes times their group's scale, to one 16-byte piece of a tile row.
+__device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
+  uint32_t x[4];
+  e2m1x8_to_f16(w, x);
+  return make_uint4(mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f), mul_f16x2(x[3], f));
+}
+
+// The largest scale byte of a row that is not NaN, or -1.
+template <int D>
+__device__ __forceinline__ int largest_scale(uint32_t e) {
+  int m = -1;
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b) {
+    const int x = (e >> (8 * b)) & 0xff;
+    if (x != 255) m = max(m, x);
+  }
+  return m;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params p) {
+  using L = Layout<D>;
+  constexpr int NDH = L::NDH;
+  constexpr int NB = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  float* xch = reinterpret_cast<float*>(smem + L::kXch);
+  Meta* metas = reinterpret_cast<Meta*>(smem + L::kMeta);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
+
+  // the kernel before may write q, the cache, out or the metadata
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.num_reqs;
+  const int entries = (R + (1 << p.entry_shift) - 1) >> p.entry_shift;
+  int32_t* scan_tmp = prefix + entries + 1;
+  const int cid = blockIdx.x, ncta = gridDim.x;
+  const int G = p.group;
+  const int tpt = kRows / G;  // query tokens per tile
+
+  // ---- plan: tiles per entry and their prefix sum ----
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    prefix[0] = 0;
+    for (int b = 0; b < kNumBars; ++b) {
+      uint32_t n = 1;
+      if (b == kQFull || (b >= kKFull0 && b < kKFull0 + kKStages) ||
+          (b >= kVFull0 && b < kVFull0 + kVStages) || (b >= kMFull0 && b < kMFull0 + kMetas))
+        n = 4;  // converting warps
+      if ((b >= kPFull0 && b < kPFull0 + kSBufs) || (b >= kMFree0 && b < kMFree0 + kMetas))
+        n = 8;  // softmax warps
+      if (b >= kPair0 && b < kPair0 + 4) n = 2;  // the two warps sharing a quadrant
+      mbar_init(&bars[b], n);
+    }
+    fence_mbar_init();
+  }
+  bool bad = false;
+  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
+    int n = 0;
+    for (int k = 0; k < (1 << p.entry_shift); ++k) {
+      const int r = (i << p.entry_shift) + k;
+      if (r < R) n += request_tiles(p, r, tpt, &bad);
+    }
+    prefix[i + 1] = n;
+  }
+  if (bad && cid == 0) atomicOr(p.err, PKV_ERR_METADATA);
+  __syncthreads();
+  block_inclusive_scan(prefix + 1, entries, scan_tmp);
+  __syncthreads();
+  const int total = prefix[entries];
+  if (cid >= total) return;  // no tile for this CTA, and no tensor memory held
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ============================ QK^T issuer ============================
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys, 0);
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::kQ), 16, 1024);
+      // K stage: groups of 8 keys every NDH KiB, dim half dh at +dh KiB
+      const uint64_t k_desc0 = smem_desc_sw128(smem_u32(smem + L::kK), 16, NDH * 1024);
+      uint32_t q_count = 0, count = 0;
+      bool ok = true;
+      for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok && !*abort_flag;
+           ct = cta_tile(++it, cid, ncta, total)) {
+        const Tile t = find_tile(ct, prefix, entries, p, tpt);
+        ok = mbar_wait_or_abort(&bars[kQFull], q_count & 1, p.err, abort_flag);
+        ++q_count;
+        for (int j = 0; j < t.nkt && ok; ++j, ++count) {
+          const int ks = count % kKStages, b = count % kSBufs;
+          ok = mbar_wait_or_abort(&bars[kKFull0 + ks], (count / kKStages) & 1, p.err, abort_flag);
+          // S/P buffer b is free once PV of the key tile that last used it is done
+          if (ok && count >= kSBufs)
+            ok = mbar_wait_or_abort(&bars[kSFree0 + b], (count / kSBufs - 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = k_desc0 + ((ks * L::kHalf) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t q_off = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
+            const uint64_t k_off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+            tc_mma_ss(tmem + kColS + b * kKeys, q_desc + q_off, kd + k_off, idesc_s, kk > 0);
+          }
+          tc_commit(&bars[kSFull0 + b]);
+          tc_commit(&bars[kKEmpty0 + ks]);
+          if (j == t.nkt - 1) tc_commit(&bars[kQEmpty]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ============================ PV issuer ============================
+    if (lane == 0) {
+      constexpr uint32_t idesc_o = idesc_f16_f32(kRows, D, 1);
+      // V stage, MN-major: 64-dim atoms of a group of 8 keys 1 KiB apart, groups
+      // of 8 keys NDH KiB apart
+      const uint64_t v_desc0 = smem_desc_sw128(smem_u32(smem + L::kV), 1024, NDH * 1024);
+      uint32_t count = 0;
+      bool ok = true;
+      for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok && !*abort_flag;
+           ct = cta_tile(++it, cid, ncta, total)) {
+        const Tile t = find_tile(ct, prefix, entries, p, tpt);
+        for (int j = 0; j < t.nkt && ok; ++j, ++count) {
+          const int vs = count % kVStages, b = count % kSBufs;
+          ok = mbar_wait_or_abort(&bars[kPFull0 + b], (count / kSBufs) & 1, p.err, abort_flag) &&
+               mbar_wait_or_abort(&bars[kVFull0 + vs], (count / kVStages) & 1, p.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc0 + ((vs * L::kHalf) >> 4);
+          const uint32_t a_p = tmem + kColS + b * kKeys;
+          // P columns hold the keys of each softmax half in their first 32 (f16
+          // pairs), V rows [64 half, 64 half + 64)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_ts(tmem + kColO, a_p + half * 64 + kk * 8,
+                        vd + ((((half * 64 + kk * 16) / 8) * NDH * 1024) >> 4), idesc_o,
+                        (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(&bars[kODone0 + b]);
+          if (j == t.nkt - 1) tc_commit(&bars[kOFinal]);
+          tc_commit(&bars[kSFree0 + b]);
+          tc_commit(&bars[kVEmpty0 + vs]);
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ============================ converting warps ============================
+    const int cw = warp - 12;              // keys [32 cw, 32 cw + 32) of every key tile
+    const int key = cw * 32 + lane;
+    const int64_t block_bytes = static_cast<int64_t>(p.hkv) * mx_chunk_bytes(D);
+    // where this thread's row starts in a K or V stage, and its swizzle
+    const uint32_t row_off = (key / 8) * NDH * 1024 + (key % 8) * 128;
+    const int sw = key % 8;
+    uint32_t count = 0, tiles = 0;
+    bool ok = true;
+    for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok;
+         ct = cta_tile(++it, cid, ncta, total), ++tiles) {
+      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+      const Tile t = find_tile(ct, prefix, entries, p, tpt);
+      const int32_t* row = p.block_table + static_cast<int64_t>(t.r) * p.bt_stride;
+      // this thread's block of key tile j, or -1 (behind the keys, or not in the pool)
+      auto load_id = [&](int j) -> int {
+        const int pos = j * kKeys + key;
+        return j < t.nkt && pos < t.nkeys ? __ldg(row + pos / kMxBlock) : -1;
+      };
+      auto check_id = [&](int id, int j) -> int {
+        if (j < t.nkt && j * kKeys + key < t.nkeys && (id < 0 || id >= p.num_blocks)) {
+          atomicOr(p.err, PKV_ERR_BLOCK_ID);
+          return -1;
+        }
+        return id;
+      };
+      const int tk = key % kMxBlock;  // token within the block
+      auto load_k = [&](int id, KeyRow<D>& k) {
+        k.e = 0u;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) k.c[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (id < 0) return;
+        const uint8_t* chunk = p.key_cache + id * block_bytes + t.h * mx_chunk_bytes(D);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          k.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
+        if constexpr (D == 128)
+          k.e = __ldg(reinterpret_cast<const uint32_t*>(chunk + mx_scale_off(D)) + tk);
+        else
+          k.e = __ldg(reinterpret_cast<const uint16_t*>(chunk + mx_scale_off(D)) + tk);
+      };
+      auto load_v = [&](int id, KeyRow<D>& v) {
+        v.e = 0u;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) v.c[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (id < 0) return;
+        const uint8_t* chunk = p.value_cache + id * block_bytes + t.h * mx_chunk_bytes(D);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          v.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w)
+          v.e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(
+                     chunk + mx_vscale_off<D>(tk, 2 * w)))) << (16 * w);
+      };
+      KeyRow<D> k, v;
+      int id = check_id(load_id(0), 0);
+      int next_id = load_id(1);
+      load_k(id, k);
+      load_v(id, v);
+
+      // ---- Q: thread t brings row t to f16 ----
+      float qf = 0.f;
+      {
+        const int u = key / G;
+        const bool real = u < t.ntok;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
+            static_cast<int64_t>(t.h * G + (real ? key % G : 0)) * D);
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = __ldg(src + i);
+          mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
+                           max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
+          mx = max(mx, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu),
+                           max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
+        }
+        // largest element to [2^14, 2^15); the scale's sign goes onto Q
+        const int ex = static_cast<int>(min(max(mx >> 7, 15u), 254u));
+        const float f = copysignf(pow2(141 - ex), p.scale_log2);
+        qf = fabsf(p.scale_log2) * pow2(ex - 141);
+        // the tile before is done with the buffer
+        if (tiles > 0) ok = warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
+        if (!ok) break;
+        uint8_t* dst = smem + L::kQ + key * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = __ldg(src + i);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            y[c] = real ? pack_f16(__uint_as_float(w[c] << 16) * f,
+                                   __uint_as_float(w[c] & 0xffff0000u) * f)
+                        : 0u;
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * kRegion + (((i & 7) ^ sw) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kQFull]);
+      }
+
+      for (int j = 0; j < t.nkt && ok; ++j, ++count) {
+        const bool real = id >= 0;  // else zeros, which no base follows
+        // ---- bases of the warp's 32 keys ----
+        const int km = real ? largest_scale<D>(k.e) : -1, vm = real ? largest_scale<D>(v.e) : -1;
+        int kb = __reduce_max_sync(0xffffffffu, km), vbase = __reduce_max_sync(0xffffffffu, vm);
+        const int kmin = __reduce_min_sync(0xffffffffu, km < 0 ? 1000 : km);
+        const int vmin = __reduce_min_sync(0xffffffffu, vm < 0 ? 1000 : vm);
+        if (kb < 0) kb = 127;
+        if (vbase < 0) vbase = 127;
+        const bool kwide = kb - kmin > kWide, vwide = vbase - vmin > kWide;
+        uint32_t nan = 0u;  // groups of this key's V that are NaN
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (real && ((v.e >> (8 * b)) & 0xffu) == 255u) nan |= 1u << b;
+        const bool any_nan = __any_sync(0xffffffffu, nan != 0u);
+        const int ms = count % kMetas;
+        Meta& meta = metas[ms];
+        if (count >= kMetas) {
+          ok = warp_wait(&bars[kMFree0 + ms], (count / kMetas - 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          meta.kf[cw] = pow2(kb - 127 - kUp);
+          meta.vb[cw] = static_cast<float>(vbase - 127 - kUp);
+          meta.flags[cw] = (kwide ? 1u : 0u) | (vwide ? 2u : 0u) | (any_nan ? 4u : 0u);
+        }
+        if (kwide || vwide) {
+          if (kwide && km >= 0) kb = km;
+          if (vwide && vm >= 0) vbase = vm;
+          meta.key_kf[key] = pow2(kb - 127 - kUp);
+          meta.key_vb[key] = static_cast<float>(vbase - 127 - kUp);
+        }
+        if (any_nan) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int first = __reduce_min_sync(0xffffffffu, (nan >> b) & 1u ? j * kKeys + key : 0x7fffffff);
+            if (lane == 0) meta.nan_pos[cw][b] = first;
+          }
+        }
+        if (j == 0) meta.qf[key] = qf;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
+
+        // ---- K ----
+        const int id1 = check_id(next_id, j + 1);
+        next_id = load_id(j + 2);
+        {
+          const int ks = count % kKStages;
+          if (count >= kKStages) {
+            ok = warp_wait(&bars[kKEmpty0 + ks], (count / kKStages - 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+          }
+          uint8_t* dst = smem + L::kK + ks * L::kHalf + row_off;
+          uint32_t f[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int e = (k.e >> (8 * b)) & 0xff;
+            f[b] = e == 255 ? 0x7fff7fffu : f16x2_pow2(e - kb + kUp);
+          }
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {k.c[i].x, k.c[i].y, k.c[i].z, k.c[i].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              // head_dim 128: word x of piece i is (c = i, b = x); 64: (c = 2i + x / 2, b = x % 2)
+              const int c = D == 128 ? i : 2 * i + (x >> 1), b = D == 128 ? x : x & 1;
+              const int piece = 4 * b + c;  // dims 8 piece .. + 7
+              *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
+                  convert8(w[x], f[b]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kKFull0 + ks]);
+        }
+        load_k(id1, k);
+
+        // ---- V ----
+        {
+          const int vs = count % kVStages;
+          if (count >= kVStages) {
+            ok = warp_wait(&bars[kVEmpty0 + vs], (count / kVStages - 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+          }
+          uint8_t* dst = smem + L::kV + vs * L::kHalf + row_off;
+          uint32_t f[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int e = (v.e >> (8 * b)) & 0xff;
+            f[b] = e == 255 ? 0u : f16x2_pow2(e - vbase + kUp);
+          }
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {v.c[i].x, v.c[i].y, v.c[i].z, v.c[i].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              // the half-words of two words make 8 consecutive dimensions.  head_dim
+              // 128: words (b / 2) of lane groups 2i and 2i + 1; 64: of 4i + 2 (x / 2), + 1
+              const int b = D == 128 ? x : x & 1;
+              const int y = D == 128 ? i : 2 * i + (x >> 1);
+              const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (x >> 1)];
+              const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (x >> 1) + 1];
+              const uint32_t codes = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
+              const int piece = 4 * b + y;
+              *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
+                  convert8(codes, f[b]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kVFull0 + vs]);
+        }
+        load_v(id1, v);
+        id = id1;
+      }
+    }
+  } else if (warp >= 4) {
+    // ============================ softmax warps ============================
+    // Two warps share each 32-lane quadrant of tensor memory (the same 32 rows):
+    // warp half h reads S columns [64 h, 64 h + 64), the keys of converting warps
+    // 2h and 2h + 1.  They agree on the row maximum every key tile, so one O
+    // serves the row; each keeps the partial sum l of its own columns.
+    const int quad = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const int row = quad * 32 + lane;    // tile row = tensor-memory lane
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t o_cols = lane_addr + kColO + half * (D / 2);
+    uint64_t* pair_bar = &bars[kPair0 + quad];
+    uint32_t count = 0, pair_uses = 0, tiles_done = 0;
+    auto exchange = [&](float mine) -> float {
+      float* slot = xch + (pair_uses & 1) * 256;
+      slot[half * 128 + row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_bar);
+      const bool done = warp_wait(pair_bar, pair_uses & 1, p.err, abort_flag);
+      ++pair_uses;
+      return done ? slot[(half ^ 1) * 128 + row] : mine;
+    };
+    for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0;
+         ct = cta_tile(++it, cid, ncta, total)) {
+      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+      const Tile t = find_tile(ct, prefix, entries, p, tpt);
+      const int u = row / G;
+      const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
+      const int pos_min = t.nc + t.u0;
+      float m_used = -INFINITY, l = 0.f, qf = 0.f, vref = 0.f;
+      uint32_t nan_groups = 0u;  // V groups that are NaN for this row
+      bool ok = true;
+      for (int j = 0; j < t.nkt && ok; ++j, ++count) {
+        const int b = count % kSBufs, ms = count % kMetas;
+        if (!warp_wait(&bars[kMFull0 + ms], (count / kMetas) & 1, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const Meta& meta = metas[ms];
+        if (j == 0) {
+          qf = meta.qf[row];
+          vref = meta.vb[0];
+        }
+        float f[2], vb[2];
+        uint32_t flags = meta.flags[0] | meta.flags[1] | meta.flags[2] | meta.flags[3];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          // never zero, for the masked scores' infinities
+          f[g] = qf * meta.kf[2 * half + g];
+          f[g] = f[g] < 1.17549435e-38f ? 1.17549435e-38f : f[g];
+          vb[g] = meta.vb[2 * half + g];
+        }
+        if (!warp_wait(&bars[kSFull0 + b], (count / kSBufs) & 1, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
+        float sv[64];
+        {
+          uint32_t (&r)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sv);
+          tmem_ld32(s_cols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+          tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+          tmem_wait_ld();
+        }
+        float lw[2];  // what brings a weight with its V base back: 2^(vref - vb)
+        lw[0] = pow2(static_cast<int>(vref - vb[0]));
+        lw[1] = pow2(static_cast<int>(vref - vb[1]));
+        bool by_key[2] = {false, false};
+        if (flags != 0u) {
+          // rare: keys with bases of their own, NaN in V
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t fl = meta.flags[2 * half + g];
+            if (fl & 3u) {
+              by_key[g] = true;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const int key = half * 64 + g * 32 + c;
+                float fk = qf * meta.key_kf[key];
+                fk = fk < 1.17549435e-38f ? 1.17549435e-38f : fk;
+                sv[32 * g + c] = fmaf(sv[32 * g + c], fk, meta.key_vb[key]);
+              }
+              f[g] = 1.f;
+              vb[g] = 0.f;
+            }
+          }
+          if (flags & 4u)
+            for (int w = 0; w < 4; ++w)
+              if (meta.flags[w] & 4u)
+#pragma unroll
+                for (int g = 0; g < NB; ++g)
+                  if (meta.nan_pos[w][g] <= pos) nan_groups |= 1u << g;
+        }
+        // causal mask (only tiles reaching past the tile's first row) and max
+        const int key0 = j * kKeys + half * 64;
+        if (key0 + 63 > pos_min) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (key0 + c > pos) sv[c] = -INFINITY;
+        }
+        float mg[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float m4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m4[c] = sv[32 * g + c];
+#pragma unroll
+          for (int c = 4; c < 28; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], sv[32 * g + c + k], sv[32 * g + c + 4 + k]);
+          float x = fmax3(m4[0], m4[1], fmax3(m4[2], m4[3], sv[32 * g + 28]));
+          x = fmax3(x, sv[32 * g + 29], fmax3(sv[32 * g + 30], sv[32 * g + 31], x));
+          mg[g] = fmaf(x, f[g], vb[g]);
+        }
+        const float m_mine = fmaxf(mg[0], mg[1]);
+        const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
+        if (j == 0) {
+          m_used = mx;  // key 0 is visible to every row
+        } else {
+          // both warps of the quadrant see the same mx and m_used
+          const bool grow = mx > m_used + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, grow)) {
+            // O must hold PV of the previous key tile before it is rescaled
+            const uint32_t prev = count - 1;
+            if (!warp_wait(&bars[kODone0 + prev % kSBufs], (prev / kSBufs) & 1, p.err, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
+            if (grow) m_used = mx;
+            l *= alpha;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t r32[32];
+              tmem_ld32(o_cols + c * 32, r32);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                r32[e] = __float_as_uint(__uint_as_float(r32[e]) * alpha);
+              tmem_st32(o_cols + c * 32, r32);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P = 2^(s f + vb - m_used) as f16 pairs over the first 32 of this
+        // warp's 64 S columns
+        uint32_t w[32];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float2 f2 = make_float2(f[g], f[g]);
+          const float2 c2 = make_float2(vb[g] - m_used, vb[g] - m_used);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float by = 0.f;
+          const bool keyed = by_key[g];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(sv[32 * g + 2 * e], sv[32 * g + 2 * e + 1]), f2, c2);
+            const float2 pe = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            l2[e & 1] = __fadd2_rn(l2[e & 1], pe);
+            w[16 * g + e] = pack_f16(pe.x, pe.y);
+            if (keyed) {
+              // the weight from the score itself: with a small enough V scale P is 0
+              const int key = half * 64 + g * 32 + 2 * e;
+              by += exp2_approx(sv[32 * g + 2 * e] - meta.key_vb[key] + (vref - m_used));
+              by += exp2_approx(sv[32 * g + 2 * e + 1] - meta.key_vb[key + 1] + (vref - m_used));
+            }
+          }
+          l += keyed ? by : ((l2[0].x + l2[1].x) + (l2[0].y + l2[1].y)) * lw[g];
+        }
+        tmem_st32(s_cols, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[kPFull0 + b]);
+          mbar_arrive(&bars[kMFree0 + ms]);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: O 2^vref / (l_0 + l_1) -> out ----
+      if (!warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
+      ++tiles_done;
+      tc_fence_after();
+      // (two factors: their product may be too small for a float)
+      const float inv = 1.f / (l + exchange(l)), unit = pow2(static_cast<int>(vref));
+      // This warp holds output dims [half * D/2, half * D/2 + D/2) of its 32
+      // rows: NV 16-byte pieces per row, transposed among groups of NV lanes so
+      // that every store instruction writes whole rows' segments.
+      constexpr int NV = D / 16;
+      uint4 seg[NV];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t r0[32];
+        tmem_ld32(lane_addr + kColO + half * (D / 2) + c * 32, r0);
+        tmem_wait_ld();
+        // these 32 dimensions are one scale group of V
+        const float s = (nan_groups >> (half * (D / 64) + c)) & 1u ? __uint_as_float(0x7fffffffu) : inv;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint4& v = seg[c * 4 + q4];
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r0[q4 * 8 + e]) * s * unit;
+          v.x = pack_bf16(x[0], x[1]);
+          v.y = pack_bf16(x[2], x[3]);
+          v.z = pack_bf16(x[4], x[5]);
+          v.w = pack_bf16(x[6], x[7]);
+        }
+      }
+      transpose_lane_groups<NV>(seg, lane);
+      // lane NV g + j now holds piece j of rows NV g + k (k < NV) of the warp
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int trow = quad * 32 + (lane & ~(NV - 1)) + k;  // tile row
+        if (trow / G < t.ntok) {
+          __nv_bfloat16* dst = p.out + (t.qs + t.u0 + trow / G) * p.out_stride +
+                               static_cast<int64_t>(t.h * G + trow % G) * D + half * (D / 2) +
+                               (lane & (NV - 1)) * 8;
+          *reinterpret_cast<uint4*>(dst) = seg[k];
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+static cudaError_t launch_prefill_t(Params p, int sms, cudaStream_t stream) {
+  int entries = p.num_reqs;
+  p.entry_shift = 0;
+  while (entries > kPrefixMax) {
+    ++p.entry_shift;
+    entries = (p.num_reqs + (1 << p.entry_shift) - 1) >> p.entry_shift;
+  }
+  const size_t smem = 1024 + Layout<D>::kPrefix + 4 * (static_cast<size_t>(entries) + 1) + 4 * 32;
+  if (smem > kSmemLimit) return cudaErrorInvalidValue;
+  const cudaError_t e = raise_smem_limit_once<prefill_mxfp4_kernel<D>>(kSmemLimit);
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(prefill_mxfp4_kernel<D>, dim3(static_cast<unsigned>(sms)), dim3(kThreads),
+                             smem, stream, p);
+}
+
+cudaError_t launch_prefill_mxfp4(const AttnArgs& a, int sms, cudaStream_t stream) {
+  Params p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.q_stride = a.q_stride;
+  p.key_cache = static_cast<const uint8_t*>(a.key_cache);
+  p.value_cache = static_cast<const uint8_t*>(a.value_cache);
+  p.block_table = a.block_table;
+  p.bt_stride = a.bt_stride;
+  p.bt_width = a.bt_width;
+  p.qsl = a.qsl;
+  p.seq_lens = a.seq_lens;
+  p.num_computed = a.num_computed;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.out_stride = a.out_stride;
+  p.num_tokens = a.num_tokens;
+  p.num_reqs = a.num_reqs;
+  p.num_blocks = static_cast<int32_t>(a.num_blocks);
+  p.hkv = a.num_kv_heads;
+  p.group = a.num_heads / a.num_kv_heads;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.err = a.err;
+  p.entry_shift = 0;
+  if (a.head_dim == 128) return launch_prefill_t<128>(p, sms, stream);
+  if (a.head_dim == 64) return launch_prefill_t<64>(p, sms, stream);
+  return cudaErrorNotSupported;
+}
+
+}  // namespace pkv
