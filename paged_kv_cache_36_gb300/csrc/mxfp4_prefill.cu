@@ -32,9 +32,10 @@
 // issue slots beside the tensor core; K and V come from L2 at a quarter of the
 // bytes.
 //
-// Warp roles (16 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1
+// Warp roles (20 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1
 // issues P V; warps 4-11 run the softmax and the epilogue, two per 32-lane quadrant
-// of tensor memory, each with half of the key tile's columns; warps 12-15 convert.
+// of tensor memory, each with half of the key tile's columns; warps 12-15 convert
+// Q and K, warps 16-19 V.
 // Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that
 // stops all roles.
 #include <cuda_bf16.h>
@@ -60,7 +61,13 @@ constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 constexpr int kSBufs = 3;
 constexpr int kMetas = 4;            // key tiles whose scales are in flight
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+// Registers a thread by role (setmaxnreg; five warpgroups of 96 at launch): the
+// softmax holds 64 scores, the converting warps two rows of codes.
+constexpr int kLaunchRegs = 96, kIssueRegs = 32, kSoftmaxRegs = 152, kConvertRegs = 72;
+static_assert(kIssueRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs <= 5 * kLaunchRegs,
+              "the roles' registers fit in what the block is launched with");
+static_assert(kThreads * kLaunchRegs <= 65536, "and those in an SM");
 constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
@@ -105,11 +112,13 @@ struct Params {
 };
 
 // What the softmax has to know of one key tile: by converting warp (32 keys), and
-// by key where a warp's keys are far apart.
+// by key where a warp's keys are far apart.  The K warps write kf, k_flags, key_kf
+// and qf, the V warps the rest.
 struct Meta {
   float kf[4];           // K base: 2^(base - 127 - kUp)
   float vb[4];           // V base: base - 127 - kUp, log2 units
-  uint32_t flags[4];     // 1: K by key, 2: V by key, 4: NaN in V
+  uint32_t k_flags[4];   // 1: K by key
+  uint32_t v_flags[4];   // 2: V by key, 4: NaN in V
   int32_t nan_pos[4][4]; // first key position with a NaN V group, by warp and group
   float key_kf[kKeys];
   float key_vb[kKeys];
@@ -210,12 +219,46 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_majo
   return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
-// The codes of one key's row, and the scale bytes of its groups in order.
+// The codes of one key's row, the scale bytes of its groups in order, and whether
+// the row is one (else all zeros, which no base follows).
 template <int D>
 struct KeyRow {
   uint4 c[D / 32];
   uint32_t e;
+  bool real;
 };
+
+template <int D, bool kIsV>
+__device__ __forceinline__ void load_row(KeyRow<D>& x, const uint8_t* cache, int id,
+                                         int64_t block_bytes, int h, int tk) {
+  x.e = 0u;
+  x.real = id >= 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) x.c[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (id < 0) return;
+  const uint8_t* chunk = cache + id * block_bytes + static_cast<int64_t>(h) * mx_chunk_bytes(D);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    x.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
+  if constexpr (kIsV) {
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w)
+      x.e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(
+                 chunk + mx_vscale_off<D>(tk, 2 * w)))) << (16 * w);
+  } else if constexpr (D == 128) {
+    x.e = __ldg(reinterpret_cast<const uint32_t*>(chunk + mx_scale_off(D)) + tk);
+  } else {
+    x.e = __ldg(reinterpret_cast<const uint16_t*>(chunk + mx_scale_off(D)) + tk);
+  }
+}
+
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // Eight codes times their group's scale, to one 16-byte piece of a tile row.
 __device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
@@ -270,8 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
     for (int b = 0; b < kNumBars; ++b) {
       uint32_t n = 1;
       if (b == kQFull || (b >= kKFull0 && b < kKFull0 + kKStages) ||
-          (b >= kVFull0 && b < kVFull0 + kVStages) || (b >= kMFull0 && b < kMFull0 + kMetas))
-        n = 4;  // converting warps
+          (b >= kVFull0 && b < kVFull0 + kVStages))
+        n = 4;  // the converting warps of K (Q too) or V
+      if (b >= kMFull0 && b < kMFull0 + kMetas) n = 8;  // all converting warps
       if ((b >= kPFull0 && b < kPFull0 + kSBufs) || (b >= kMFree0 && b < kMFree0 + kMetas))
         n = 8;  // softmax warps
       if (b >= kPair0 && b < kPair0 + 4) n = 2;  // the two warps sharing a quadrant
@@ -303,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp < 4) {
+    set_registers<kIssueRegs, false>();
   if (warp == 0) {
     // ============================ QK^T issuer ============================
     if (lane == 0) {
@@ -375,14 +421,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         }
       }
     }
+  }
   } else if (warp >= 12) {
     // ============================ converting warps ============================
-    const int cw = warp - 12;              // keys [32 cw, 32 cw + 32) of every key tile
+    set_registers<kConvertRegs, false>();
+    const bool is_v = warp >= 16;
+    const int cw = (warp - 12) & 3;        // keys [32 cw, 32 cw + 32) of every key tile
     const int key = cw * 32 + lane;
     const int64_t block_bytes = static_cast<int64_t>(p.hkv) * mx_chunk_bytes(D);
-    // where this thread's row starts in a K or V stage, and its swizzle
+    // where this thread's row starts in a stage, and its swizzle
     const uint32_t row_off = (key / 8) * NDH * 1024 + (key % 8) * 128;
-    const int sw = key % 8;
+    const int sw = key % 8, tk = key % kMxBlock;
     uint32_t count = 0, tiles = 0;
     bool ok = true;
     for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok;
@@ -402,51 +451,116 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         }
         return id;
       };
-      const int tk = key % kMxBlock;  // token within the block
-      auto load_k = [&](int id, KeyRow<D>& k) {
-        k.e = 0u;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) k.c[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (id < 0) return;
-        const uint8_t* chunk = p.key_cache + id * block_bytes + t.h * mx_chunk_bytes(D);
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          k.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
-        if constexpr (D == 128)
-          k.e = __ldg(reinterpret_cast<const uint32_t*>(chunk + mx_scale_off(D)) + tk);
-        else
-          k.e = __ldg(reinterpret_cast<const uint16_t*>(chunk + mx_scale_off(D)) + tk);
+      auto fetch = [&](KeyRow<D>& x, int id) {
+        if (is_v) load_row<D, true>(x, p.value_cache, id, block_bytes, t.h, tk);
+        else load_row<D, false>(x, p.key_cache, id, block_bytes, t.h, tk);
       };
-      auto load_v = [&](int id, KeyRow<D>& v) {
-        v.e = 0u;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) v.c[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (id < 0) return;
-        const uint8_t* chunk = p.value_cache + id * block_bytes + t.h * mx_chunk_bytes(D);
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          v.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w)
-          v.e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(
-                     chunk + mx_vscale_off<D>(tk, 2 * w)))) << (16 * w);
-      };
-      KeyRow<D> k, v;
-      int id = check_id(load_id(0), 0);
-      int next_id = load_id(1);
-      load_k(id, k);
-      load_v(id, v);
-
-      // ---- Q: thread t brings row t to f16 ----
+      // converts x, key tile j's row; afterwards y holds the next tile's
+      int id = check_id(load_id(0), 0), next_id = load_id(1);
       float qf = 0.f;
-      {
+      auto convert = [&](KeyRow<D>& x, KeyRow<D>& y, int j) {
+        const int id1 = check_id(next_id, j + 1);
+        next_id = load_id(j + 2);
+        fetch(y, id1);
+        // ---- base of the warp's 32 keys ----
+        const int mine = x.real ? largest_scale<D>(x.e) : -1;
+        int base = __reduce_max_sync(0xffffffffu, mine);
+        const int least = __reduce_min_sync(0xffffffffu, mine < 0 ? 1000 : mine);
+        if (base < 0) base = 127;
+        const bool wide = base - least > kWide;
+        const int ms = count % kMetas;
+        Meta& meta = metas[ms];
+        if (count >= kMetas) {
+          ok = warp_wait(&bars[kMFree0 + ms], (count / kMetas - 1) & 1, p.err, abort_flag);
+          if (!ok) return;
+        }
+        if (is_v) {
+          uint32_t nan = 0u;  // groups of this key that are NaN
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (x.real && ((x.e >> (8 * b)) & 0xffu) == 255u) nan |= 1u << b;
+          const bool any_nan = __any_sync(0xffffffffu, nan != 0u);
+          if (lane == 0) {
+            meta.vb[cw] = static_cast<float>(base - 127 - kUp);
+            meta.v_flags[cw] = (wide ? 2u : 0u) | (any_nan ? 4u : 0u);
+          }
+          if (wide) {
+            if (mine >= 0) base = mine;
+            meta.key_vb[key] = static_cast<float>(base - 127 - kUp);
+          }
+          if (any_nan) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const int first =
+                  __reduce_min_sync(0xffffffffu, (nan >> b) & 1u ? j * kKeys + key : 0x7fffffff);
+              if (lane == 0) meta.nan_pos[cw][b] = first;
+            }
+          }
+        } else {
+          if (lane == 0) {
+            meta.kf[cw] = pow2(base - 127 - kUp);
+            meta.k_flags[cw] = wide ? 1u : 0u;
+          }
+          if (wide) {
+            if (mine >= 0) base = mine;
+            meta.key_kf[key] = pow2(base - 127 - kUp);
+          }
+          if (j == 0) meta.qf[key] = qf;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
+
+        // ---- the row, to its stage ----
+        const int stages = is_v ? kVStages : kKStages;
+        const int st = count % stages;
+        if (count >= static_cast<uint32_t>(stages)) {
+          ok = warp_wait(&bars[(is_v ? kVEmpty0 : kKEmpty0) + st], (count / stages - 1) & 1, p.err,
+                         abort_flag);
+          if (!ok) return;
+        }
+        uint8_t* dst = smem + (is_v ? L::kV : L::kK) + st * L::kHalf + row_off;
+        uint32_t f[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int e = (x.e >> (8 * b)) & 0xff;
+          f[b] = e == 255 ? (is_v ? 0u : 0x7fff7fffu) : f16x2_pow2(e - base + kUp);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // K: a word is 8 dimensions.  head_dim 128: word e of piece i is (lane c =
+            // i, group e); 64: (c = 2i + e / 2, group e % 2).  V: the half-words of two
+            // words are 8 dimensions; 128: words (group / 2) of lane groups 2i and
+            // 2i + 1; 64: of lane groups 4i + 2 (e / 2) and + 1.
+            const int b = D == 128 ? e : e & 1;
+            const int c = D == 128 ? i : 2 * i + (e >> 1);
+            const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
+            const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
+            const uint32_t codes = is_v ? __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410) : w[e];
+            const int piece = 4 * b + c;  // dims 8 piece .. + 7
+            *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
+                convert8(codes, f[b]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[(is_v ? kVFull0 : kKFull0) + st]);
+        ++count;
+      };
+      KeyRow<D> even, odd;
+      fetch(even, id);
+
+      // ---- Q: thread t of the K warps brings row t to f16 ----
+      if (!is_v) {
         const int u = key / G;
         const bool real = u < t.ntok;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
             static_cast<int64_t>(t.h * G + (real ? key % G : 0)) * D);
         uint32_t mx = 0u;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = __ldg(src + i);
           mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
@@ -462,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         if (tiles > 0) ok = warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
         if (!ok) break;
         uint8_t* dst = smem + L::kQ + key * 128;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = __ldg(src + i);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -479,125 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kQFull]);
       }
-
-      for (int j = 0; j < t.nkt && ok; ++j, ++count) {
-        const bool real = id >= 0;  // else zeros, which no base follows
-        // ---- bases of the warp's 32 keys ----
-        const int km = real ? largest_scale<D>(k.e) : -1, vm = real ? largest_scale<D>(v.e) : -1;
-        int kb = __reduce_max_sync(0xffffffffu, km), vbase = __reduce_max_sync(0xffffffffu, vm);
-        const int kmin = __reduce_min_sync(0xffffffffu, km < 0 ? 1000 : km);
-        const int vmin = __reduce_min_sync(0xffffffffu, vm < 0 ? 1000 : vm);
-        if (kb < 0) kb = 127;
-        if (vbase < 0) vbase = 127;
-        const bool kwide = kb - kmin > kWide, vwide = vbase - vmin > kWide;
-        uint32_t nan = 0u;  // groups of this key's V that are NaN
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (real && ((v.e >> (8 * b)) & 0xffu) == 255u) nan |= 1u << b;
-        const bool any_nan = __any_sync(0xffffffffu, nan != 0u);
-        const int ms = count % kMetas;
-        Meta& meta = metas[ms];
-        if (count >= kMetas) {
-          ok = warp_wait(&bars[kMFree0 + ms], (count / kMetas - 1) & 1, p.err, abort_flag);
-          if (!ok) break;
-        }
-        if (lane == 0) {
-          meta.kf[cw] = pow2(kb - 127 - kUp);
-          meta.vb[cw] = static_cast<float>(vbase - 127 - kUp);
-          meta.flags[cw] = (kwide ? 1u : 0u) | (vwide ? 2u : 0u) | (any_nan ? 4u : 0u);
-        }
-        if (kwide || vwide) {
-          if (kwide && km >= 0) kb = km;
-          if (vwide && vm >= 0) vbase = vm;
-          meta.key_kf[key] = pow2(kb - 127 - kUp);
-          meta.key_vb[key] = static_cast<float>(vbase - 127 - kUp);
-        }
-        if (any_nan) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int first = __reduce_min_sync(0xffffffffu, (nan >> b) & 1u ? j * kKeys + key : 0x7fffffff);
-            if (lane == 0) meta.nan_pos[cw][b] = first;
-          }
-        }
-        if (j == 0) meta.qf[key] = qf;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
-
-        // ---- K ----
-        const int id1 = check_id(next_id, j + 1);
-        next_id = load_id(j + 2);
-        {
-          const int ks = count % kKStages;
-          if (count >= kKStages) {
-            ok = warp_wait(&bars[kKEmpty0 + ks], (count / kKStages - 1) & 1, p.err, abort_flag);
-            if (!ok) break;
-          }
-          uint8_t* dst = smem + L::kK + ks * L::kHalf + row_off;
-          uint32_t f[NB];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int e = (k.e >> (8 * b)) & 0xff;
-            f[b] = e == 255 ? 0x7fff7fffu : f16x2_pow2(e - kb + kUp);
-          }
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const uint32_t w[4] = {k.c[i].x, k.c[i].y, k.c[i].z, k.c[i].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              // head_dim 128: word x of piece i is (c = i, b = x); 64: (c = 2i + x / 2, b = x % 2)
-              const int c = D == 128 ? i : 2 * i + (x >> 1), b = D == 128 ? x : x & 1;
-              const int piece = 4 * b + c;  // dims 8 piece .. + 7
-              *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
-                  convert8(w[x], f[b]);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kKFull0 + ks]);
-        }
-        load_k(id1, k);
-
-        // ---- V ----
-        {
-          const int vs = count % kVStages;
-          if (count >= kVStages) {
-            ok = warp_wait(&bars[kVEmpty0 + vs], (count / kVStages - 1) & 1, p.err, abort_flag);
-            if (!ok) break;
-          }
-          uint8_t* dst = smem + L::kV + vs * L::kHalf + row_off;
-          uint32_t f[NB];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int e = (v.e >> (8 * b)) & 0xff;
-            f[b] = e == 255 ? 0u : f16x2_pow2(e - vbase + kUp);
-          }
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const uint32_t w[4] = {v.c[i].x, v.c[i].y, v.c[i].z, v.c[i].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              // the half-words of two words make 8 consecutive dimensions.  head_dim
-              // 128: words (b / 2) of lane groups 2i and 2i + 1; 64: of 4i + 2 (x / 2), + 1
-              const int b = D == 128 ? x : x & 1;
-              const int y = D == 128 ? i : 2 * i + (x >> 1);
-              const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (x >> 1)];
-              const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (x >> 1) + 1];
-              const uint32_t codes = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
-              const int piece = 4 * b + y;
-              *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
-                  convert8(codes, f[b]);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kVFull0 + vs]);
-        }
-        load_v(id1, v);
-        id = id1;
+      for (int j = 0; j < t.nkt && ok; j += 2) {
+        convert(even, odd, j);
+        if (ok && j + 1 < t.nkt) convert(odd, even, j + 1);
       }
     }
   } else if (warp >= 4) {
     // ============================ softmax warps ============================
+    set_registers<kSoftmaxRegs, true>();
     // Two warps share each 32-lane quadrant of tensor memory (the same 32 rows):
     // warp half h reads S columns [64 h, 64 h + 64), the keys of converting warps
     // 2h and 2h + 1.  They agree on the row maximum every key tile, so one O
@@ -640,7 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           vref = meta.vb[0];
         }
         float f[2], vb[2];
-        uint32_t flags = meta.flags[0] | meta.flags[1] | meta.flags[2] | meta.flags[3];
+        uint32_t flags = 0u;  // of anything rare in the key tile
+#pragma unroll
+        for (int c = 0; c < 4; ++c) flags |= meta.k_flags[c] | meta.v_flags[c];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           // never zero, for the masked scores' infinities
@@ -664,31 +669,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         float lw[2];  // what brings a weight with its V base back: 2^(vref - vb)
         lw[0] = pow2(static_cast<int>(vref - vb[0]));
         lw[1] = pow2(static_cast<int>(vref - vb[1]));
-        bool by_key[2] = {false, false};
+        uint32_t keyed = 0u;  // this warp's groups of 32 keys with bases by key
         if (flags != 0u) {
-          // rare: keys with bases of their own, NaN in V
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const uint32_t fl = meta.flags[2 * half + g];
-            if (fl & 3u) {
-              by_key[g] = true;
+            const bool by_k = meta.k_flags[2 * half + g] != 0u;
+            const bool by_v = (meta.v_flags[2 * half + g] & 2u) != 0u;
+            if (by_k || by_v) {
+              keyed |= 1u << g;
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
                 const int key = half * 64 + g * 32 + c;
-                float fk = qf * meta.key_kf[key];
+                float fk = by_k ? qf * meta.key_kf[key] : f[g];
                 fk = fk < 1.17549435e-38f ? 1.17549435e-38f : fk;
-                sv[32 * g + c] = fmaf(sv[32 * g + c], fk, meta.key_vb[key]);
+                sv[32 * g + c] = fmaf(sv[32 * g + c], fk, by_v ? meta.key_vb[key] : vb[g]);
               }
               f[g] = 1.f;
               vb[g] = 0.f;
             }
           }
-          if (flags & 4u)
-            for (int w = 0; w < 4; ++w)
-              if (meta.flags[w] & 4u)
+          for (int c = 0; c < 4; ++c)
+            if (meta.v_flags[c] & 4u)
 #pragma unroll
-                for (int g = 0; g < NB; ++g)
-                  if (meta.nan_pos[w][g] <= pos) nan_groups |= 1u << g;
+              for (int g = 0; g < NB; ++g)
+                if (meta.nan_pos[c][g] <= pos) nan_groups |= 1u << g;
         }
         // causal mask (only tiles reaching past the tile's first row) and max
         const int key0 = j * kKeys + half * 64;
@@ -742,6 +746,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
             tmem_wait_st();
           }
         }
+        if (keyed != 0u) {
+          // The weights from the scores themselves: with a small enough V scale P is 0.
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (!((keyed >> g) & 1u)) continue;
+            const bool by_v = (meta.v_flags[2 * half + g] & 2u) != 0u;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int key = half * 64 + g * 32 + c;
+              const float v = by_v ? meta.key_vb[key] : meta.vb[2 * half + g];
+              sum += exp2_approx(sv[32 * g + c] - v + (vref - m_used));
+            }
+            l += sum;
+            lw[g] = 0.f;  // and not again below
+          }
+        }
         // P = 2^(s f + vb - m_used) as f16 pairs over the first 32 of this
         // warp's 64 S columns
         uint32_t w[32];
@@ -750,22 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           const float2 f2 = make_float2(f[g], f[g]);
           const float2 c2 = make_float2(vb[g] - m_used, vb[g] - m_used);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          float by = 0.f;
-          const bool keyed = by_key[g];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 x = __ffma2_rn(make_float2(sv[32 * g + 2 * e], sv[32 * g + 2 * e + 1]), f2, c2);
             const float2 pe = make_float2(exp2_approx(x.x), exp2_approx(x.y));
             l2[e & 1] = __fadd2_rn(l2[e & 1], pe);
             w[16 * g + e] = pack_f16(pe.x, pe.y);
-            if (keyed) {
-              // the weight from the score itself: with a small enough V scale P is 0
-              const int key = half * 64 + g * 32 + 2 * e;
-              by += exp2_approx(sv[32 * g + 2 * e] - meta.key_vb[key] + (vref - m_used));
-              by += exp2_approx(sv[32 * g + 2 * e + 1] - meta.key_vb[key + 1] + (vref - m_used));
-            }
           }
-          l += keyed ? by : ((l2[0].x + l2[1].x) + (l2[0].y + l2[1].y)) * lw[g];
+          l = fmaf((l2[0].x + l2[1].x) + (l2[0].y + l2[1].y), lw[g], l);
         }
         tmem_st32(s_cols, w);
         tmem_wait_st();
