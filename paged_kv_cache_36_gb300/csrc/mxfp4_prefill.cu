@@ -114,7 +114,7 @@ struct Params {
 // What the softmax has to know of one key tile: by converting warp (32 keys), and
 // by key where a warp's keys are far apart.  The K warps write kf, k_flags, key_kf
 // and qf, the V warps the rest.
-struct Meta {
+struct alignas(16) Meta {
   float kf[4];           // K base: 2^(base - 127 - kUp)
   float vb[4];           // V base: base - 127 - kUp, log2 units
   uint32_t k_flags[4];   // 1: K by key
@@ -133,10 +133,11 @@ struct Layout {
   static constexpr uint32_t kK = kQ + kHalf;
   static constexpr uint32_t kV = kK + kKStages * kHalf;
   static constexpr uint32_t kBars = kV + kVStages * kHalf;
-  static constexpr uint32_t kXch = kBars + 8 * kNumBars;     // [2 parity][2 half][128 rows] floats
+  static constexpr uint32_t kXch = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [2 parity][2 half][128 rows] floats
   static constexpr uint32_t kMeta = kXch + 2 * 2 * 128 * 4;
   static constexpr uint32_t kMisc = kMeta + kMetas * sizeof(Meta);  // tensor memory slot, abort flag
   static constexpr uint32_t kPrefix = kMisc + 16;
+  static_assert(kMeta % alignof(Meta) == 0 && kBars % 8 == 0, "vector loads of Meta, and the barriers");
 };
 
 struct Tile {
@@ -199,10 +200,9 @@ __device__ __forceinline__ float pow2(int k) {
   return k < -149 ? 0.f : __uint_as_float(1u << (k + 149));
 }
 
-// 2^x as a pair of f16, gradually down to 2^-24, then 0.
-__device__ __forceinline__ uint32_t f16x2_pow2(int x) {
-  const uint32_t h = x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
-  return h * 0x00010001u;
+// 2^x as f16, gradually down to 2^-24, then 0.
+__device__ __forceinline__ uint32_t f16_pow2(int x) {
+  return x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -214,42 +214,43 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Like mbar_wait_or_abort, but the hardware may hold the warp for a while before
+// it answers "not yet", so that waiting warps leave the issue slots to the
+// others (they wake when the phase completes).
+__device__ __forceinline__ bool held_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                          volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  auto ready = [&]() {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(20000u)  // nanoseconds, at most
+        : "memory");
+    return done != 0;
+  };
+  if (ready()) return true;
+  const long long t0 = clock64();
+  while (!ready()) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(err, PKV_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool held_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               volatile int* abort) {
+  return __all_sync(0xffffffffu, held_wait(bar, parity, err, abort));
+}
+
 // Instruction descriptor of kind::f16 with f16 A and B, float32 D.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_major) {
   return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
-}
-
-// The codes of one key's row, the scale bytes of its groups in order, and whether
-// the row is one (else all zeros, which no base follows).
-template <int D>
-struct KeyRow {
-  uint4 c[D / 32];
-  uint32_t e;
-  bool real;
-};
-
-template <int D, bool kIsV>
-__device__ __forceinline__ void load_row(KeyRow<D>& x, const uint8_t* cache, int id,
-                                         int64_t block_bytes, int h, int tk) {
-  x.e = 0u;
-  x.real = id >= 0;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) x.c[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (id < 0) return;
-  const uint8_t* chunk = cache + id * block_bytes + static_cast<int64_t>(h) * mx_chunk_bytes(D);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    x.c[i] = __ldg(reinterpret_cast<const uint4*>(chunk + tk * (D / 2)) + i);
-  if constexpr (kIsV) {
-#pragma unroll
-    for (int w = 0; w < D / 64; ++w)
-      x.e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(
-                 chunk + mx_vscale_off<D>(tk, 2 * w)))) << (16 * w);
-  } else if constexpr (D == 128) {
-    x.e = __ldg(reinterpret_cast<const uint32_t*>(chunk + mx_scale_off(D)) + tk);
-  } else {
-    x.e = __ldg(reinterpret_cast<const uint16_t*>(chunk + mx_scale_off(D)) + tk);
-  }
 }
 
 template <int kRegs, bool kMore>
@@ -270,13 +271,234 @@ __device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
 // The largest scale byte of a row that is not NaN, or -1.
 template <int D>
 __device__ __forceinline__ int largest_scale(uint32_t e) {
-  int m = -1;
+  const uint32_t b0 = e & 0xffu, b1 = (e >> 8) & 0xffu, b2 = (e >> 16) & 0xffu, b3 = e >> 24;
+  const uint32_t m = D == 128 ? max(max(b0, b1), max(b2, b3)) : max(b0, b1);
+  if (m < 255u) return static_cast<int>(m);
+  int x = -1;
+  if (b0 != 255u) x = max(x, static_cast<int>(b0));
+  if (b1 != 255u) x = max(x, static_cast<int>(b1));
+  if (D == 128 && b2 != 255u) x = max(x, static_cast<int>(b2));
+  if (D == 128 && b3 != 255u) x = max(x, static_cast<int>(b3));
+  return x;
+}
+
+// The converting warps of K (and Q), or of V: warp cw of the four takes keys
+// [32 cw, 32 cw + 32) of every key tile.
+template <int D, bool kIsV>
+__device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, const int32_t* prefix,
+                                             int entries, int total, int tpt, int cw) {
+  using L = Layout<D>;
+  constexpr int NDH = L::NDH;
+  constexpr int NB = D / 32;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  Meta* metas = reinterpret_cast<Meta*>(smem + L::kMeta);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  const int lane = threadIdx.x & 31, cid = blockIdx.x, ncta = gridDim.x, G = p.group;
+  const int key = cw * 32 + lane;
+  const int64_t block_bytes = static_cast<int64_t>(p.hkv) * mx_chunk_bytes(D);
+  // where this thread's row starts in a stage, and its swizzle
+  const uint32_t row_off = (key / 8) * NDH * 1024 + (key % 8) * 128;
+  const int sw = key % 8, tk = key % kMxBlock;
+  uint32_t count = 0, tiles = 0;
+  bool ok = true;
+  for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok;
+       ct = cta_tile(++it, cid, ncta, total), ++tiles) {
+    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+    const Tile t = find_tile(ct, prefix, entries, p, tpt);
+    // This thread's block of the next key tile, and where a block's row of it is;
+    // `left` keys of the request from this thread's on (none: not a key, block 0
+    // is read and its factors are 0).
+    const int32_t* ids = p.block_table + static_cast<int64_t>(t.r) * p.bt_stride + key / kMxBlock;
+    int left = t.nkeys - key;
+    const uint8_t* head =
+        (kIsV ? p.value_cache : p.key_cache) + static_cast<int64_t>(t.h) * mx_chunk_bytes(D);
+    const uint8_t* codes_at = head + tk * (D / 2);
+    const uint8_t* scales_at = head + (kIsV ? mx_vscale_off<D>(tk, 0) : mx_scale_off(D) + tk * (D / 32));
+    auto load_id = [&](int ahead) -> int { return left > ahead * kKeys ? __ldg(ids + 8 * ahead) : 0; };
+    auto load_scales = [&](int id) -> uint32_t {
+      const uint8_t* at = scales_at + static_cast<uint32_t>(id) * static_cast<uint64_t>(block_bytes);
+      if constexpr (kIsV) {
+        uint32_t e = __ldg(reinterpret_cast<const uint16_t*>(at));
+        if constexpr (D == 128) e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(at + 4))) << 16;
+        return e;
+      } else if constexpr (D == 128) {
+        return __ldg(reinterpret_cast<const uint32_t*>(at));
+      } else {
+        return __ldg(reinterpret_cast<const uint16_t*>(at));
+      }
+    };
+    // id of a key tile this thread has a key in, checked; 0 where it is not in the pool
+    auto checked = [&](int id, int ahead, bool& real) -> int {
+      real = left > ahead * kKeys;
+      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.num_blocks)) {
+        atomicOr(p.err, PKV_ERR_BLOCK_ID);
+        real = false;
+        id = 0;
+      }
+      return id;
+    };
+    bool real, next_real = false;
+    int id = checked(load_id(0), 0, real), next_id = load_id(1);
+    const uint4* codes = reinterpret_cast<const uint4*>(
+        codes_at + static_cast<uint32_t>(id) * static_cast<uint64_t>(block_bytes));
+    uint4 c[NB];  // this key's codes: of the current tile, piece by piece replaced by the next's
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b) {
-    const int x = (e >> (8 * b)) & 0xff;
-    if (x != 255) m = max(m, x);
+    for (int i = 0; i < NB; ++i) c[i] = __ldg(codes + i);
+    uint32_t scales = load_scales(id), next_scales = 0u;
+    float qf = 0.f;
+
+    // ---- Q: thread t of the K warps brings row t to f16 ----
+    if constexpr (!kIsV) {
+      const int u = key / G;
+      const bool real = u < t.ntok;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
+          static_cast<int64_t>(t.h * G + (real ? key % G : 0)) * D);
+      uint32_t mx = 0u;
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = __ldg(src + i);
+        mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
+                         max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
+        mx = max(mx, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu),
+                         max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
+      }
+      // largest element to [2^14, 2^15); the scale's sign goes onto Q
+      const int ex = static_cast<int>(min(max(mx >> 7, 15u), 254u));
+      const float f = copysignf(pow2(141 - ex), p.scale_log2);
+      qf = fabsf(p.scale_log2) * pow2(ex - 141);
+      // the tile before is done with the buffer
+      if (tiles > 0) ok = held_warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
+      if (!ok) break;
+      uint8_t* dst = smem + L::kQ + key * 128;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = __ldg(src + i);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          y[c] = real ? pack_f16(__uint_as_float(w[c] << 16) * f,
+                                 __uint_as_float(w[c] & 0xffff0000u) * f)
+                      : 0u;
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * kRegion + (((i & 7) ^ sw) << 4)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kQFull]);
+    }
+    for (int j = 0; j < t.nkt && ok; ++j, ++count) {
+      // the next tile's block, its scales, and the block after it
+      next_id = checked(next_id, 1, next_real);
+      codes = reinterpret_cast<const uint4*>(
+          codes_at + static_cast<uint32_t>(next_id) * static_cast<uint64_t>(block_bytes));
+      next_scales = load_scales(next_id);
+      next_id = load_id(2);
+      // ---- base of the warp's 32 keys ----
+      const int mine = real ? largest_scale<D>(scales) : -1;
+      int base = __reduce_max_sync(0xffffffffu, mine);
+      const int least = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine));  // -1: largest
+      if (base < 0) base = 127;
+      const bool wide = least >= 0 && base - least > kWide;
+      const int ms = count % kMetas;
+      Meta& meta = metas[ms];
+      if (count >= kMetas) {
+        ok = held_warp_wait(&bars[kMFree0 + ms], (count / kMetas - 1) & 1, p.err, abort_flag);
+        if (!ok) break;
+      }
+      if constexpr (kIsV) {
+        // a byte of 255 among this key's scales?
+        const bool has_nan = real && ((~scales - 0x01010101u) & scales & 0x80808080u) != 0u;
+        const bool any_nan = __any_sync(0xffffffffu, has_nan);
+        if (lane == 0) {
+          meta.vb[cw] = static_cast<float>(base - 127 - kUp);
+          meta.v_flags[cw] = (wide ? 2u : 0u) | (any_nan ? 4u : 0u);
+        }
+        if (wide) {
+          if (mine >= 0) base = mine;
+          meta.key_vb[key] = static_cast<float>(base - 127 - kUp);
+        }
+        if (any_nan) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const bool nan = real && ((scales >> (8 * b)) & 0xffu) == 255u;
+            const int first = __reduce_min_sync(0xffffffffu, nan ? j * kKeys + key : 0x7fffffff);
+            if (lane == 0) meta.nan_pos[cw][b] = first;
+          }
+        }
+      } else {
+        if (lane == 0) {
+          meta.kf[cw] = pow2(base - 127 - kUp);
+          meta.k_flags[cw] = wide ? 1u : 0u;
+        }
+        if (wide) {
+          if (mine >= 0) base = mine;
+          meta.key_kf[key] = pow2(base - 127 - kUp);
+        }
+        if (j == 0) meta.qf[key] = qf;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
+
+      // ---- the row, to its stage ----
+      uint32_t f[NB];  // the groups' factors 2^(e - base + kUp), in both halves
+      // All scales in [base - 26, base + 5]: the exponent fields by arithmetic.  (A byte
+      // below by at most 223, or NaN's 255, leaves a tested bit set.)
+      const uint32_t low = static_cast<uint32_t>(max(base - 26, 0)) * 0x01010101u;
+      const uint32_t tested = D == 128 ? 0xe0e0e0e0u : 0x0000e0e0u;
+      if (((scales - low) & tested) == 0u && real && base <= 249) {
+        const uint32_t add = static_cast<uint32_t>((kUp + 15 - base) * 1024) * 0x00010001u;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          f[b] = __byte_perm(scales, 0u, 0x4040 + 0x0101 * b) * 1024u + add;
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int e = (scales >> (8 * b)) & 0xff;
+          f[b] = !real ? 0u : e == 255 ? (kIsV ? 0u : 0x7fff7fffu) : f16_pow2(e - base + kUp) * 0x00010001u;
+        }
+      }
+      constexpr int kStages = kIsV ? kVStages : kKStages;
+      const int st = count % kStages;
+      if (count >= kStages) {
+        ok = held_warp_wait(&bars[(kIsV ? kVEmpty0 : kKEmpty0) + st], (count / kStages - 1) & 1, p.err,
+                            abort_flag);
+        if (!ok) break;
+      }
+      uint8_t* dst = smem + (kIsV ? L::kV : L::kK) + st * L::kHalf + row_off;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // K: a word is 8 dimensions.  head_dim 128: word e of piece i is (lane c = i,
+          // group e); 64: (c = 2i + e / 2, group e % 2).  V: the half-words of two words
+          // are 8 dimensions; 128: words (group / 2) of lane groups 2i and 2i + 1; 64: of
+          // lane groups 4i + 2 (e / 2) and + 1.
+          const int b = D == 128 ? e : e & 1;
+          const int q = D == 128 ? i : 2 * i + (e >> 1);
+          uint32_t eight = w[e];
+          if constexpr (kIsV) {
+            const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
+            const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
+            eight = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
+          }
+          const int piece = 4 * b + q;  // dims 8 piece .. + 7
+          *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
+              convert8(eight, f[b]);
+        }
+        c[i] = __ldg(codes + i);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[(kIsV ? kVFull0 : kKFull0) + st]);
+      scales = next_scales;
+      real = next_real;
+      ids += 8;
+      left -= kKeys;
+    }
   }
-  return m;
 }
 
 }  // namespace
@@ -361,14 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok && !*abort_flag;
            ct = cta_tile(++it, cid, ncta, total)) {
         const Tile t = find_tile(ct, prefix, entries, p, tpt);
-        ok = mbar_wait_or_abort(&bars[kQFull], q_count & 1, p.err, abort_flag);
+        ok = held_wait(&bars[kQFull], q_count & 1, p.err, abort_flag);
         ++q_count;
         for (int j = 0; j < t.nkt && ok; ++j, ++count) {
           const int ks = count % kKStages, b = count % kSBufs;
-          ok = mbar_wait_or_abort(&bars[kKFull0 + ks], (count / kKStages) & 1, p.err, abort_flag);
+          ok = held_wait(&bars[kKFull0 + ks], (count / kKStages) & 1, p.err, abort_flag);
           // S/P buffer b is free once PV of the key tile that last used it is done
           if (ok && count >= kSBufs)
-            ok = mbar_wait_or_abort(&bars[kSFree0 + b], (count / kSBufs - 1) & 1, p.err, abort_flag);
+            ok = held_wait(&bars[kSFree0 + b], (count / kSBufs - 1) & 1, p.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = k_desc0 + ((ks * L::kHalf) >> 4);
@@ -398,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         const Tile t = find_tile(ct, prefix, entries, p, tpt);
         for (int j = 0; j < t.nkt && ok; ++j, ++count) {
           const int vs = count % kVStages, b = count % kSBufs;
-          ok = mbar_wait_or_abort(&bars[kPFull0 + b], (count / kSBufs) & 1, p.err, abort_flag) &&
-               mbar_wait_or_abort(&bars[kVFull0 + vs], (count / kVStages) & 1, p.err, abort_flag);
+          ok = held_wait(&bars[kPFull0 + b], (count / kSBufs) & 1, p.err, abort_flag) &&
+               held_wait(&bars[kVFull0 + vs], (count / kVStages) & 1, p.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = v_desc0 + ((vs * L::kHalf) >> 4);
@@ -422,182 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       }
     }
   }
-  } else if (warp >= 12) {
-    // ============================ converting warps ============================
+  } else if (warp >= 16) {
     set_registers<kConvertRegs, false>();
-    const bool is_v = warp >= 16;
-    const int cw = (warp - 12) & 3;        // keys [32 cw, 32 cw + 32) of every key tile
-    const int key = cw * 32 + lane;
-    const int64_t block_bytes = static_cast<int64_t>(p.hkv) * mx_chunk_bytes(D);
-    // where this thread's row starts in a stage, and its swizzle
-    const uint32_t row_off = (key / 8) * NDH * 1024 + (key % 8) * 128;
-    const int sw = key % 8, tk = key % kMxBlock;
-    uint32_t count = 0, tiles = 0;
-    bool ok = true;
-    for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok;
-         ct = cta_tile(++it, cid, ncta, total), ++tiles) {
-      if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const Tile t = find_tile(ct, prefix, entries, p, tpt);
-      const int32_t* row = p.block_table + static_cast<int64_t>(t.r) * p.bt_stride;
-      // this thread's block of key tile j, or -1 (behind the keys, or not in the pool)
-      auto load_id = [&](int j) -> int {
-        const int pos = j * kKeys + key;
-        return j < t.nkt && pos < t.nkeys ? __ldg(row + pos / kMxBlock) : -1;
-      };
-      auto check_id = [&](int id, int j) -> int {
-        if (j < t.nkt && j * kKeys + key < t.nkeys && (id < 0 || id >= p.num_blocks)) {
-          atomicOr(p.err, PKV_ERR_BLOCK_ID);
-          return -1;
-        }
-        return id;
-      };
-      auto fetch = [&](KeyRow<D>& x, int id) {
-        if (is_v) load_row<D, true>(x, p.value_cache, id, block_bytes, t.h, tk);
-        else load_row<D, false>(x, p.key_cache, id, block_bytes, t.h, tk);
-      };
-      // converts x, key tile j's row; afterwards y holds the next tile's
-      int id = check_id(load_id(0), 0), next_id = load_id(1);
-      float qf = 0.f;
-      auto convert = [&](KeyRow<D>& x, KeyRow<D>& y, int j) {
-        const int id1 = check_id(next_id, j + 1);
-        next_id = load_id(j + 2);
-        fetch(y, id1);
-        // ---- base of the warp's 32 keys ----
-        const int mine = x.real ? largest_scale<D>(x.e) : -1;
-        int base = __reduce_max_sync(0xffffffffu, mine);
-        const int least = __reduce_min_sync(0xffffffffu, mine < 0 ? 1000 : mine);
-        if (base < 0) base = 127;
-        const bool wide = base - least > kWide;
-        const int ms = count % kMetas;
-        Meta& meta = metas[ms];
-        if (count >= kMetas) {
-          ok = warp_wait(&bars[kMFree0 + ms], (count / kMetas - 1) & 1, p.err, abort_flag);
-          if (!ok) return;
-        }
-        if (is_v) {
-          uint32_t nan = 0u;  // groups of this key that are NaN
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            if (x.real && ((x.e >> (8 * b)) & 0xffu) == 255u) nan |= 1u << b;
-          const bool any_nan = __any_sync(0xffffffffu, nan != 0u);
-          if (lane == 0) {
-            meta.vb[cw] = static_cast<float>(base - 127 - kUp);
-            meta.v_flags[cw] = (wide ? 2u : 0u) | (any_nan ? 4u : 0u);
-          }
-          if (wide) {
-            if (mine >= 0) base = mine;
-            meta.key_vb[key] = static_cast<float>(base - 127 - kUp);
-          }
-          if (any_nan) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              const int first =
-                  __reduce_min_sync(0xffffffffu, (nan >> b) & 1u ? j * kKeys + key : 0x7fffffff);
-              if (lane == 0) meta.nan_pos[cw][b] = first;
-            }
-          }
-        } else {
-          if (lane == 0) {
-            meta.kf[cw] = pow2(base - 127 - kUp);
-            meta.k_flags[cw] = wide ? 1u : 0u;
-          }
-          if (wide) {
-            if (mine >= 0) base = mine;
-            meta.key_kf[key] = pow2(base - 127 - kUp);
-          }
-          if (j == 0) meta.qf[key] = qf;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
-
-        // ---- the row, to its stage ----
-        const int stages = is_v ? kVStages : kKStages;
-        const int st = count % stages;
-        if (count >= static_cast<uint32_t>(stages)) {
-          ok = warp_wait(&bars[(is_v ? kVEmpty0 : kKEmpty0) + st], (count / stages - 1) & 1, p.err,
-                         abort_flag);
-          if (!ok) return;
-        }
-        uint8_t* dst = smem + (is_v ? L::kV : L::kK) + st * L::kHalf + row_off;
-        uint32_t f[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int e = (x.e >> (8 * b)) & 0xff;
-          f[b] = e == 255 ? (is_v ? 0u : 0x7fff7fffu) : f16x2_pow2(e - base + kUp);
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // K: a word is 8 dimensions.  head_dim 128: word e of piece i is (lane c =
-            // i, group e); 64: (c = 2i + e / 2, group e % 2).  V: the half-words of two
-            // words are 8 dimensions; 128: words (group / 2) of lane groups 2i and
-            // 2i + 1; 64: of lane groups 4i + 2 (e / 2) and + 1.
-            const int b = D == 128 ? e : e & 1;
-            const int c = D == 128 ? i : 2 * i + (e >> 1);
-            const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
-            const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
-            const uint32_t codes = is_v ? __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410) : w[e];
-            const int piece = 4 * b + c;  // dims 8 piece .. + 7
-            *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
-                convert8(codes, f[b]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[(is_v ? kVFull0 : kKFull0) + st]);
-        ++count;
-      };
-      KeyRow<D> even, odd;
-      fetch(even, id);
-
-      // ---- Q: thread t of the K warps brings row t to f16 ----
-      if (!is_v) {
-        const int u = key / G;
-        const bool real = u < t.ntok;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
-            static_cast<int64_t>(t.h * G + (real ? key % G : 0)) * D);
-        uint32_t mx = 0u;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = __ldg(src + i);
-          mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
-                           max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
-          mx = max(mx, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu),
-                           max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
-        }
-        // largest element to [2^14, 2^15); the scale's sign goes onto Q
-        const int ex = static_cast<int>(min(max(mx >> 7, 15u), 254u));
-        const float f = copysignf(pow2(141 - ex), p.scale_log2);
-        qf = fabsf(p.scale_log2) * pow2(ex - 141);
-        // the tile before is done with the buffer
-        if (tiles > 0) ok = warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
-        if (!ok) break;
-        uint8_t* dst = smem + L::kQ + key * 128;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = __ldg(src + i);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            y[c] = real ? pack_f16(__uint_as_float(w[c] << 16) * f,
-                                   __uint_as_float(w[c] & 0xffff0000u) * f)
-                        : 0u;
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * kRegion + (((i & 7) ^ sw) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kQFull]);
-      }
-      for (int j = 0; j < t.nkt && ok; j += 2) {
-        convert(even, odd, j);
-        if (ok && j + 1 < t.nkt) convert(odd, even, j + 1);
-      }
-    }
+    convert_role<D, true>(p, smem, prefix, entries, total, tpt, warp - 16);
+  } else if (warp >= 12) {
+    set_registers<kConvertRegs, false>();
+    convert_role<D, false>(p, smem, prefix, entries, total, tpt, warp - 12);
   } else if (warp >= 4) {
     // ============================ softmax warps ============================
     set_registers<kSoftmaxRegs, true>();
@@ -617,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       slot[half * 128 + row] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_bar);
-      const bool done = warp_wait(pair_bar, pair_uses & 1, p.err, abort_flag);
+      const bool done = held_warp_wait(pair_bar, pair_uses & 1, p.err, abort_flag);
       ++pair_uses;
       return done ? slot[(half ^ 1) * 128 + row] : mine;
     };
@@ -633,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       bool ok = true;
       for (int j = 0; j < t.nkt && ok; ++j, ++count) {
         const int b = count % kSBufs, ms = count % kMetas;
-        if (!warp_wait(&bars[kMFull0 + ms], (count / kMetas) & 1, p.err, abort_flag)) {
+        if (!held_warp_wait(&bars[kMFull0 + ms], (count / kMetas) & 1, p.err, abort_flag)) {
           ok = false;
           break;
         }
@@ -643,9 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           vref = meta.vb[0];
         }
         float f[2], vb[2];
-        uint32_t flags = 0u;  // of anything rare in the key tile
-#pragma unroll
-        for (int c = 0; c < 4; ++c) flags |= meta.k_flags[c] | meta.v_flags[c];
+        const uint4 kfl = *reinterpret_cast<const uint4*>(meta.k_flags);
+        const uint4 vfl = *reinterpret_cast<const uint4*>(meta.v_flags);
+        const uint32_t flags =  // of anything rare in the key tile
+            kfl.x | kfl.y | kfl.z | kfl.w | vfl.x | vfl.y | vfl.z | vfl.w;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           // never zero, for the masked scores' infinities
@@ -653,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           f[g] = f[g] < 1.17549435e-38f ? 1.17549435e-38f : f[g];
           vb[g] = meta.vb[2 * half + g];
         }
-        if (!warp_wait(&bars[kSFull0 + b], (count / kSBufs) & 1, p.err, abort_flag)) {
+        if (!held_warp_wait(&bars[kSFull0 + b], (count / kSBufs) & 1, p.err, abort_flag)) {
           ok = false;
           break;
         }
@@ -670,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         lw[0] = pow2(static_cast<int>(vref - vb[0]));
         lw[1] = pow2(static_cast<int>(vref - vb[1]));
         uint32_t keyed = 0u;  // this warp's groups of 32 keys with bases by key
-        if (flags != 0u) {
+        if (__builtin_expect(flags != 0u, 0)) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const bool by_k = meta.k_flags[2 * half + g] != 0u;
@@ -725,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           if (__any_sync(0xffffffffu, grow)) {
             // O must hold PV of the previous key tile before it is rescaled
             const uint32_t prev = count - 1;
-            if (!warp_wait(&bars[kODone0 + prev % kSBufs], (prev / kSBufs) & 1, p.err, abort_flag)) {
+            if (!held_warp_wait(&bars[kODone0 + prev % kSBufs], (prev / kSBufs) & 1, p.err, abort_flag)) {
               ok = false;
               break;
             }
@@ -746,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
             tmem_wait_st();
           }
         }
-        if (keyed != 0u) {
+        if (__builtin_expect(keyed != 0u, 0)) {
           // The weights from the scores themselves: with a small enough V scale P is 0.
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -791,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       }
       if (!ok) break;
       // ---- epilogue: O 2^vref / (l_0 + l_1) -> out ----
-      if (!warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
+      if (!held_warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
       ++tiles_done;
       tc_fence_after();
       // (two factors: their product may be too small for a float)
