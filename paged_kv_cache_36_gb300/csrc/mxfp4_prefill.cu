@@ -467,28 +467,33 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
         if (!ok) break;
       }
       uint8_t* dst = smem + (kIsV ? L::kV : L::kK) + st * L::kHalf + row_off;
-#pragma unroll
+      // One piece of the row at a time, the next tile's taking its place behind the
+      // others: a short loop, because the roles' code shares the instruction cache
+      // (unrolled, the kernel took longer by a tenth).
+#pragma unroll 1
       for (int i = 0; i < NB; ++i) {
-        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        const uint32_t w[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+#pragma unroll
+        for (int e = 0; e < NB - 1; ++e) c[e] = c[e + 1];
+        c[NB - 1] = __ldg(codes + i);
+        // K: a word is 8 dimensions.  head_dim 128: word e is (lane c = i, group e); 64:
+        // (c = 2i + e / 2, group e % 2).  V: the half-words of two words are 8
+        // dimensions; 128: words (group / 2) of lane groups 2i and 2i + 1; 64: of lane
+        // groups 4i + 2 (e / 2) and + 1.
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // K: a word is 8 dimensions.  head_dim 128: word e of piece i is (lane c = i,
-          // group e); 64: (c = 2i + e / 2, group e % 2).  V: the half-words of two words
-          // are 8 dimensions; 128: words (group / 2) of lane groups 2i and 2i + 1; 64: of
-          // lane groups 4i + 2 (e / 2) and + 1.
           const int b = D == 128 ? e : e & 1;
-          const int q = D == 128 ? i : 2 * i + (e >> 1);
+          const int q = D == 128 ? i : 2 * i + (e >> 1);  // below 4
           uint32_t eight = w[e];
           if constexpr (kIsV) {
             const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
             const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
             eight = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
           }
-          const int piece = 4 * b + q;  // dims 8 piece .. + 7
-          *reinterpret_cast<uint4*>(dst + (piece >> 3) * 1024 + (((piece & 7) ^ sw) << 4)) =
-              convert8(eight, f[b]);
+          // dims 32 b + 8 q .. + 7: piece 4 b + q of the row
+          const uint32_t at = (static_cast<uint32_t>(q ^ sw) << 4) ^ ((b & 1) << 6);
+          *reinterpret_cast<uint4*>(dst + (b >> 1) * 1024 + at) = convert8(eight, f[b]);
         }
-        c[i] = __ldg(codes + i);
       }
       fence_proxy_async_smem();
       __syncwarp();
