@@ -9,6 +9,7 @@ built, importing the binding's entry points raises ImportError.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import numpy as np
@@ -277,8 +278,9 @@ def prepare_reshape_and_cache_paged_attention(key, value, slot_mapping, q, key_c
 # ---------------------------------------------------------------------------
 # the 4-bit paged cache and the device-built step metadata
 # ---------------------------------------------------------------------------
-# The checks below run on every call, beside launches of a few microseconds: they
-# compare device indices and dtype objects and make no temporary objects.
+# These calls launch kernels of a few microseconds, so the checks of each are one
+# expression of cheap comparisons (dtype objects, device indices), and what is
+# wrong is worked out by name only when something is.
 def _check_device(where: str, index: int, *tensors) -> None:
     """The tensors (None allowed) are on CUDA device `index`."""
     for t in tensors:
@@ -298,20 +300,29 @@ def _expect(where: str, name: str, t, dtype, shape) -> None:
         raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _device_call(where: str, fn, index: int, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current, on its current stream
-    if none is given."""
-    import torch
+_raw_stream = _current_device = None
+
+
+def _device_call(where: str, name: str, index: int, stream, *args) -> None:
+    """The library's function `name`(*args, stream) with the tensors' device
+    current, on its current stream if none is given."""
+    global _raw_stream, _current_device
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch._C._cuda_getDevice
     if stream is None:
-        ptr = torch._C._cuda_getCurrentRawStream(index)
+        ptr = _raw_stream(index)
     else:
         device = getattr(stream, "device", None)
         if device is not None and device.index != index:
             raise ValueError(f"{where}: the stream is on another device than the tensors")
         ptr = stream.cuda_stream
-    if index == torch._C._cuda_getDevice():
+    fn = getattr(_lib or lib(), name)
+    if index == _current_device():
         code = fn(*args, ptr)
     else:
+        import torch
         with torch.cuda.device(index):
             code = fn(*args, ptr)
     if code < 0:
@@ -320,8 +331,11 @@ def _device_call(where: str, fn, index: int, stream, *args) -> None:
 
 def _allocating_on(index: int, stream):
     """Context in which a call's own buffers are made: on its stream, so that
-    their memory is neither filled nor reused ahead of it."""
+    their memory is neither filled nor reused ahead of it.  (Host tensors, which
+    the call refuses by name, have index -1.)"""
     import torch
+    if index < 0:
+        return contextlib.nullcontext()
     if stream is not None:
         return torch.cuda.stream(stream)
     return torch.cuda.device(index)
@@ -344,34 +358,53 @@ def new_cache_mxfp4(num_blocks: int, num_kv_heads: int, head_dim: int, device="c
             torch.zeros(shape, dtype=torch.uint8, device=device))
 
 
-def _mxfp4_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int) -> int:
+def _check_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int) -> None:
     import torch
     if head_dim != 64 and head_dim != 128:
         raise ValueError(f"{where}: head_dim must be 64 or 128, not {head_dim}")
-    # 16 tokens of head_dim / 2 code bytes and head_dim / 32 scale bytes per KV head
-    shape = (key_cache.shape[0], num_kv_heads * head_dim * 17 // 2)
+    shape = (key_cache.shape[0], mxfp4_block_bytes(num_kv_heads, head_dim))
     _expect(where, "key_cache", key_cache, torch.uint8, shape)
     _expect(where, "value_cache", value_cache, torch.uint8, shape)
-    return shape[0]
+
+
+def _rows_and_pools(where: str, key, value, key_cache, value_cache, slot_mapping, error_word):
+    """(device index, T, num_blocks, Hkv, D, dtype code) of K and V rows [T, Hkv, D]
+    with their caches and slots."""
+    import torch
+    T, hkv, d = key.shape
+    nb = key_cache.shape[0]
+    # 16 tokens of head_dim / 2 code bytes and head_dim / 32 scale bytes per KV head
+    pool = (nb, hkv * d * 17 // 2)
+    dev = key.get_device()
+    u8, dtype = torch.uint8, key.dtype
+    if not (dev >= 0 and value.shape == key.shape and value.dtype is dtype
+            and key_cache.dtype is u8 and value_cache.dtype is u8
+            and key_cache.shape == pool and value_cache.shape == pool and (d == 64 or d == 128)
+            and key_cache.is_contiguous() and value_cache.is_contiguous()
+            and slot_mapping.dtype is torch.int64 and slot_mapping.shape == (T,)
+            and slot_mapping.is_contiguous()
+            and value.get_device() == dev == key_cache.get_device()
+            and value_cache.get_device() == dev == slot_mapping.get_device()
+            and (error_word is None or error_word.get_device() == dev)):
+        if value.shape != key.shape or value.dtype is not dtype:
+            raise ValueError(f"{where}: the K and the V rows must have one shape and dtype")
+        _check_pools(where, key_cache, value_cache, hkv, d)
+        _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
+        _check_device(where, dev, value, key_cache, value_cache, slot_mapping, error_word)
+    return dev, T, nb, hkv, d, PKV_BF16 if dtype is torch.bfloat16 else _dtype_code(key)
 
 
 def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, slot_mapping, error_word=None,
                             stream=None) -> None:
     """Quantise key/value [T, Hkv, D] (bfloat16 or float32) into the 4-bit caches
     (new_cache_mxfp4) at slot_mapping[T] (int64; negative: padding)."""
-    import torch
     where = "reshape_and_cache_mxfp4"
-    T, hkv, d = key.shape
-    if value.shape != key.shape or value.dtype != key.dtype:
-        raise ValueError(f"{where}: key and value must have one shape and dtype")
-    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
-    _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
-    dev = key.get_device()
-    _check_device(where, dev, value, key_cache, value_cache, slot_mapping, error_word)
-    _device_call(where, lib().pkv_reshape_and_cache_mxfp4, dev, stream, key.data_ptr(),
+    dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key, value, key_cache, value_cache,
+                                                slot_mapping, error_word)
+    _device_call(where, "pkv_reshape_and_cache_mxfp4", dev, stream, key.data_ptr(),
                  value.data_ptr(), _token_stride(key), _token_stride(value), key_cache.data_ptr(),
-                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d,
-                 _dtype_code(key), error_word.data_ptr() if error_word is not None else None)
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d, dtype,
+                 error_word.data_ptr() if error_word is not None else None)
 
 
 def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out, error_word=None,
@@ -379,20 +412,13 @@ def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out,
     """Read the rows at slot_mapping[T] (int64; negative: the row of the outputs
     is left alone) back from the 4-bit caches into key_out and value_out
     [T, Hkv, D], bfloat16 or float32; exact.  Returns (key_out, value_out)."""
-    import torch
     where = "gather_cache_mxfp4"
-    T, hkv, d = key_out.shape
-    if value_out.shape != key_out.shape or value_out.dtype != key_out.dtype:
-        raise ValueError(f"{where}: key_out and value_out must have one shape and dtype")
-    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, d)
-    _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
-    dev = key_out.get_device()
-    _check_device(where, dev, key_cache, value_cache, slot_mapping, value_out, error_word)
-    _device_call(where, lib().pkv_gather_cache_mxfp4, dev, stream, key_cache.data_ptr(),
+    dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key_out, value_out, key_cache, value_cache,
+                                                slot_mapping, error_word)
+    _device_call(where, "pkv_gather_cache_mxfp4", dev, stream, key_cache.data_ptr(),
                  value_cache.data_ptr(), slot_mapping.data_ptr(), key_out.data_ptr(),
                  value_out.data_ptr(), _token_stride(key_out), _token_stride(value_out), T, nb, 16,
-                 hkv, d, _dtype_code(key_out),
-                 error_word.data_ptr() if error_word is not None else None)
+                 hkv, d, dtype, error_word.data_ptr() if error_word is not None else None)
     return key_out, value_out
 
 
@@ -422,18 +448,33 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
     where = "paged_attention_varlen_mxfp4"
     T, H, D = q.shape
     hkv = max(1, key_cache.shape[1] * 2 // (17 * D))
-    nb = _mxfp4_pools(where, key_cache, value_cache, hkv, D)
-    if q.dtype is not torch.bfloat16:
-        raise TypeError(f"{where}: q must be bfloat16")
-    R = seq_lens.shape[0]
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
-    _expect(where, "query_start_loc", query_start_loc, torch.int32, (R + 1,))
-    _expect(where, "seq_lens", seq_lens, torch.int32, (R,))
-    _expect(where, "num_computed_tokens", num_computed_tokens, torch.int32, (R,))
+    nb, R = key_cache.shape[0], seq_lens.shape[0]
+    pool = (nb, hkv * D * 17 // 2)
     dev = q.get_device()
-    _check_device(where, dev, key_cache, value_cache, block_table, query_start_loc, seq_lens,
-                  num_computed_tokens, workspace, out)
+    u8, i32 = torch.uint8, torch.int32
+    if not (dev >= 0 and q.dtype is torch.bfloat16
+            and key_cache.dtype is u8 and value_cache.dtype is u8
+            and key_cache.shape == pool and value_cache.shape == pool and (D == 64 or D == 128)
+            and key_cache.is_contiguous() and value_cache.is_contiguous()
+            and block_table.dtype is i32 and block_table.dim() == 2 and block_table.shape[0] == R
+            and query_start_loc.dtype is i32 and query_start_loc.shape == (R + 1,)
+            and seq_lens.dtype is i32 and seq_lens.dim() == 1
+            and num_computed_tokens.dtype is i32 and num_computed_tokens.shape == (R,)
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous()
+            and num_computed_tokens.is_contiguous()
+            and key_cache.get_device() == dev == value_cache.get_device()
+            and block_table.get_device() == dev == query_start_loc.get_device()
+            and seq_lens.get_device() == dev == num_computed_tokens.get_device()):
+        _check_pools(where, key_cache, value_cache, hkv, D)
+        if q.dtype is not torch.bfloat16:
+            raise TypeError(f"{where}: q must be bfloat16")
+        if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != R:
+            raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
+        _expect(where, "query_start_loc", query_start_loc, i32, (R + 1,))
+        _expect(where, "seq_lens", seq_lens, i32, (R,))
+        _expect(where, "num_computed_tokens", num_computed_tokens, i32, (R,))
+        _check_device(where, dev, key_cache, value_cache, block_table, query_start_loc, seq_lens,
+                      num_computed_tokens)
     if out is None or workspace is None:
         with _allocating_on(dev, stream):
             if out is None:
@@ -442,9 +483,9 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
                 workspace = new_workspace_mxfp4(H, hkv, D, q.device)
     if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError(f"{where}: out must have q's shape and dtype")
-    if not workspace.is_contiguous():
-        raise ValueError(f"{where}: workspace must be contiguous")
-    _device_call(where, lib().pkv_paged_attention_varlen_mxfp4, dev, stream, q.data_ptr(),
+    if out.get_device() != dev or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{where}: out and a contiguous workspace must be on q's CUDA device")
+    _device_call(where, "pkv_paged_attention_varlen_mxfp4", dev, stream, q.data_ptr(),
                  _token_stride(q), key_cache.data_ptr(), value_cache.data_ptr(),
                  block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
                  query_start_loc.data_ptr(), seq_lens.data_ptr(), num_computed_tokens.data_ptr(),
@@ -470,21 +511,9 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
     where = "build_step_metadata"
     R, T = query_lens.shape[0], int(num_tokens)
     i32, i64 = torch.int32, torch.int64
-    _expect(where, "query_lens", query_lens, i32, (R,))
-    _expect(where, "num_computed_tokens", num_computed_tokens, i32, (R,))
-    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
-    if free_ring.dtype is not i32 or free_ring.dim() != 1 or not free_ring.is_contiguous():
-        raise ValueError(f"{where}: free_ring must be a contiguous int32 [ring size]")
-    _expect(where, "free_state", free_state, i64, (4,))
+    dev = query_lens.get_device()
     if free_state_out is None:
         free_state_out = free_state
-    elif free_state_out.dtype is not i64 or free_state_out.numel() < 2 or \
-            not free_state_out.is_contiguous():
-        raise ValueError(f"{where}: free_state_out must be int64 with at least 2 entries")
-    dev = query_lens.get_device()
-    _check_device(where, dev, num_computed_tokens, block_table, free_ring, free_state,
-                  free_state_out, query_start_loc, seq_lens, slot_mapping, positions, error_word)
     if query_start_loc is None or seq_lens is None or slot_mapping is None or positions is None:
         with _allocating_on(dev, stream):
             new = dict(device=query_lens.device)
@@ -496,11 +525,42 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
                 slot_mapping = torch.empty(T, dtype=i64, **new)
             if positions is None:
                 positions = torch.empty(T, dtype=i64, **new)
-    _expect(where, "query_start_loc", query_start_loc, i32, (R + 1,))
-    _expect(where, "seq_lens", seq_lens, i32, (R,))
-    _expect(where, "slot_mapping", slot_mapping, i64, (T,))
-    _expect(where, "positions", positions, i64, (T,))
-    _device_call(where, lib().pkv_build_step_metadata, dev, stream, query_lens.data_ptr(),
+    if not (dev >= 0 and query_lens.dtype is i32 and num_computed_tokens.dtype is i32
+            and block_table.dtype is i32 and free_ring.dtype is i32 and free_state.dtype is i64
+            and free_state_out.dtype is i64 and query_start_loc.dtype is i32
+            and seq_lens.dtype is i32 and slot_mapping.dtype is i64 and positions.dtype is i64
+            and query_lens.shape == (R,) == num_computed_tokens.shape == seq_lens.shape
+            and block_table.dim() == 2 and block_table.shape[0] == R and free_ring.dim() == 1
+            and free_state.shape == (4,) and free_state_out.numel() >= 2
+            and query_start_loc.shape == (R + 1,) and slot_mapping.shape == (T,) == positions.shape
+            and query_lens.is_contiguous() and num_computed_tokens.is_contiguous()
+            and free_ring.is_contiguous() and free_state.is_contiguous()
+            and free_state_out.is_contiguous() and query_start_loc.is_contiguous()
+            and seq_lens.is_contiguous() and slot_mapping.is_contiguous()
+            and positions.is_contiguous()
+            and num_computed_tokens.get_device() == dev == block_table.get_device()
+            and free_ring.get_device() == dev == free_state.get_device()
+            and free_state_out.get_device() == dev == query_start_loc.get_device()
+            and seq_lens.get_device() == dev == slot_mapping.get_device()
+            and positions.get_device() == dev
+            and (error_word is None or error_word.get_device() == dev)):
+        _expect(where, "query_lens", query_lens, i32, (R,))
+        _expect(where, "num_computed_tokens", num_computed_tokens, i32, (R,))
+        if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != R:
+            raise ValueError(f"{where}: block_table must be int32 [{R}, max_blocks]")
+        if free_ring.dtype is not i32 or free_ring.dim() != 1 or not free_ring.is_contiguous():
+            raise ValueError(f"{where}: free_ring must be a contiguous int32 [ring size]")
+        _expect(where, "free_state", free_state, i64, (4,))
+        if free_state_out.dtype is not i64 or free_state_out.numel() < 2 or \
+                not free_state_out.is_contiguous():
+            raise ValueError(f"{where}: free_state_out must be int64 with at least 2 entries")
+        _expect(where, "query_start_loc", query_start_loc, i32, (R + 1,))
+        _expect(where, "seq_lens", seq_lens, i32, (R,))
+        _expect(where, "slot_mapping", slot_mapping, i64, (T,))
+        _expect(where, "positions", positions, i64, (T,))
+        _check_device(where, dev, num_computed_tokens, block_table, free_ring, free_state,
+                      free_state_out, query_start_loc, seq_lens, slot_mapping, positions, error_word)
+    _device_call(where, "pkv_build_step_metadata", dev, stream, query_lens.data_ptr(),
                  num_computed_tokens.data_ptr(), R, block_table.data_ptr(),
                  _row_stride(block_table), block_table.shape[1], free_ring.data_ptr(),
                  free_ring.numel(),

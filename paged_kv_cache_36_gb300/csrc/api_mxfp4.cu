@@ -90,12 +90,6 @@ MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   return w;
 }
 
-int current_sms() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
-  return decode_grid_size(dev);
-}
-
 }  // namespace
 }  // namespace pkv
 
@@ -148,7 +142,7 @@ size_t pkv_mxfp4_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_hea
   if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       num_heads / num_kv_heads > kMaxGroup || (head_dim != 64 && head_dim != 128))
     return 0;
-  return mx_workspace(current_sms(), num_heads, num_kv_heads, head_dim).total;
+  return mx_workspace(current_sm_count(), num_heads, num_kv_heads, head_dim).total;
 }
 
 int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void* key_cache,
@@ -173,7 +167,7 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
     return fail(PKV_E_UNSUPPORTED, "%s: at most %d requests and 2^31 - 1 tokens", where,
                 step_metadata_max_reqs());
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
-  const int sms = current_sms();
+  const int sms = current_sm_count();
   const MxWorkspace w = mx_workspace(sms, num_heads, num_kv_heads, head_dim);
   if (workspace_bytes < w.total || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,

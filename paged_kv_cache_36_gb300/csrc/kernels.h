@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -27,6 +28,21 @@ cudaError_t raise_smem_limit_once(size_t bytes) {
                                        static_cast<int>(bytes));
   });
   return status[dev];
+}
+
+// SMs of the current device, looked up once per device (148 if that fails).
+inline int current_sm_count() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+      return 148;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
 }
 
 // Launches `kern` as a programmatic dependent of the kernel before it on

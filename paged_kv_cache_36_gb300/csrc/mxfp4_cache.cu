@@ -196,11 +196,8 @@ __global__ void __launch_bounds__(256) gather_cache_mxfp4_kernel(
 }
 
 unsigned token_grid(int64_t num_tokens) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t blocks = (num_tokens + 7) / 8;  // 8 warps, one token each
-  const int64_t cap = static_cast<int64_t>(sms) * 8;
+  const int64_t cap = static_cast<int64_t>(current_sm_count()) * 8;
   return static_cast<unsigned>(blocks < cap ? blocks : cap);
 }
 

@@ -188,9 +188,7 @@ cudaError_t launch_step_metadata(const StepMetadataArgs& a, cudaStream_t stream)
   const cudaError_t e =
       raise_smem_limit_once<step_metadata_kernel>(8 * static_cast<size_t>(step_metadata_max_reqs()));
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = current_sm_count();
   const int64_t items = a.num_tokens > a.num_reqs ? a.num_tokens : a.num_reqs;
   int64_t grid = (items + kThreads - 1) / kThreads;
   if (grid > sms) grid = sms;
