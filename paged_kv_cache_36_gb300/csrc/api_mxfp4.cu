@@ -185,7 +185,7 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   if (max_blocks_per_req <= 0 || (num_reqs > 1 && block_table_stride < max_blocks_per_req))
     return fail(PKV_E_INVALID, "%s: block_table rows of %d entries, %d apart", where,
                 max_blocks_per_req, block_table_stride);
-  if (static_cast<int64_t>(num_reqs) * max_blocks_per_req > 0x7fffffffLL)
+  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kMxRequestCost) > 0x7fffffffLL)
     return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
   AttnArgs a;
   a.q = q;

@@ -212,6 +212,10 @@ struct MxDecodeScratch {
   float* part_o;              // [slots][group][head_dim]
 };
 
+// What the change to a request costs a warp of the 4-bit decode, in blocks: the
+// partial written, the queries read, the first stage's scale bases.
+constexpr int kMxRequestCost = 3;
+
 // Slots of the 4-bit decode on a device of `sms` SMs.
 int64_t decode_mxfp4_slots(int sms, int num_kv_heads);
 

@@ -4,11 +4,15 @@
 //   out = sum_j softmax_j(scale <q, K_j>) V_j,
 // K and V the values that codes and power-of-two scales stand for (mxfp4.cuh).
 //
-// Work split.  The decode requests' blocks form one sequence of N blocks, cut
-// into Q ranges [qN/Q, (q+1)N/Q); a range is walked by one warp per KV head,
-// the warps of a range side by side in one CTA, so that every warp streams the
-// same bytes whatever the context lengths, no warp waits for another, and a
-// block's heads are fetched together.  A request that crosses ranges leaves one
+// Work split.  The decode requests' blocks form one sequence, cut into Q equal
+// ranges; a range is walked by one warp per KV head, the warps of a range side by
+// side in one CTA, so that every warp has the same work whatever the context
+// lengths, no warp waits for another, and a block's heads are fetched together.
+// Work is counted in units: a block is one, and the change to a request
+// kMxRequestCost, ahead of its blocks, so N = sum (blocks + kMxRequestCost) and
+// range q is the units [floor(qN/Q), floor((q+1)N/Q)).  (64 requests of some 2000
+// tokens, 8 KV heads of 128: counting blocks alone, warps with no change were
+// through after 31.5 us, those with one after 34.3, with two after 37.1.)  A request that crosses ranges leaves one
 // partial (m, l, o) per range and head in the workspace, and a second kernel
 // joins them,
 //   M = max_s m_s,  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
@@ -53,7 +57,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kMinBlocks = 8;    // blocks in a range at least (128 tokens)
+constexpr int kMinUnits = 8;     // units in a range, nearly: at least 4
 // Weights stay below 2^kMaxSlack (the running maximum moves when a score
 // exceeds it by more), and a V scale multiplies them by 2^(e - base + kLow) with
 // e - base in [0, 15]: at most 2^(3 + 12), inside f16, and at the window's lower
@@ -111,6 +115,9 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
                "n"(kDst), "n"(kSrc), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -163,17 +170,24 @@ __device__ __forceinline__ int slot_of(int q, bool starts_inside) {
   return 2 * q + (starts_inside ? 1 : 0);
 }
 
-// A position in a range: `run` blocks of request r to go, then `rest` more of
-// later requests.
+// A position in a range: `run` blocks of request r to go, then `rest` more units
+// of later requests.
 struct Cursor {
   int r, run, rest;
+  // the next request's part; run is 0 where the range ends before its blocks
   __device__ __forceinline__ void next_run(const int32_t* prefix) {
     do ++r; while (prefix[r + 1] == prefix[r]);
-    const int nb = prefix[r + 1] - prefix[r];
-    run = rest < nb ? rest : nb;
-    rest -= run;
+    const int units = prefix[r + 1] - prefix[r];
+    const int take = rest < units ? rest : units;
+    rest -= take;
+    run = take > kMxRequestCost ? take - kMxRequestCost : 0;
   }
 };
+
+// Unit where range q of Q begins, floor(q N / Q), from N / Q and N % Q.
+__device__ __forceinline__ int range_begin(int q, int Q, int quot, int rem) {
+  return q * quot + static_cast<int>(static_cast<uint32_t>(q * rem) / static_cast<uint32_t>(Q));
+}
 
 // base + a b, 64-bit.
 __device__ __forceinline__ const uint8_t* at_offset(const uint8_t* base, uint32_t a, uint32_t b) {
@@ -204,7 +218,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   const int gid = lane >> 2, tid = lane & 3;
   const int R = p.num_reqs;
 
-  // ---- plan: blocks of every decode request and their prefix sum ----
+  // ---- plan: units of every decode request and their prefix sum ----
   for (int r = threadIdx.x; r < R; r += blockDim.x) {
     const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
     const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         nb = 0;
       }
     }
-    prefix[r + 1] = nb;
+    prefix[r + 1] = nb > 0 ? nb + kMxRequestCost : 0;
   }
   __syncthreads();
   {
@@ -245,27 +259,34 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   }
   const int N = prefix[R];
   const int per_cta = ranges_per_cta(kWarps, p.hkv);
-  const int Q = min((N + kMinBlocks - 1) / kMinBlocks, static_cast<int>(gridDim.x) * per_cta);
+  const int Q = min((N + kMinUnits - 1) / kMinUnits, static_cast<int>(gridDim.x) * per_cta);
+  const int quot = N / max(Q, 1), rem = N % max(Q, 1);
   // what the join has to do for each request: its first range, and twice the
   // number of its ranges plus whether it starts inside the first; 0: nothing
-  for (int r = threadIdx.x * gridDim.x + blockIdx.x; r < R; r += blockDim.x * gridDim.x) {
-    const int run0 = prefix[r], run1 = prefix[r + 1];
-    int2 to_join = make_int2(0, 0);
-    if (run1 > run0) {
-      // the range of block x: the largest q with floor(qN/Q) <= x
-      const int qf = static_cast<int>(((static_cast<int64_t>(run0) + 1) * Q - 1) / N);
-      const int ql = static_cast<int>((static_cast<int64_t>(run1) * Q - 1) / N);
-      const bool inside = run0 > static_cast<int>(static_cast<int64_t>(qf) * N / Q);
-      if (ql > qf) to_join = make_int2(qf, 2 * (ql - qf + 1) + (inside ? 1 : 0));
+  auto write_plan = [&]() {
+    for (int r = threadIdx.x * gridDim.x + blockIdx.x; r < R; r += blockDim.x * gridDim.x) {
+      const int run0 = prefix[r], run1 = prefix[r + 1];
+      int2 to_join = make_int2(0, 0);
+      if (run1 > run0) {
+        // the range of unit x: the largest q with floor(qN/Q) <= x
+        auto range_of = [&](int x) {
+          return static_cast<int>(((static_cast<int64_t>(x) + 1) * Q - 1) / N);
+        };
+        const int qf = range_of(run0 + kMxRequestCost), ql = range_of(run1 - 1);
+        const bool inside = run0 > range_begin(qf, Q, quot, rem);
+        if (ql > qf) to_join = make_int2(qf, 2 * (ql - qf + 1) + (inside ? 1 : 0));
+      }
+      p.plan[r] = to_join;
     }
-    p.plan[r] = to_join;
-  }
+  };
   // few ranges: one per SM first
   const int sub = warp / p.hkv;
   const int me = sub * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-  if (sub >= per_cta || me >= Q) return;
-  const int u0 = static_cast<int>(static_cast<int64_t>(me) * N / Q);
-  const int u1 = static_cast<int>(static_cast<int64_t>(me + 1) * N / Q);
+  if (sub >= per_cta || me >= Q) {
+    write_plan();
+    return;
+  }
+  const int u0 = range_begin(me, Q, quot, rem), u1 = range_begin(me + 1, Q, quot, rem);
 
   // ---- the ring ----
   // A lane copies the same 16-byte pieces of every unit: NW of the K codes, NW
@@ -303,6 +324,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   Cursor next;
   const int32_t* row;
   uint32_t id0 = 0u, id1 = 0u;
+  int first_j;  // the block of its request that the run begins with
   {
     int lo = 0, hi = R;  // prefix[lo] <= u0 < prefix[hi]
     while (hi - lo > 1) {
@@ -310,9 +332,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
     next.r = lo;
-    next.run = min(u1, prefix[lo + 1]) - u0;
-    next.rest = u1 - u0 - next.run;
-    row = p.block_table + static_cast<int64_t>(lo) * p.bt_stride + (u0 - prefix[lo]);
+    // a range has more units than a request's cost: at least one block comes
+    const int end = min(u1, prefix[lo + 1]);
+    first_j = max(u0 - prefix[lo] - kMxRequestCost, 0);
+    next.run = end - prefix[lo] - kMxRequestCost - first_j;
+    next.rest = u1 - end;
+    row = p.block_table + static_cast<int64_t>(lo) * p.bt_stride + first_j;
   }
   Cursor at = next;
   auto load_ids = [&]() {
@@ -365,6 +390,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       if (next.run <= 0 && next.rest > 0) {
         next.next_run(prefix);
         row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride;
+        // its query heads are wanted two stages on
+        if (lane * 128 < 2 * G * D)
+          prefetch_l2(p.q + static_cast<int64_t>(__ldg(p.qsl + next.r)) * p.q_stride +
+                      static_cast<int64_t>(h * G) * D + lane * 64);
       }
       if (next.run > 0) load_ids();
     }
@@ -372,9 +401,9 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   };
   load_ids();
   for (int s = 0; s < stages - 1; ++s) fetch(s * kStage);
+  if (h < kWarps) write_plan();  // with the first bytes on their way
   uint32_t stage = 0;                          // the stage to compute on
   uint32_t refill = (stages - 1) * kStage;     // the one it takes the next fetch
-  int first_j = u0 - prefix[at.r];
   while (true) {
     // ======================= the range's part of one request =======================
     const int r = at.r;
@@ -799,7 +828,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         l[nt][cc] = x;
       }
     const bool inside = prefix[r] > u0;
-    const bool whole = prefix[r] >= u0 && prefix[r + 1] <= u1;
+    const bool whole = prefix[r] + kMxRequestCost >= u0 && prefix[r + 1] <= u1;
     const int64_t mine = static_cast<int64_t>(slot_of(me, inside)) * p.hkv + h;
     const int64_t tok = __ldg(p.qsl + r);
 #pragma unroll
@@ -829,23 +858,24 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       }
     if (at.rest == 0) break;
     at.next_run(prefix);
+    if (at.run == 0) break;
     first_j = 0;
   }
   // every copy of this pass has been waited for by its stage; none is in flight
   }
 }
 
-// Joins the partials of every request that crosses ranges.  Eight lanes take 32
-// dimensions of one (request, query head); the four eights of a warp take every
-// fourth range, kBatch loads of a lane in flight, and add up at the end.
-template <int D>
+// Joins the partials of every request that crosses ranges.  kLanes lanes take 4
+// kLanes dimensions of one (request, query head); the groups of a warp take the
+// ranges in turn, kBatch loads of a lane in flight, and add up at the end.
+template <int D, int kLanes>
 __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
   grid_dependency_wait();  // the decode's partials
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 4, kParts = 32 / kLanes, kItems = D / (4 * kLanes);
   const int G = p.group, H = p.hkv * G;
-  const int lane = threadIdx.x & 31, part = lane >> 3;
-  const int per_req = H * (D / 32);  // warps' items of a request
+  const int lane = threadIdx.x & 31, part = lane / kLanes;
+  const int per_req = H * kItems;  // warps' items of a request
   const int64_t total = static_cast<int64_t>(p.num_reqs) * per_req;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < total;
        i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
@@ -855,16 +885,16 @@ __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
     if (to_join.y == 0) continue;  // written by the decode itself, or no decode row
     const int splits = to_join.y >> 1;
     const bool inside = to_join.y & 1;
-    const int head = item / (D / 32), d4 = (item % (D / 32)) * 8 + (lane & 7);
+    const int head = item / kItems, d4 = (item % kItems) * kLanes + (lane & (kLanes - 1));
     const int h = head / G, g = head - h * G;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float big = -INFINITY, den = 0.f;
-    for (int k0 = part; k0 < splits; k0 += 4 * kBatch) {
+    for (int k0 = part; k0 < splits; k0 += kParts * kBatch) {
       float2 ml[kBatch];
       float4 x[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int q = k0 + 4 * k;
+        const int q = k0 + kParts * k;
         ml[k] = make_float2(-INFINITY, 0.f);
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (q < splits) {
@@ -886,7 +916,7 @@ __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
       acc.w *= keep;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (k0 + 4 * k >= splits) break;
+        if (k0 + kParts * k >= splits) break;
         const float w = ml[k].x == mx ? 1.f : exp2_approx(ml[k].x - mx);
         den = fmaf(ml[k].y, w, den);
         acc.x = fmaf(x[k].x, w, acc.x);
@@ -896,7 +926,7 @@ __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
       }
     }
 #pragma unroll
-    for (int x = 8; x < 32; x <<= 1) {
+    for (int x = kLanes; x < 32; x <<= 1) {
       const float mx = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
       const float w = big == mx ? 1.f : exp2_approx(big - mx);
       big = mx;
@@ -933,11 +963,17 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   e = launch_programmatic(decode_mxfp4_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
                           dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group * (D / 32);
-  int64_t grid = (items + 7) / 8;
-  if (grid > 8 * static_cast<int64_t>(sms)) grid = 8 * static_cast<int64_t>(sms);
-  return launch_programmatic(join_mxfp4_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
-                             stream, p);
+  // Few requests have many ranges each: eight lanes take 32 dimensions, four
+  // ranges at a time.  Where that is more than a wave of warps, a warp takes as
+  // many dimensions as it can.
+  const int64_t heads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group;
+  const int64_t wave = 32 * static_cast<int64_t>(sms);
+  constexpr int kWide = D / 4;
+  const bool narrow = heads * (D / 32) <= wave;
+  const int64_t grid = ((narrow ? heads * (D / 32) : heads) + 7) / 8;
+  return launch_programmatic(narrow ? join_mxfp4_kernel<D, 8> : join_mxfp4_kernel<D, kWide>,
+                             dim3(static_cast<unsigned>(grid < wave / 4 ? grid : wave / 4)),
+                             dim3(256), 0, stream, p);
 }
 
 }  // namespace
