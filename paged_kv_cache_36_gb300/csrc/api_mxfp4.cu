@@ -73,11 +73,15 @@ int cache_args(const char* where, const void* rows_k, const void* rows_v, int64_
 }
 
 struct MxWorkspace {
-  size_t plan, ml, o, total;
+  size_t plan, ml, o, image_base, images, total;
+  int32_t image_tiles;
 };
 
-// The error word's 256 bytes, then the decode's plan (for the largest batch)
-// and partials.
+// Room for the prefill's converted key tiles: 65408 tokens of 8 KV heads of 128.
+constexpr int64_t kImageRoom = 256 << 20;
+
+// The error word's 256 bytes, then the decode's plan (for the largest batch) and
+// partials, then the prefill's images and where each request has them.
 MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
   const size_t slots = static_cast<size_t>(decode_mxfp4_slots(sms, num_kv_heads));
   const size_t group = static_cast<size_t>(num_heads / num_kv_heads);
@@ -86,7 +90,11 @@ MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   w.plan = 256;
   w.ml = w.plan + up(static_cast<size_t>(step_metadata_max_reqs()) * 8);
   w.o = w.ml + up(slots * group * 8);
-  w.total = w.o + up(slots * group * head_dim * 4);
+  w.image_base = w.o + up(slots * group * head_dim * 4);
+  w.images = w.image_base + up(static_cast<size_t>(step_metadata_max_reqs() + 1) * 4);
+  const int64_t tile = prefill_mxfp4_image_bytes(num_kv_heads, head_dim);
+  w.image_tiles = static_cast<int32_t>(kImageRoom / tile);
+  w.total = w.images + static_cast<size_t>(w.image_tiles * tile);
   return w;
 }
 
@@ -216,7 +224,13 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
   ds.part_o = reinterpret_cast<float*>(ws + w.o);
   cudaError_t e = cudaSuccess;
-  if (max_query_len != 1) e = launch_prefill_mxfp4(a, sms, st);
+  if (max_query_len != 1) {
+    MxPrefillScratch ps;
+    ps.images = ws + w.images;
+    ps.image_base = reinterpret_cast<int32_t*>(ws + w.image_base);
+    ps.image_tiles = w.image_tiles;
+    e = launch_prefill_mxfp4(a, ps, max_query_len, sms, st);
+  }
   if (e == cudaSuccess) e = launch_decode_mxfp4(a, ds, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_mxfp4 launch");
   return validate_error_word(a.err, st, "paged_attention_varlen_mxfp4");

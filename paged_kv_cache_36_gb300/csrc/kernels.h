@@ -200,9 +200,21 @@ struct MxCacheArgs {
 cudaError_t launch_reshape_and_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 
+// Scratch of the 4-bit prefill: key tiles converted ahead of it.
+struct MxPrefillScratch {
+  uint8_t* images;
+  int32_t* image_base;        // [1 + num_reqs]
+  int32_t image_tiles;        // key tiles (of all KV heads) that images has room for
+};
+
+// Bytes of one key tile, all KV heads, in MxPrefillScratch::images.
+int64_t prefill_mxfp4_image_bytes(int num_kv_heads, int head_dim);
+
 // Chunked-prefill attention over the 4-bit cache (tcgen05) of the rows of
 // requests with query length > 1, on a device of `sms` SMs.
-cudaError_t launch_prefill_mxfp4(const AttnArgs& a, int sms, cudaStream_t stream);
+// `max_query_len` may be 0 (unknown).
+cudaError_t launch_prefill_mxfp4(const AttnArgs& a, const MxPrefillScratch& ws, int max_query_len,
+                                 int sms, cudaStream_t stream);
 
 // Scratch of the 4-bit decode: the plan that its join follows, and slots that
 // hold one range's partial of the query heads of one KV head.

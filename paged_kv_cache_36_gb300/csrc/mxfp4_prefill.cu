@@ -38,25 +38,14 @@
 // Q and K, warps 16-19 V.
 // Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that
 // stops all roles.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include <cstdint>
-
-#include "kernels.h"
-#include "mxfp4.cuh"
-#include "pkv_device.cuh"
-#include "prefill_common.cuh"
-#include "tcgen05.cuh"
+#include "mxfp4_prefill.cuh"
 
 namespace pkv {
 
+using namespace mxprefill;
+
 namespace {
 
-constexpr int kRows = 128;
-constexpr int kKeys = 128;
-constexpr uint32_t kRegion = 16384;  // 128 rows x 128 bytes
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 constexpr int kSBufs = 3;
@@ -68,14 +57,8 @@ constexpr int kLaunchRegs = 96, kIssueRegs = 32, kSoftmaxRegs = 152, kConvertReg
 static_assert(kIssueRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs <= 5 * kLaunchRegs,
               "the roles' registers fit in what the block is launched with");
 static_assert(kThreads * kLaunchRegs <= 65536, "and those in an SM");
-constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
-constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = kSBufs * kKeys;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kUp = 12;              // a base's scale becomes 2^kUp: 6 2^12 is inside f16
-constexpr int kWide = 14;            // binades between the keys of a warp before each has its base
-constexpr size_t kSmemLimit = 232448;
 
 enum Bar {
   kQFull, kQEmpty,
@@ -86,29 +69,6 @@ enum Bar {
   kOFinal = kODone0 + kSBufs, kPair0,
   kMFull0 = kPair0 + 4, kMFree0 = kMFull0 + kMetas,
   kNumBars = kMFree0 + kMetas
-};
-
-struct Params {
-  const __nv_bfloat16* q;
-  int64_t q_stride;
-  const uint8_t* key_cache;
-  const uint8_t* value_cache;
-  const int32_t* block_table;
-  int32_t bt_stride;
-  int32_t bt_width;
-  const int32_t* qsl;
-  const int32_t* seq_lens;
-  const int32_t* num_computed;
-  __nv_bfloat16* out;
-  int64_t out_stride;
-  int64_t num_tokens;
-  int32_t num_reqs;
-  int32_t num_blocks;
-  int32_t hkv;
-  int32_t group;
-  float scale_log2;
-  uint32_t* err;
-  int32_t entry_shift;  // requests per plan entry, as a power of two
 };
 
 // What the softmax has to know of one key tile: by converting warp (32 keys), and
@@ -140,148 +100,6 @@ struct Layout {
   static_assert(kMeta % alignof(Meta) == 0 && kBars % 8 == 0, "vector loads of Meta, and the barriers");
 };
 
-struct Tile {
-  int r, h, u0, ntok;
-  int nkeys;   // keys any of the tile's rows sees
-  int nkt;     // key tiles
-  int64_t qs;
-  int nc;
-};
-
-// Query tiles of request r (all KV heads); 0 where it has no rows here or its
-// metadata is wrong (*bad).
-__device__ __forceinline__ int request_tiles(const Params& p, int r, int tpt, bool* bad) {
-  const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
-  const int qlen = q1 - q0;
-  if (qlen <= 1) return 0;
-  const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
-  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || nc < 0 || nc > 0x7fffffff - qlen ||
-      seq != nc + qlen || (seq - 1) / kMxBlock >= p.bt_width) {
-    *bad = true;
-    return 0;
-  }
-  return (qlen + tpt - 1) / tpt * p.hkv;
-}
-
-// Tile `ct` -> (request, KV head, query rows).  prefix[i] counts the tiles before
-// plan entry i; within a request tiles run KV head fastest, then query tiles.
-__device__ __forceinline__ Tile find_tile(int ct, const int32_t* prefix, int entries,
-                                          const Params& p, int tpt) {
-  int lo = 0, hi = entries;  // prefix[lo] <= ct < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= ct) lo = mid; else hi = mid;
-  }
-  Tile t;
-  t.r = lo << p.entry_shift;
-  int rem = ct - prefix[lo];
-  if (p.entry_shift > 0) {  // an entry of several requests
-    bool bad = false;
-    for (int n = request_tiles(p, t.r, tpt, &bad); rem >= n; n = request_tiles(p, t.r, tpt, &bad)) {
-      rem -= n;
-      ++t.r;
-    }
-  }
-  const int qt = rem / p.hkv;
-  t.h = rem - qt * p.hkv;
-  t.qs = __ldg(p.qsl + t.r);
-  const int qlen = __ldg(p.qsl + t.r + 1) - static_cast<int>(t.qs);
-  t.nc = __ldg(p.num_computed + t.r);
-  t.u0 = qt * tpt;
-  t.ntok = min(tpt, qlen - t.u0);
-  t.nkeys = t.nc + t.u0 + t.ntok;
-  t.nkt = (t.nkeys + kKeys - 1) / kKeys;
-  return t;
-}
-
-// 2^k, subnormal or zero below 2^-126.
-__device__ __forceinline__ float pow2(int k) {
-  if (k >= -126) return __uint_as_float(static_cast<uint32_t>(min(k, 127) + 127) << 23);
-  return k < -149 ? 0.f : __uint_as_float(1u << (k + 149));
-}
-
-// 2^x as f16, gradually down to 2^-24, then 0.
-__device__ __forceinline__ uint32_t f16_pow2(int x) {
-  return x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Like mbar_wait_or_abort, but the hardware may hold the warp for a while before
-// it answers "not yet", so that waiting warps leave the issue slots to the
-// others (they wake when the phase completes).
-__device__ __forceinline__ bool held_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                          volatile int* abort) {
-  const uint32_t addr = smem_u32(bar);
-  auto ready = [&]() {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity), "r"(20000u)  // nanoseconds, at most
-        : "memory");
-    return done != 0;
-  };
-  if (ready()) return true;
-  const long long t0 = clock64();
-  while (!ready()) {
-    if (*abort) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      atomicOr(err, PKV_ERR_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool held_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                               volatile int* abort) {
-  return __all_sync(0xffffffffu, held_wait(bar, parity, err, abort));
-}
-
-// Instruction descriptor of kind::f16 with f16 A and B, float32 D.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_major) {
-  return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
-}
-
-template <int kRegs, bool kMore>
-__device__ __forceinline__ void set_registers() {
-  if constexpr (kMore)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// Eight codes times their group's scale, to one 16-byte piece of a tile row.
-__device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
-  uint32_t x[4];
-  e2m1x8_to_f16(w, x);
-  return make_uint4(mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f), mul_f16x2(x[3], f));
-}
-
-// The largest scale byte of a row that is not NaN, or -1.
-template <int D>
-__device__ __forceinline__ int largest_scale(uint32_t e) {
-  const uint32_t b0 = e & 0xffu, b1 = (e >> 8) & 0xffu, b2 = (e >> 16) & 0xffu, b3 = e >> 24;
-  const uint32_t m = D == 128 ? max(max(b0, b1), max(b2, b3)) : max(b0, b1);
-  if (m < 255u) return static_cast<int>(m);
-  int x = -1;
-  if (b0 != 255u) x = max(x, static_cast<int>(b0));
-  if (b1 != 255u) x = max(x, static_cast<int>(b1));
-  if (D == 128 && b2 != 255u) x = max(x, static_cast<int>(b2));
-  if (D == 128 && b3 != 255u) x = max(x, static_cast<int>(b3));
-  return x;
-}
-
 // The converting warps of K (and Q), or of V: warp cw of the four takes keys
 // [32 cw, 32 cw + 32) of every key tile.
 template <int D, bool kIsV>
@@ -293,7 +111,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   Meta* metas = reinterpret_cast<Meta*>(smem + L::kMeta);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  const int lane = threadIdx.x & 31, cid = blockIdx.x, ncta = gridDim.x, G = p.group;
+  const int lane = threadIdx.x & 31, cid = blockIdx.x, ncta = gridDim.x;
   const int key = cw * 32 + lane;
   const int64_t block_bytes = static_cast<int64_t>(p.hkv) * mx_chunk_bytes(D);
   // where this thread's row starts in a stage, and its swizzle
@@ -304,7 +122,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
   for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok;
        ct = cta_tile(++it, cid, ncta, total), ++tiles) {
     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-    const Tile t = find_tile(ct, prefix, entries, p, tpt);
+    const Tile t = find_tile<false>(ct, prefix, entries, p, tpt);
     // This thread's block of the next key tile, and where a block's row of it is;
     // `left` keys of the request from this thread's on (none: not a key, block 0
     // is read and its factors are 0).
@@ -316,16 +134,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
     const uint8_t* scales_at = head + (kIsV ? mx_vscale_off<D>(tk, 0) : mx_scale_off(D) + tk * (D / 32));
     auto load_id = [&](int ahead) -> int { return left > ahead * kKeys ? __ldg(ids + 8 * ahead) : 0; };
     auto load_scales = [&](int id) -> uint32_t {
-      const uint8_t* at = scales_at + static_cast<uint32_t>(id) * static_cast<uint64_t>(block_bytes);
-      if constexpr (kIsV) {
-        uint32_t e = __ldg(reinterpret_cast<const uint16_t*>(at));
-        if constexpr (D == 128) e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(at + 4))) << 16;
-        return e;
-      } else if constexpr (D == 128) {
-        return __ldg(reinterpret_cast<const uint32_t*>(at));
-      } else {
-        return __ldg(reinterpret_cast<const uint16_t*>(at));
-      }
+      return load_scale_bytes<D, kIsV>(scales_at + static_cast<uint32_t>(id) * static_cast<uint64_t>(block_bytes));
     };
     // id of a key tile this thread has a key in, checked; 0 where it is not in the pool
     auto checked = [&](int id, int ahead, bool& real) -> int {
@@ -338,7 +147,8 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
       return id;
     };
     bool real, next_real = false;
-    int id = checked(load_id(0), 0, real), next_id = load_id(1);
+    const int id = checked(load_id(0), 0, real);
+    int next_id = load_id(1);
     const uint4* codes = reinterpret_cast<const uint4*>(
         codes_at + static_cast<uint32_t>(id) * static_cast<uint64_t>(block_bytes));
     uint4 c[NB];  // this key's codes: of the current tile, piece by piece replaced by the next's
@@ -349,45 +159,18 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
 
     // ---- Q: thread t of the K warps brings row t to f16 ----
     if constexpr (!kIsV) {
-      const int u = key / G;
-      const bool real = u < t.ntok;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
-          static_cast<int64_t>(t.h * G + (real ? key % G : 0)) * D);
-      uint32_t mx = 0u;
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = __ldg(src + i);
-        mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
-                         max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
-        mx = max(mx, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu),
-                         max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
-      }
-      // largest element to [2^14, 2^15); the scale's sign goes onto Q
-      const int ex = static_cast<int>(min(max(mx >> 7, 15u), 254u));
-      const float f = copysignf(pow2(141 - ex), p.scale_log2);
-      qf = fabsf(p.scale_log2) * pow2(ex - 141);
       // the tile before is done with the buffer
-      if (tiles > 0) ok = held_warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
+      ok = convert_q_row<D>(p, t, key, smem + L::kQ, qf, [&]() {
+        return tiles == 0 || held_warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
+      });
       if (!ok) break;
-      uint8_t* dst = smem + L::kQ + key * 128;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = __ldg(src + i);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          y[c] = real ? pack_f16(__uint_as_float(w[c] << 16) * f,
-                                 __uint_as_float(w[c] & 0xffff0000u) * f)
-                      : 0u;
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * kRegion + (((i & 7) ^ sw) << 4)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kQFull]);
     }
+    constexpr int kStages = kIsV ? kVStages : kKStages;
+    constexpr int kFull0 = kIsV ? kVFull0 : kKFull0, kEmpty0 = kIsV ? kVEmpty0 : kKEmpty0;
+    constexpr uint32_t kTiles = kIsV ? L::kV : L::kK;
     for (int j = 0; j < t.nkt && ok; ++j, ++count) {
       // the next tile's block, its scales, and the block after it
       next_id = checked(next_id, 1, next_real);
@@ -397,10 +180,8 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
       next_id = load_id(2);
       // ---- base of the warp's 32 keys ----
       const int mine = real ? largest_scale<D>(scales) : -1;
-      int base = __reduce_max_sync(0xffffffffu, mine);
-      const int least = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine));  // -1: largest
-      if (base < 0) base = 127;
-      const bool wide = least >= 0 && base - least > kWide;
+      bool wide;
+      int base = common_base(mine, wide);
       const int ms = count % kMetas;
       Meta& meta = metas[ms];
       if (count >= kMetas) {
@@ -408,9 +189,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
         if (!ok) break;
       }
       if constexpr (kIsV) {
-        // a byte of 255 among this key's scales?
-        const bool has_nan = real && ((~scales - 0x01010101u) & scales & 0x80808080u) != 0u;
-        const bool any_nan = __any_sync(0xffffffffu, has_nan);
+        const bool any_nan = __any_sync(0xffffffffu, real && nan_scale(scales));
         if (lane == 0) {
           meta.vb[cw] = static_cast<float>(base - 127 - kUp);
           meta.v_flags[cw] = (wide ? 2u : 0u) | (any_nan ? 4u : 0u);
@@ -442,62 +221,28 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
       if (lane == 0) mbar_arrive(&bars[kMFull0 + ms]);
 
       // ---- the row, to its stage ----
-      uint32_t f[NB];  // the groups' factors 2^(e - base + kUp), in both halves
-      // All scales in [base - 26, base + 5]: the exponent fields by arithmetic.  (A byte
-      // below by at most 223, or NaN's 255, leaves a tested bit set.)
-      const uint32_t low = static_cast<uint32_t>(max(base - 26, 0)) * 0x01010101u;
-      const uint32_t tested = D == 128 ? 0xe0e0e0e0u : 0x0000e0e0u;
-      if (((scales - low) & tested) == 0u && real && base <= 249) {
-        const uint32_t add = static_cast<uint32_t>((kUp + 15 - base) * 1024) * 0x00010001u;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          f[b] = __byte_perm(scales, 0u, 0x4040 + 0x0101 * b) * 1024u + add;
-      } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int e = (scales >> (8 * b)) & 0xff;
-          f[b] = !real ? 0u : e == 255 ? (kIsV ? 0u : 0x7fff7fffu) : f16_pow2(e - base + kUp) * 0x00010001u;
-        }
-      }
-      constexpr int kStages = kIsV ? kVStages : kKStages;
+      uint32_t f[NB];
+      row_factors<D, kIsV>(scales, real, base, f);
       const int st = count % kStages;
       if (count >= kStages) {
-        ok = held_warp_wait(&bars[(kIsV ? kVEmpty0 : kKEmpty0) + st], (count / kStages - 1) & 1, p.err,
-                            abort_flag);
+        ok = held_warp_wait(&bars[kEmpty0 + st], (count / kStages - 1) & 1, p.err, abort_flag);
         if (!ok) break;
       }
-      uint8_t* dst = smem + (kIsV ? L::kV : L::kK) + st * L::kHalf + row_off;
+      uint8_t* dst = smem + kTiles + st * L::kHalf + row_off;
       // One piece of the row at a time, the next tile's taking its place behind the
       // others: a short loop, because the roles' code shares the instruction cache
       // (unrolled, the kernel took longer by a tenth).
 #pragma unroll 1
       for (int i = 0; i < NB; ++i) {
-        const uint32_t w[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+        const uint4 piece = c[0];
 #pragma unroll
         for (int e = 0; e < NB - 1; ++e) c[e] = c[e + 1];
         c[NB - 1] = __ldg(codes + i);
-        // K: a word is 8 dimensions.  head_dim 128: word e is (lane c = i, group e); 64:
-        // (c = 2i + e / 2, group e % 2).  V: the half-words of two words are 8
-        // dimensions; 128: words (group / 2) of lane groups 2i and 2i + 1; 64: of lane
-        // groups 4i + 2 (e / 2) and + 1.
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int b = D == 128 ? e : e & 1;
-          const int q = D == 128 ? i : 2 * i + (e >> 1);  // below 4
-          uint32_t eight = w[e];
-          if constexpr (kIsV) {
-            const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
-            const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
-            eight = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
-          }
-          // dims 32 b + 8 q .. + 7: piece 4 b + q of the row
-          const uint32_t at = (static_cast<uint32_t>(q ^ sw) << 4) ^ ((b & 1) << 6);
-          *reinterpret_cast<uint4*>(dst + (b >> 1) * 1024 + at) = convert8(eight, f[b]);
-        }
+        store_piece<D, kIsV>(dst, i, piece, f, sw);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[(kIsV ? kVFull0 : kKFull0) + st]);
+      if (lane == 0) mbar_arrive(&bars[kFull0 + st]);
       scales = next_scales;
       real = next_real;
       ids += 8;
@@ -525,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
   // the kernel before may write q, the cache, out or the metadata
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
+  if (p.images != nullptr && __ldcg(p.any_direct) == 0) return;  // images serve every row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.num_reqs;
   const int entries = (R + (1 << p.entry_shift) - 1) >> p.entry_shift;
@@ -555,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
     int n = 0;
     for (int k = 0; k < (1 << p.entry_shift); ++k) {
       const int r = (i << p.entry_shift) + k;
-      if (r < R) n += request_tiles(p, r, tpt, &bad);
+      if (r < R) n += own_tiles<false>(p, r, tpt, &bad);
     }
     prefix[i + 1] = n;
   }
@@ -587,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       bool ok = true;
       for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok && !*abort_flag;
            ct = cta_tile(++it, cid, ncta, total)) {
-        const Tile t = find_tile(ct, prefix, entries, p, tpt);
+        const Tile t = find_tile<false>(ct, prefix, entries, p, tpt);
         ok = held_wait(&bars[kQFull], q_count & 1, p.err, abort_flag);
         ++q_count;
         for (int j = 0; j < t.nkt && ok; ++j, ++count) {
@@ -622,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       bool ok = true;
       for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok && !*abort_flag;
            ct = cta_tile(++it, cid, ncta, total)) {
-        const Tile t = find_tile(ct, prefix, entries, p, tpt);
+        const Tile t = find_tile<false>(ct, prefix, entries, p, tpt);
         for (int j = 0; j < t.nkt && ok; ++j, ++count) {
           const int vs = count % kVStages, b = count % kSBufs;
           ok = held_wait(&bars[kPFull0 + b], (count / kSBufs) & 1, p.err, abort_flag) &&
@@ -681,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
     for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0;
          ct = cta_tile(++it, cid, ncta, total)) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const Tile t = find_tile(ct, prefix, entries, p, tpt);
+      const Tile t = find_tile<false>(ct, prefix, entries, p, tpt);
       const int u = row / G;
       const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
       const int pos_min = t.nc + t.u0;
@@ -916,30 +662,9 @@ static cudaError_t launch_prefill_t(Params p, int sms, cudaStream_t stream) {
                              smem, stream, p);
 }
 
-cudaError_t launch_prefill_mxfp4(const AttnArgs& a, int sms, cudaStream_t stream) {
-  Params p;
-  p.q = static_cast<const __nv_bfloat16*>(a.q);
-  p.q_stride = a.q_stride;
-  p.key_cache = static_cast<const uint8_t*>(a.key_cache);
-  p.value_cache = static_cast<const uint8_t*>(a.value_cache);
-  p.block_table = a.block_table;
-  p.bt_stride = a.bt_stride;
-  p.bt_width = a.bt_width;
-  p.qsl = a.qsl;
-  p.seq_lens = a.seq_lens;
-  p.num_computed = a.num_computed;
-  p.out = static_cast<__nv_bfloat16*>(a.out);
-  p.out_stride = a.out_stride;
-  p.num_tokens = a.num_tokens;
-  p.num_reqs = a.num_reqs;
-  p.num_blocks = static_cast<int32_t>(a.num_blocks);
-  p.hkv = a.num_kv_heads;
-  p.group = a.num_heads / a.num_kv_heads;
-  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  p.err = a.err;
-  p.entry_shift = 0;
-  if (a.head_dim == 128) return launch_prefill_t<128>(p, sms, stream);
-  if (a.head_dim == 64) return launch_prefill_t<64>(p, sms, stream);
+cudaError_t launch_prefill_mxfp4_direct(Params p, int head_dim, int sms, cudaStream_t stream) {
+  if (head_dim == 128) return launch_prefill_t<128>(p, sms, stream);
+  if (head_dim == 64) return launch_prefill_t<64>(p, sms, stream);
   return cudaErrorNotSupported;
 }
 

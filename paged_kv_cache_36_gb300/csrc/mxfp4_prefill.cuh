@@ -1,0 +1,346 @@
+// What the 4-bit prefill kernels share: query tiles and their plan, bounded waits that
+// leave the issue slots to others, and the conversion of cache rows to f16 tiles.
+//
+// Scales.  Keys that are converted together share a base exponent for K and one for
+// V: a value is code 2^(e - base + kUp) in f16, exact for scales down to 2^-26 of the
+// base's and then rounded at f16's 2^-25.  The softmax puts the bases back for free:
+// x = s f + (v - M), with f = 2^(K base) times the query's factor and v the V base in
+// log2 units, so that P carries 2^v, the running maximum M is one of s + v, and l sums
+// P 2^(vref - v).  Where those keys differ by more than 2^kWide (an outlier, perhaps
+// one that the row may not even see), every key gets a base of its own, and the softmax
+// a factor and an offset per column: no key's precision depends on another's.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "pkv_device.cuh"
+#include "prefill_common.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace mxprefill {
+
+constexpr int kRows = 128;
+constexpr int kKeys = 128;
+constexpr uint32_t kRegion = 16384;  // 128 rows x 128 bytes
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kUp = 12;              // a base's scale becomes 2^kUp: 6 2^12 is inside f16
+constexpr int kWide = 14;            // binades between keys before each has its base
+constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
+constexpr int kMaxKeys = 0x7fffff00;  // a whole key tile more is still an int
+constexpr int kImageQueryTiles = 4;  // query tiles of a request that has its key tiles converted ahead
+constexpr size_t kSmemLimit = 232448;
+
+struct Params {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const uint8_t* key_cache;
+  const uint8_t* value_cache;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  int32_t bt_width;
+  const int32_t* qsl;
+  const int32_t* seq_lens;
+  const int32_t* num_computed;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  int64_t num_tokens;
+  int32_t num_reqs;
+  int32_t num_blocks;
+  int32_t hkv;
+  int32_t group;
+  float scale_log2;
+  uint32_t* err;
+  int32_t entry_shift;  // requests per plan entry, as a power of two
+  // Key tiles converted ahead (null: none): request r's are images image_base[r] hkv
+  // on, its key tiles in order, KV head fastest; -1: none, its rows are the direct
+  // kernel's (*any_direct: whether there are such).
+  uint8_t* images;
+  int32_t* image_base;
+  int32_t* any_direct;
+  int32_t image_tiles;  // key tiles (of all KV heads) there is room for
+};
+
+struct Tile {
+  int r, h, u0, ntok;
+  int nkeys;   // keys any of the tile's rows sees
+  int nkt;     // key tiles
+  int64_t qs;
+  int nc;
+};
+
+// Query tiles of request r (all KV heads); 0 where it has no rows of length > 1 or its
+// metadata is wrong (*bad).
+__device__ __forceinline__ int request_tiles(const Params& p, int r, int tpt, bool* bad) {
+  const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
+  const int qlen = q1 - q0;
+  if (qlen <= 1) return 0;
+  const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || nc < 0 || nc > kMaxKeys - qlen ||
+      seq != nc + qlen || (seq - 1) / kMxBlock >= p.bt_width) {
+    *bad = true;
+    return 0;
+  }
+  return (qlen + tpt - 1) / tpt * p.hkv;
+}
+
+// The query tiles of request r that are computed from images (kImages), or directly.
+template <bool kImages>
+__device__ __forceinline__ int own_tiles(const Params& p, int r, int tpt, bool* bad) {
+  const int n = request_tiles(p, r, tpt, bad);
+  if (n == 0 || p.images == nullptr) return kImages ? 0 : n;
+  return (__ldcg(p.image_base + r) >= 0) == kImages ? n : 0;
+}
+
+// Tile `ct` -> (request, KV head, query rows).  prefix[i] counts the tiles before
+// plan entry i; within a request tiles run KV head fastest, then query tiles.
+template <bool kImages>
+__device__ __forceinline__ Tile find_tile(int ct, const int32_t* prefix, int entries,
+                                          const Params& p, int tpt) {
+  int lo = 0, hi = entries;  // prefix[lo] <= ct < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= ct) lo = mid; else hi = mid;
+  }
+  Tile t;
+  t.r = lo << p.entry_shift;
+  int rem = ct - prefix[lo];
+  if (p.entry_shift > 0) {  // an entry of several requests
+    bool bad = false;
+    for (int n = own_tiles<kImages>(p, t.r, tpt, &bad); rem >= n;
+         n = own_tiles<kImages>(p, t.r, tpt, &bad)) {
+      rem -= n;
+      ++t.r;
+    }
+  }
+  const int qt = rem / p.hkv;
+  t.h = rem - qt * p.hkv;
+  t.qs = __ldg(p.qsl + t.r);
+  const int qlen = __ldg(p.qsl + t.r + 1) - static_cast<int>(t.qs);
+  t.nc = __ldg(p.num_computed + t.r);
+  t.u0 = qt * tpt;
+  t.ntok = min(tpt, qlen - t.u0);
+  t.nkeys = t.nc + t.u0 + t.ntok;
+  t.nkt = (t.nkeys - 1) / kKeys + 1;
+  return t;
+}
+
+// 2^k, subnormal or zero below 2^-126.
+__device__ __forceinline__ float pow2(int k) {
+  if (k >= -126) return __uint_as_float(static_cast<uint32_t>(min(k, 127) + 127) << 23);
+  return k < -149 ? 0.f : __uint_as_float(1u << (k + 149));
+}
+
+// 2^x as f16, gradually down to 2^-24, then 0.
+__device__ __forceinline__ uint32_t f16_pow2(int x) {
+  return x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Like mbar_wait_or_abort, but the hardware may hold the warp for a while before
+// it answers "not yet", so that waiting warps leave the issue slots to the
+// others (they wake when the phase completes).
+__device__ __forceinline__ bool held_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                          volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  auto ready = [&]() {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(20000u)  // nanoseconds, at most
+        : "memory");
+    return done != 0;
+  };
+  if (ready()) return true;
+  const long long t0 = clock64();
+  while (!ready()) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(err, PKV_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool held_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               volatile int* abort) {
+  return __all_sync(0xffffffffu, held_wait(bar, parity, err, abort));
+}
+
+// Instruction descriptor of kind::f16 with f16 A and B, float32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_major) {
+  return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Eight codes times their group's scale, to one 16-byte piece of a tile row.
+__device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
+  uint32_t x[4];
+  e2m1x8_to_f16(w, x);
+  return make_uint4(mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f), mul_f16x2(x[3], f));
+}
+
+// The largest scale byte of a row that is not NaN, or -1.
+template <int D>
+__device__ __forceinline__ int largest_scale(uint32_t e) {
+  const uint32_t b0 = e & 0xffu, b1 = (e >> 8) & 0xffu, b2 = (e >> 16) & 0xffu, b3 = e >> 24;
+  const uint32_t m = D == 128 ? max(max(b0, b1), max(b2, b3)) : max(b0, b1);
+  if (m < 255u) return static_cast<int>(m);
+  int x = -1;
+  if (b0 != 255u) x = max(x, static_cast<int>(b0));
+  if (b1 != 255u) x = max(x, static_cast<int>(b1));
+  if (D == 128 && b2 != 255u) x = max(x, static_cast<int>(b2));
+  if (D == 128 && b3 != 255u) x = max(x, static_cast<int>(b3));
+  return x;
+}
+
+// The scale bytes of a row, group by group; `at` is its first group's.
+template <int D, bool kIsV>
+__device__ __forceinline__ uint32_t load_scale_bytes(const uint8_t* at) {
+  if constexpr (kIsV) {
+    uint32_t e = __ldg(reinterpret_cast<const uint16_t*>(at));
+    if constexpr (D == 128) e |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(at + 4))) << 16;
+    return e;
+  } else if constexpr (D == 128) {
+    return __ldg(reinterpret_cast<const uint32_t*>(at));
+  } else {
+    return __ldg(reinterpret_cast<const uint16_t*>(at));
+  }
+}
+
+// The groups' factors 2^(e - base + kUp) as f16, in both halves.
+template <int D, bool kIsV>
+__device__ __forceinline__ void row_factors(uint32_t scales, bool real, int base, uint32_t (&f)[D / 32]) {
+  // All scales in [base - 26, base + 5]: the exponent fields by arithmetic.  (A byte
+  // below by at most 223, or NaN's 255, leaves a tested bit set.)
+  const uint32_t low = static_cast<uint32_t>(max(base - 26, 0)) * 0x01010101u;
+  const uint32_t tested = D == 128 ? 0xe0e0e0e0u : 0x0000e0e0u;
+  if (((scales - low) & tested) == 0u && real && base <= 249) {
+    const uint32_t add = static_cast<uint32_t>((kUp + 15 - base) * 1024) * 0x00010001u;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+      f[b] = __byte_perm(scales, 0u, 0x4040 + 0x0101 * b) * 1024u + add;
+  } else {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+      const int e = (scales >> (8 * b)) & 0xff;
+      f[b] = !real ? 0u : e == 255 ? (kIsV ? 0u : 0x7fff7fffu) : f16_pow2(e - base + kUp) * 0x00010001u;
+    }
+  }
+}
+
+// The i-th 16 bytes of a row's codes times the groups' factors, to the row at dst of
+// a swizzled tile (sw: the row's index modulo 8).
+// K: a word is 8 dimensions.  head_dim 128: word e is (lane c = i, group e); 64: (c =
+// 2i + e / 2, group e % 2).  V: the half-words of two words are 8 dimensions; 128:
+// words (group / 2) of lane groups 2i and 2i + 1; 64: of lane groups 4i + 2 (e / 2)
+// and + 1.
+template <int D, bool kIsV>
+__device__ __forceinline__ void store_piece(uint8_t* dst, int i, const uint4& codes,
+                                            const uint32_t (&f)[D / 32], int sw) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int b = D == 128 ? e : e & 1;
+    const int q = D == 128 ? i : 2 * i + (e >> 1);  // below 4
+    uint32_t eight = w[e];
+    if constexpr (kIsV) {
+      const uint32_t lo = D == 128 ? w[b >> 1] : w[2 * (e >> 1)];
+      const uint32_t hi = D == 128 ? w[2 + (b >> 1)] : w[2 * (e >> 1) + 1];
+      eight = __byte_perm(lo, hi, (b & 1) ? 0x7632 : 0x5410);
+    }
+    // dims 32 b + 8 q .. + 7: piece 4 b + q of the row
+    const uint32_t at = (static_cast<uint32_t>(q ^ sw) << 4) ^ ((b & 1) << 6);
+    *reinterpret_cast<uint4*>(dst + (b >> 1) * 1024 + at) = convert8(eight, f[b]);
+  }
+}
+
+// The base exponent of a warp's 32 keys, `mine` being each lane's largest scale (-1:
+// none), and whether the keys are too far apart for one.
+__device__ __forceinline__ int common_base(int mine, bool& wide) {
+  const int base = __reduce_max_sync(0xffffffffu, mine);
+  const int least = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine));  // -1: largest
+  wide = least >= 0 && base - least > kWide;
+  return base < 0 ? 127 : base;
+}
+
+// A byte of 255 among a row's scales?
+__device__ __forceinline__ bool nan_scale(uint32_t scales) {
+  return ((~scales - 0x01010101u) & scales & 0x80808080u) != 0u;
+}
+
+// A row of Q (row `key` of the tile at dst_tile, one region of 128 bytes a row per 64
+// dimensions) brought to f16: its largest element to [2^14, 2^15), the scale's sign on
+// it; zeros where there is no row.  qf is what undoes that, times the scale in log2
+// units.  `ready` is waited with before the tile is written; false if it was.
+template <int D, typename F>
+__device__ __forceinline__ bool convert_q_row(const Params& p, const Tile& t, int row, uint8_t* q_tile,
+                                              float& qf, F&& ready) {
+  const int G = p.group, u = row / G, sw = row % 8;
+  const bool real = u < t.ntok;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
+      static_cast<int64_t>(t.h * G + (real ? row % G : 0)) * D);
+  uint32_t mx = 0u;
+#pragma unroll 8
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 x = __ldg(src + i);
+    mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
+                     max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
+    mx = max(mx, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu),
+                     max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
+  }
+  const int ex = static_cast<int>(min(max(mx >> 7, 15u), 254u));
+  const float f = copysignf(pow2(141 - ex), p.scale_log2);
+  qf = fabsf(p.scale_log2) * pow2(ex - 141);
+  if (!ready()) return false;
+  uint8_t* dst = q_tile + row * 128;
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 x = __ldg(src + i);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      y[c] = real ? pack_f16(__uint_as_float(w[c] << 16) * f,
+                             __uint_as_float(w[c] & 0xffff0000u) * f)
+                  : 0u;
+    *reinterpret_cast<uint4*>(dst + (i >> 3) * kRegion + (((i & 7) ^ sw) << 4)) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  return true;
+}
+
+}  // namespace mxprefill
+
+// The prefill without images; rows of requests that have images are left out.
+cudaError_t launch_prefill_mxfp4_direct(mxprefill::Params p, int head_dim, int sms, cudaStream_t stream);
+
+}  // namespace pkv
