@@ -463,13 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         }
         tc_fence_after();
         const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
-        float sv[64];
-        {
-          uint32_t (&r)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sv);
-          tmem_ld32(s_cols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-          tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-          tmem_wait_ld();
-        }
         float lw[2];  // what brings a weight with its V base back: 2^(vref - vb)
         lw[0] = pow2(static_cast<int>(vref - vb[0]));
         lw[1] = pow2(static_cast<int>(vref - vb[1]));
@@ -481,29 +474,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
             const bool by_v = (meta.v_flags[2 * half + g] & 2u) != 0u;
             if (by_k || by_v) {
               keyed |= 1u << g;
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const int key = half * 64 + g * 32 + c;
-                float fk = by_k ? qf * meta.key_kf[key] : f[g];
-                fk = fk < 1.17549435e-38f ? 1.17549435e-38f : fk;
-                sv[32 * g + c] = fmaf(sv[32 * g + c], fk, by_v ? meta.key_vb[key] : vb[g]);
-              }
+              const int key = half * 64 + g * 32;
+              scale_scores<32>(s_cols + 32 * g, qf, by_k ? meta.key_kf + key : nullptr, f[g],
+                               by_v ? meta.key_vb + key : nullptr, vb[g]);
               f[g] = 1.f;
               vb[g] = 0.f;
             }
           }
           for (int c = 0; c < 4; ++c)
             if (meta.v_flags[c] & 4u)
-#pragma unroll
               for (int g = 0; g < NB; ++g)
                 if (meta.nan_pos[c][g] <= pos) nan_groups |= 1u << g;
         }
-        // causal mask (only tiles reaching past the tile's first row) and max
+        // causal mask (only tiles reaching past the tile's first row)
         const int key0 = j * kKeys + half * 64;
-        if (key0 + 63 > pos_min) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (key0 + c > pos) sv[c] = -INFINITY;
+        if (key0 + 63 > pos_min) mask_scores(s_cols, pos_min + 1 - key0, pos + 1 - key0);
+        float sv[64];
+        {
+          uint32_t (&r)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sv);
+          tmem_ld32(s_cols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+          tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+          tmem_wait_ld();
         }
         float mg[2];
 #pragma unroll
@@ -537,17 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
             const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
             if (grow) m_used = mx;
             l *= alpha;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t r32[32];
-              tmem_ld32(o_cols + c * 32, r32);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                r32[e] = __float_as_uint(__uint_as_float(r32[e]) * alpha);
-              tmem_st32(o_cols + c * 32, r32);
-            }
-            tmem_wait_st();
+            rescale<D / 2>(o_cols, alpha);
           }
         }
         if (__builtin_expect(keyed != 0u, 0)) {
@@ -556,14 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           for (int g = 0; g < 2; ++g) {
             if (!((keyed >> g) & 1u)) continue;
             const bool by_v = (meta.v_flags[2 * half + g] & 2u) != 0u;
-            float sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int key = half * 64 + g * 32 + c;
-              const float v = by_v ? meta.key_vb[key] : meta.vb[2 * half + g];
-              sum += exp2_approx(sv[32 * g + c] - v + (vref - m_used));
-            }
-            l += sum;
+            l += sum_scores<32>(s_cols + 32 * g, by_v ? meta.key_vb + half * 64 + g * 32 : nullptr,
+                                meta.vb[2 * half + g], vref - m_used);
             lw[g] = 0.f;  // and not again below
           }
         }

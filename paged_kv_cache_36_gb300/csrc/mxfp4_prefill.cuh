@@ -296,6 +296,91 @@ __device__ __forceinline__ bool nan_scale(uint32_t scales) {
   return ((~scales - 0x01010101u) & scales & 0x80808080u) != 0u;
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// What only some key tiles need is done to the scores in tensor memory, in short loops:
+// unrolled over the registers, code that hardly ever runs took instruction cache from
+// the code that always does (a prompt of 4096 tokens: 177 us instead of 152).
+
+// Scores of N columns from `cols` on times a factor plus an offset by key: qf kf[c] (f
+// where kf is null) and kv[c] (v).
+template <int N>
+__device__ __forceinline__ void scale_scores(uint32_t cols, float qf, const float* kf, float f,
+                                             const float* kv, float v) {
+#pragma unroll 1
+  for (int c = 0; c < N; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(cols + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float fk = kf != nullptr ? qf * kf[c + e] : f;
+      fk = fk < 1.17549435e-38f ? 1.17549435e-38f : fk;
+      r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), fk, kv != nullptr ? kv[c + e] : v));
+    }
+    tmem_st8(cols + c, r);
+  }
+  tmem_wait_st();
+}
+
+// The sum of 2^(x - kv[c] + add) over N columns of such scores (v where kv is null).
+template <int N>
+__device__ __forceinline__ float sum_scores(uint32_t cols, const float* kv, float v, float add) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < N; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(cols + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      sum += exp2_approx(__uint_as_float(r[e]) - (kv != nullptr ? kv[c + e] : v) + add);
+  }
+  return sum;
+}
+
+// -inf into this row's columns from `visible` on, of 64; `first` is the smallest such
+// column of the warp's rows.
+__device__ __forceinline__ void mask_scores(uint32_t cols, int first, int visible) {
+#pragma unroll 1
+  for (int c = max(first, 0) & ~7; c < 64; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(cols + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= visible) r[e] = 0xff800000u;
+    tmem_st8(cols + c, r);
+  }
+  tmem_wait_st();
+}
+
+// Rescales N columns of O from `cols` on.
+template <int N>
+__device__ __forceinline__ void rescale(uint32_t cols, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < N; c += 32) {
+    uint32_t r32[32];
+    tmem_ld32(cols + c, r32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r32[e] = __float_as_uint(__uint_as_float(r32[e]) * alpha);
+    tmem_st32(cols + c, r32);
+  }
+  tmem_wait_st();
+}
+
 // A row of Q (row `key` of the tile at dst_tile, one region of 128 bytes a row per 64
 // dimensions) brought to f16: its largest element to [2^14, 2^15), the scale's sign on
 // it; zeros where there is no row.  qf is what undoes that, times the scale in log2

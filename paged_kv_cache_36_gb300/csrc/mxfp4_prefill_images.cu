@@ -355,35 +355,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
         }
         tc_fence_after();
         const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
+        if (__builtin_expect(flags != 0u, 0)) {
+          if (flags & 3u) {  // bases by key
+            scale_scores<64>(s_cols, qf, (flags & 1u) ? meta.key_kf + half * 64 : nullptr, f,
+                             (flags & 2u) ? meta.key_vb + half * 64 : nullptr, vb);
+            f = 1.f;
+            vb = 0.f;
+          }
+          if (flags & 4u)
+            for (int g = 0; g < NB; ++g)
+              if (meta.nan_pos[g] <= pos) nan_groups |= 1u << g;
+        }
+        // causal mask (only tiles reaching past the tile's first row)
+        const int key0 = j * kKeys + half * 64;
+        if (key0 + 63 > pos_min) mask_scores(s_cols, pos_min + 1 - key0, pos + 1 - key0);
         float sv[64];
         {
           uint32_t (&r)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sv);
           tmem_ld32(s_cols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
           tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
           tmem_wait_ld();
-        }
-        if (__builtin_expect(flags != 0u, 0)) {
-          if (flags & 3u) {  // bases by key
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              float fk = (flags & 1u) ? qf * meta.key_kf[half * 64 + c] : f;
-              fk = fk < 1.17549435e-38f ? 1.17549435e-38f : fk;
-              sv[c] = fmaf(sv[c], fk, (flags & 2u) ? meta.key_vb[half * 64 + c] : vb);
-            }
-            f = 1.f;
-            vb = 0.f;
-          }
-          if (flags & 4u)
-#pragma unroll
-            for (int g = 0; g < NB; ++g)
-              if (meta.nan_pos[g] <= pos) nan_groups |= 1u << g;
-        }
-        // causal mask (only tiles reaching past the tile's first row) and max
-        const int key0 = j * kKeys + half * 64;
-        if (key0 + 63 > pos_min) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (key0 + c > pos) sv[c] = -INFINITY;
         }
         // row max: four chains of three-input maxima
         float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
@@ -411,28 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
             const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
             if (grow) m_used = mx;
             l *= alpha;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t r32[32];
-              tmem_ld32(o_cols + c * 32, r32);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                r32[e] = __float_as_uint(__uint_as_float(r32[e]) * alpha);
-              tmem_st32(o_cols + c * 32, r32);
-            }
-            tmem_wait_st();
+            rescale<D / 2>(o_cols, alpha);
           }
         }
         if (__builtin_expect((flags & 3u) != 0u, 0)) {
           // The weights from the scores themselves: with a small enough V scale P is 0.
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float v = (flags & 2u) ? meta.key_vb[half * 64 + c] : __uint_as_float(head.y);
-            sum += exp2_approx(sv[c] - v + (vref - m_used));
-          }
-          l += sum;
+          l += sum_scores<64>(s_cols, (flags & 2u) ? meta.key_vb + half * 64 : nullptr,
+                              __uint_as_float(head.y), vref - m_used);
           lw = 0.f;  // and not again below
         }
         // P = 2^(s f + vb - m_used) as f16 pairs over the first 32 of this warp's 64 S
