@@ -422,11 +422,20 @@ int pkv_gather_cache_mxfp4(const void* key_cache, const void* value_cache,
  * ones are then not computed).  Rows of a request whose metadata fails the
  * checks (PKV_ERR_METADATA), and rows behind the last request, are left as
  * they were; a block id outside the pool reads as zeros (PKV_ERR_BLOCK_ID).
+ * A request with several query tokens has 2^31 - 256 keys at most.
  * Bytes of tokens past a request's end may hold anything.
  *
+ * Requests with many query tokens have their keys and values converted to f16
+ * once, in the workspace's last 256 MiB; what finds no room there (some 65000
+ * tokens of 8 KV heads of 128) is converted again for every 128 / G query
+ * tokens.  Both products take f16 with float32 sums: queries keep their 8 bits
+ * over 30 binades, a 4-bit value is exact unless its scale is 2^26 times below
+ * the largest of the keys around it, weights are rounded to 11 bits.
+ *
  * The workspace is pkv_mxfp4_attention_workspace_bytes() bytes whatever the
- * batch, zero-filled before its first use, word 0 the error word; two calls
- * that overlap on the GPU must not share one.  All arguments, the metadata
+ * batch (all but its last 256 MiB are needed), its first 256 bytes zero before
+ * its first use, word 0 the error word; two calls that overlap on the GPU must
+ * not share one.  All arguments, the metadata
  * among them, are read only after the work before the call on `stream`. */
 size_t pkv_mxfp4_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads,
                                            int32_t head_dim);

@@ -431,10 +431,14 @@ def mxfp4_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim:
 
 
 def new_workspace_mxfp4(num_heads: int, num_kv_heads: int, head_dim: int, device="cuda"):
-    """A zero-filled workspace of paged_attention_varlen_mxfp4, for any batch."""
+    """A workspace of paged_attention_varlen_mxfp4, for any batch.  All but its
+    last 256 MiB are needed: a shorter slice serves, with less room for what long
+    prompts convert ahead."""
     import torch
-    return torch.zeros(mxfp4_attention_workspace_bytes(num_heads, num_kv_heads, head_dim),
-                       dtype=torch.uint8, device=device)
+    ws = torch.empty(mxfp4_attention_workspace_bytes(num_heads, num_kv_heads, head_dim),
+                     dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the error word
+    return ws
 
 
 def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_start_loc, seq_lens,

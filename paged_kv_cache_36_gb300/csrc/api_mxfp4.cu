@@ -3,6 +3,7 @@
 // contract.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "api.h"
@@ -73,12 +74,11 @@ int cache_args(const char* where, const void* rows_k, const void* rows_v, int64_
 }
 
 struct MxWorkspace {
-  size_t plan, ml, o, image_base, images, total;
-  int32_t image_tiles;
+  size_t plan, ml, o, image_base, images, tile, total;
 };
 
 // Room for the prefill's converted key tiles: 65408 tokens of 8 KV heads of 128.
-constexpr int64_t kImageRoom = 256 << 20;
+constexpr size_t kImageRoom = 256u << 20;
 
 // The error word's 256 bytes, then the decode's plan (for the largest batch) and
 // partials, then the prefill's images and where each request has them.
@@ -92,9 +92,8 @@ MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   w.o = w.ml + up(slots * group * 8);
   w.image_base = w.o + up(slots * group * head_dim * 4);
   w.images = w.image_base + up(static_cast<size_t>(step_metadata_max_reqs() + 1) * 4);
-  const int64_t tile = prefill_mxfp4_image_bytes(num_kv_heads, head_dim);
-  w.image_tiles = static_cast<int32_t>(kImageRoom / tile);
-  w.total = w.images + static_cast<size_t>(w.image_tiles * tile);
+  w.tile = static_cast<size_t>(prefill_mxfp4_image_bytes(num_kv_heads, head_dim));
+  w.total = w.images + kImageRoom / w.tile * w.tile;
   return w;
 }
 
@@ -177,9 +176,9 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
   const int sms = current_sm_count();
   const MxWorkspace w = mx_workspace(sms, num_heads, num_kv_heads, head_dim);
-  if (workspace_bytes < w.total || !aligned16(workspace))
+  if (workspace_bytes < w.images || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,
-                workspace_bytes, w.total);
+                workspace_bytes, w.images);
   if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
   if (!q || !key_cache || !value_cache || !block_table || !query_start_loc || !seq_lens ||
       !num_computed_tokens || !out)
@@ -228,7 +227,7 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
     MxPrefillScratch ps;
     ps.images = ws + w.images;
     ps.image_base = reinterpret_cast<int32_t*>(ws + w.image_base);
-    ps.image_tiles = w.image_tiles;
+    ps.image_tiles = static_cast<int32_t>((std::min(workspace_bytes, w.total) - w.images) / w.tile);
     e = launch_prefill_mxfp4(a, ps, max_query_len, sms, st);
   }
   if (e == cudaSuccess) e = launch_decode_mxfp4(a, ds, sms, st);
