@@ -472,7 +472,8 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
  * and ever returned (0 <= head <= tail <= head + ring_size).  To return a block
  * write it at free_ring[tail % ring_size] and add one to tail.  free_state_out
  * may be free_state (then words 2 and 3 must be zero, and are left so) or
- * another int64 [2].
+ * another int64 [2].  Calls that share a ring follow one another on a
+ * stream, or are ordered by events.
  *
  * Nothing is taken and the step is an empty one (query_start_loc all zero,
  * seq_lens = T, every slot -1, every position 0, block_table and the ring's

@@ -451,7 +451,7 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
     import torch
     where = "paged_attention_varlen_mxfp4"
     T, H, D = q.shape
-    hkv = max(1, key_cache.shape[1] * 2 // (17 * D))
+    hkv = max(1, key_cache.shape[1] * 2 // (17 * max(1, D)))
     nb, R = key_cache.shape[0], seq_lens.shape[0]
     pool = (nb, hkv * D * 17 // 2)
     dev = q.get_device()
