@@ -1,43 +1,34 @@
-// Chunked-prefill attention over the 4-bit paged cache on the 5th-generation
-// tensor cores: rows of requests with query length > 1.
+// Chunked-prefill attention over the 4-bit paged cache on the 5th-generation tensor
+// cores, with the conversion of keys and values inside: rows of requests with query
+// length > 1 whose key tiles are not converted ahead (mxfp4_prefill_images.cu).
 //
-// For a query row at position p and KV head g, out = softmax_{j <= p}(scale
-// <q, K_j>) V_j with K, V the values that codes and power-of-two scales stand
-// for (mxfp4.cuh).
+// For a query row at position p and KV head g, out = softmax_{j <= p}(scale <q, K_j>)
+// V_j with K, V the values that codes and power-of-two scales stand for (mxfp4.cuh).
 //
-// Tiling is that of the bfloat16 prefill: 128 rows = floor(128 / G) query tokens
-// x the G query heads of a KV head against key tiles of 128, S = Q K^T and O += P
-// V as tcgen05 products, S and O in tensor memory, P written over S.  The operands
-// are f16, and the copies are made by four warps that convert:
-//   - Thread t of the four takes key t of every key tile, 64 code bytes of K and
-//     of V (head_dim 128): one conversion a pair, one f16x2 product by its
-//     group's scale, one 16-byte store per 8 dimensions, in the 128-byte
-//     swizzled layout that both operands read.  Codes of the next tile are
-//     loaded while this one is converted.
-//   - Scales.  A warp's 32 keys share a base exponent for K and one for V: a value
-//     is code 2^(e - base + 12) in f16, exact for scales down to 2^-26 of the
-//     base's and then rounded at f16's 2^-25.  The softmax puts the bases back
-//     for free: x = s f + (v - M), with f = 2^(K base) times the query's factor
-//     and v the V base in log2 units, so that P carries 2^v, the running
-//     maximum M is one of s + v, and l sums P 2^(vref - v).  Where the keys of
-//     the 32 differ by more than 2^14 (an outlier, perhaps one that the row may
-//     not even see), every key gets a base of its own, and the softmax a factor
-//     and an offset per column: no key's precision depends on another's.
+// Tiling is that of the bfloat16 prefill: 128 rows = floor(128 / G) query tokens x the G
+// query heads of a KV head against key tiles of 128, S = Q K^T and O += P V as tcgen05
+// products, S and O in tensor memory, P written over S.  The operands are f16, and the
+// copies are made by eight warps that convert:
+//   - Thread t of four warps takes key t of every key tile, 64 code bytes of K (the
+//     other four: of V; head_dim 128): one conversion a pair, one f16x2 product by its
+//     group's scale, one 16-byte store per 8 dimensions, in the 128-byte swizzled layout
+//     that both operands read.  Codes of the next tile are loaded while this one is
+//     converted.  Each warp's 32 keys share the base exponents of mxfp4_prefill.cuh.
 //   - Q is brought to f16 by a power of two per row, as in the decode.
-//   - A V group that is NaN is stored as zeros, and its position noted; a row at
-//     or behind it gets NaN in that group's dimensions.  (0 times NaN would
-//     poison the rows before it.)
+//   - A V group that is NaN is stored as zeros, and its position noted; a row at or
+//     behind it gets NaN in that group's dimensions.  (0 times NaN would poison the rows
+//     before it.)
 //
-// What bounds it: the softmax's exponentials and the conversion share the SM's
-// issue slots beside the tensor core; K and V come from L2 at a quarter of the
-// bytes.
+// What bounds it: the conversion, which runs again for every query tile and takes issue
+// slots and instruction cache from the softmax.  32 query and 8 KV heads of 128: 512
+// tokens 22.4 us, 2048 67 us, 4096 209 us; converted ahead 27, 62 and 152.
 //
-// Warp roles (20 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1
-// issues P V; warps 4-11 run the softmax and the epilogue, two per 32-lane quadrant
-// of tensor memory, each with half of the key tile's columns; warps 12-15 convert
-// Q and K, warps 16-19 V.
-// Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that
-// stops all roles.
+// Warp roles (20 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1 issues P
+// V; warps 4-11 run the softmax and the epilogue, two per 32-lane quadrant of tensor
+// memory, each with half of the key tile's columns; warps 12-15 convert Q and K, warps
+// 16-19 V.
+// Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that stops all
+// roles.
 #include "mxfp4_prefill.cuh"
 
 namespace pkv {
@@ -160,7 +151,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
     // ---- Q: thread t of the K warps brings row t to f16 ----
     if constexpr (!kIsV) {
       // the tile before is done with the buffer
-      ok = convert_q_row<D>(p, t, key, smem + L::kQ, qf, [&]() {
+      ok = convert_q_row<D, 8, 4>(p, t, key, smem + L::kQ, qf, [&]() {
         return tiles == 0 || held_warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag);
       });
       if (!ok) break;
@@ -270,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
   // the kernel before may write q, the cache, out or the metadata
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  if (p.images != nullptr && __ldcg(p.any_direct) == 0) return;  // images serve every row
+  if (p.images != nullptr && __ldcg(p.any) == 0) return;  // images serve every row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.num_reqs;
   const int entries = (R + (1 << p.entry_shift) - 1) >> p.entry_shift;

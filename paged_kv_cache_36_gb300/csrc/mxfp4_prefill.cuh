@@ -31,18 +31,20 @@ constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr uint32_t kRegion = 16384;  // 128 rows x 128 bytes
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kRescaleThreshold = 15.0f;  // log2 units: weights below 2^15 are inside f16
 constexpr int kUp = 12;              // a base's scale becomes 2^kUp: 6 2^12 is inside f16
 constexpr int kWide = 14;            // binades between keys before each has its base
 constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;  // a whole key tile more is still an int
-// Query tiles (of a KV head) from which on a request has its key tiles converted ahead.
-// The two kernels more cost 5 us where there is little to convert, and the conversion is
-// saved for every query tile but one: with 8 KV heads of 128 and 32 query heads, 256 new
-// tokens (8 query tiles) behind 0, 2048 and 16384 take 24.6, 39.4 and 151 us that way
-// and 19.7, 40.9 and 196 directly; 128 behind 0 and 4096 24.1 and 53.9, and 18.4 and
-// 60.5.
-constexpr int kImageQueryTiles = 8;
+// Query tiles (of a KV head) and key tiles from which on a request has its key tiles
+// converted ahead.  That saves the conversion for every query tile but one, and costs two
+// kernels more, which also run, for 5 us, where no request turns out to have enough.  32
+// query and 8 KV heads of 128: 128 new tokens (4 query tiles) behind 4096 take 54 us that
+// way and 61 directly, behind 32768 276 and 370; 512 behind 0, 2048 and 16384 take 27, 43
+// and 153 us and 22 (27 behind the two kernels), 43 and 197; 1024 and 2048 behind 0 take 36
+// and 62, and 32 (38) and 67.
+constexpr int kImageQueryTiles = 4;
+constexpr int kImageKeyTiles = 8;
 constexpr size_t kSmemLimit = 232448;
 
 struct Params {
@@ -68,10 +70,10 @@ struct Params {
   int32_t entry_shift;  // requests per plan entry, as a power of two
   // Key tiles converted ahead (null: none): request r's are images image_base[r] hkv
   // on, its key tiles in order, KV head fastest; -1: none, its rows are the direct
-  // kernel's (*any_direct: whether there are such).
+  // kernel's.  any[0]: whether there are such; any[1]: whether there are images.
   uint8_t* images;
   int32_t* image_base;
-  int32_t* any_direct;
+  int32_t* any;
   int32_t image_tiles;  // key tiles (of all KV heads) there is room for
 };
 
@@ -390,9 +392,11 @@ __device__ __forceinline__ void rescale(uint32_t cols, float alpha) {
 // A row of Q (row `key` of the tile at dst_tile, one region of 128 bytes a row per 64
 // dimensions) brought to f16: its largest element to [2^14, 2^15), the scale's sign on
 // it; zeros where there is no row.  qf is what undoes that, times the scale in log2
-// units.  `ready` is waited with before the tile is written; false if it gave up.  (Short
-// loops: unrolled, a prompt of 4096 tokens took 167 us instead of 162.)
-template <int D, typename F>
+// units.  `ready` is waited with before the tile is written; false if it gave up.  The
+// loops are unrolled kRead and kWrite times: a prompt of 4096 tokens takes 162 us with 2
+// and 1 over images, where the warps have time and 8 and 4 cost 167; directly, where
+// they convert K besides, 227 with 2 and 1 and 213 with 8 and 4.
+template <int D, int kRead, int kWrite, typename F>
 __device__ __forceinline__ bool convert_q_row(const Params& p, const Tile& t, int row, uint8_t* q_tile,
                                               float& qf, F&& ready) {
   const int G = p.group, u = row / G, sw = row % 8;
@@ -401,7 +405,7 @@ __device__ __forceinline__ bool convert_q_row(const Params& p, const Tile& t, in
       p.q + (t.qs + t.u0 + (real ? u : 0)) * p.q_stride +
       static_cast<int64_t>(t.h * G + (real ? row % G : 0)) * D);
   uint32_t mx = 0u;
-#pragma unroll 2
+#pragma unroll kRead
   for (int i = 0; i < D / 8; ++i) {
     const uint4 x = __ldg(src + i);
     mx = max(mx, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu),
@@ -414,7 +418,7 @@ __device__ __forceinline__ bool convert_q_row(const Params& p, const Tile& t, in
   qf = fabsf(p.scale_log2) * pow2(ex - 141);
   if (!ready()) return false;
   uint8_t* dst = q_tile + row * 128;
-#pragma unroll 1
+#pragma unroll kWrite
   for (int i = 0; i < D / 8; ++i) {
     const uint4 x = __ldg(src + i);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};

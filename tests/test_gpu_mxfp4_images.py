@@ -1,6 +1,6 @@
 """GPU tests of the 4-bit prefill over key tiles that are converted ahead (requests
-of at least 8 query tiles of 128 / G tokens), within the bound of
-tests/mxfp4_support.py: its arithmetic is the direct kernel's, with bases of 128
+of at least 4 query tiles of 128 / G tokens and 8 key tiles of 128), within the bound
+of tests/mxfp4_support.py: its arithmetic is the direct kernel's, with bases of 128
 keys instead of 32."""
 
 import numpy as np
@@ -29,15 +29,16 @@ def _attend(s, **kw):
 
 
 @pytest.mark.parametrize("reqs, heads, hkv, d", [
-    # 16 query heads a KV head: 8 tokens a query tile, images from 57 tokens on
-    ([(57, 0)], 16, 1, 64),
-    ([(57, 71)], 16, 1, 128),                     # ends with a key tile
-    ([(64, 65)], 32, 2, 128),                     # one key into the second
-    ([(56, 300), (57, 300)], 16, 1, 64),          # one on each side of the rule
-    ([(1, 40), (70, 200), (0, 3), (9, 100), (120, 0), (1, 500), (2, 2)], 32, 2, 64),
-    ([(90, 900), (130, 1)], 16, 1, 128),
-    ([(230, 10)], 12, 3, 128),                    # 4 a KV head
-    ([(160, 333)], 28, 4, 64),                    # 7, tiles of 18 tokens
+    # 16 query heads a KV head: 8 tokens a query tile, images from 25 tokens and 897 keys on
+    ([(25, 872)], 16, 1, 64),
+    ([(57, 967)], 16, 1, 128),                    # ends with a key tile
+    ([(64, 961)], 32, 2, 128),                    # one key into the next
+    ([(24, 1300), (25, 1300)], 16, 1, 64),        # one on each side of the rule
+    ([(30, 866), (30, 867)], 16, 1, 128),         # and of the other
+    ([(1, 40), (70, 900), (0, 3), (9, 100), (920, 0), (1, 500), (2, 2)], 32, 2, 64),
+    ([(90, 1900), (30, 0), (130, 901)], 16, 1, 128),
+    ([(230, 710)], 12, 3, 128),                   # 4 a KV head
+    ([(160, 933)], 28, 4, 64),                    # 7, tiles of 18 tokens
     ([(1000, 24)], 2, 2, 64),                     # one: 128 tokens a tile
 ])
 def test_attention(reqs, heads, hkv, d):
@@ -50,17 +51,17 @@ def test_attention(reqs, heads, hkv, d):
 def test_scales_over_many_binades(lo, hi, what):
     if what == "keys" and hi > 12:
         lo, hi = lo // 8, hi // 8   # scores a softmax can tell apart
-    s = Step(hi - lo, [(57, 260)], 16, 1, 128)
+    s = Step(hi - lo, [(57, 860)], 16, 1, 128)
     s.pools.scales(s.rng, np.concatenate(s.slots), lo, hi, k=what == "keys", v=what == "values")
     s.upload()
     check(_attend(s), *s.reference())
 
 
 @pytest.mark.parametrize("is_key", [True, False])
-@pytest.mark.parametrize("tok", [3, 127, 128, 200])
+@pytest.mark.parametrize("tok", [3, 895, 896, 930])
 def test_a_nan_group_stays_with_its_rows(is_key, tok):
     """Past, at and behind the new tokens; in the first and the second key tile."""
-    s = Step(17 + tok, [(60, 150)], 16, 1, 128)
+    s = Step(17 + tok, [(60, 880)], 16, 1, 128)
     slot = int(s.slots[0][tok])
     pool = s.pools.k if is_key else s.pools.v
     pool[slot // 16, mxfp4.scale_place(slot % 16, 1, 128, is_key)] = 255
@@ -71,7 +72,7 @@ def test_a_nan_group_stays_with_its_rows(is_key, tok):
     got = _attend(s.upload()).double().cpu()
     ref, tol = s.reference()
     bad = torch.zeros_like(ref, dtype=torch.bool)
-    bad[max(0, tok - 150):, :, (slice(None) if is_key else slice(32, 64))] = True
+    bad[max(0, tok - 880):, :, (slice(None) if is_key else slice(32, 64))] = True
     assert torch.isnan(ref[bad]).all() and torch.isfinite(ref[~bad]).all()
     assert torch.isnan(got[bad]).all()
     check(got, ref, tol, rows=~bad)
@@ -81,7 +82,7 @@ def test_an_outlier_that_no_row_but_the_last_sees():
     """The last token's K and V are 2^60 times the others': the rows before it
     keep their precision."""
     n = 60
-    s = Step(23, [(n, 100)], 16, 1, 64)
+    s = Step(23, [(n, 900)], 16, 1, 64)
     plain_ref, plain_tol = s.reference()
     s.pools.scales(s.rng, s.slots[0][-1:], 60, 60)
     got = _attend(s.upload())
@@ -90,7 +91,7 @@ def test_an_outlier_that_no_row_but_the_last_sees():
 
 def test_bad_blocks_and_bad_metadata():
     pkv = _pkv()
-    reqs = [(60, 200), (58, 0), (1, 33)]
+    reqs = [(60, 900), (58, 870), (1, 33)]
     ref, tol = Step(8, reqs, 16, 1, 64).reference()
     for col, bad in ((2, -1), (15, 10 ** 6)):
         t = Step(8, reqs, 16, 1, 64)
@@ -104,7 +105,7 @@ def test_bad_blocks_and_bad_metadata():
         zero.pools.k[blk] = 0
         zero.pools.v[blk] = 0
         check(got, *zero.reference())
-    for r, field, bad in ((0, "dseq", 259), (1, "dpast", -1), (0, "dseq", 10 ** 9)):
+    for r, field, bad in ((0, "dseq", 959), (1, "dpast", -1), (0, "dseq", 10 ** 9)):
         t = Step(8, reqs, 16, 1, 64).upload()
         getattr(t, field)[r] = bad
         if field == "dpast":
@@ -119,11 +120,11 @@ def test_bad_blocks_and_bad_metadata():
         assert (got.cpu()[~keep] == 3.0).all()
 
 
-@pytest.mark.parametrize("tiles", [0, 1, 2, 3, 5, 7])
+@pytest.mark.parametrize("tiles", [0, 7, 8, 9, 16, 17, 25])
 def test_workspaces_with_less_room(tiles):
-    """Key tiles 3, 2 and 3: the requests that find no room are computed directly."""
+    """Key tiles 9, 8 and 8: the requests that find no room are computed directly."""
     pkv = _pkv()
-    s = Step(41, [(60, 250), (57, 100), (80, 200), (1, 9)], 16, 1, 128).upload()
+    s = Step(41, [(60, 1000), (57, 900), (80, 900), (1, 9)], 16, 1, 128).upload()
     full = pkv.mxfp4_attention_workspace_bytes(16, 1, 128)
     image = 2 * 32768 + 1152       # K, V, scales
     least = full - IMAGE_ROOM // image * image
@@ -141,8 +142,8 @@ def test_workspaces_with_less_room(tiles):
 def test_two_graphs_that_share_a_workspace():
     pkv = _pkv()
     ws = pkv.new_workspace_mxfp4(16, 1, 64)
-    steps = [Step(51, [(60, 70), (1, 300)], 16, 1, 64).upload(),
-             Step(52, [(1, 20), (99, 0), (3, 5)], 16, 1, 64).upload()]
+    steps = [Step(51, [(60, 870), (1, 300)], 16, 1, 64).upload(),
+             Step(52, [(1, 20), (99, 840), (3, 5)], 16, 1, 64).upload()]
     graphs, outs = [], []
     for s in steps:
         out = torch.zeros_like(s.dq)

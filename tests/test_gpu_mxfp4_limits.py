@@ -19,7 +19,7 @@ def _pkv():
     ([(1, 70), (1, 0), (1, 333)], 40, 20, 64),               # two passes over the heads
     ([(1, 70), (1, 500)], 144, 9, 128),                      # 16 query heads of 9
     ([(1, 200), (40, 17), (1, 3)], 33, 33, 64),
-    ([(70, 30), (1, 100)], 144, 9, 64),                      # converted ahead
+    ([(70, 900), (1, 100)], 144, 9, 64),                     # converted ahead
 ])
 def test_many_kv_heads(reqs, heads, hkv, d):
     pkv = _pkv()
@@ -38,7 +38,7 @@ def test_the_most_requests():
     for r in rng.choice(8192, 900, replace=False):
         reqs[r] = (int(rng.integers(0, 4)), int(rng.integers(0, 50)))
     for r in (0, 4095, 4096, 8191):
-        reqs[r] = (230 + r % 7, 20)
+        reqs[r] = (230 + r % 7, 800)
     s = Step(4, reqs, 4, 1, 64).upload()
     ws = pkv.new_workspace_mxfp4(4, 1, 64)
     got = pkv.paged_attention_varlen_mxfp4(*s.args(), workspace=ws)
@@ -46,7 +46,7 @@ def test_the_most_requests():
     check(got, *s.reference())
 
 
-@pytest.mark.parametrize("reqs", [[(1, 90), (1, 300)], [(20, 70)], [(60, 70)]])
+@pytest.mark.parametrize("reqs", [[(1, 90), (1, 300)], [(20, 70)], [(60, 870)]])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_a_query_that_is_not_finite_spoils_its_own_row(reqs, value):
     pkv = _pkv()
