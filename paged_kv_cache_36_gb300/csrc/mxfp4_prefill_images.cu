@@ -20,7 +20,7 @@
 // exchange between the two warps of a row, exponentials, P back, at eight softmax warps
 // an SM; the tensor core is busy 40 % of the time.  A prompt of 4096 tokens with 32
 // query and 8 KV heads of 128 takes 152 us, 903 TFLOP/s, about 8 us of them for the images; of
-// 16384 tokens 1704 us, 1291 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
+// 16384 tokens 1659 us, 1326 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
 //
 // Warp roles (16 warps): warp 0 copies K and Meta, warp 1 V; warp 2 owns the tensor
 // memory and issues Q K^T, warp 3 issues P V; warps 4-11 run the softmax and the
