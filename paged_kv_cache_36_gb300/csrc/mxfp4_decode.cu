@@ -48,8 +48,8 @@
 // take 199 us, 5.7 TB/s, where the copies alone (the same ring, nothing computed)
 // reach 6.9: the warps' issue slots are half full, mostly with the conversion of
 // codes, and a warp that computes late asks for its next bytes late.  64 requests of
-// 128 to 4096 tokens take 41.6 us (150 MB): 2.5 us for the plan, 4.5 until the first
-// bytes are there, 27 at 4.8 TB/s, 5 for the join with its launch.
+// 128 to 4096 tokens take 41.3 us (150 MB): 2.5 us for the plan, 4.5 until the first
+// bytes are there, 27 at 4.8 TB/s, 4 for the join with its launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -970,15 +970,17 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   e = launch_programmatic(decode_mxfp4_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
                           dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  // Few requests have many ranges each: eight lanes take 32 dimensions, four
-  // ranges at a time.  Where that is more than a wave of warps, a warp takes as
-  // many dimensions as it can.
+  // Few requests have many ranges each: eight lanes take 32 dimensions, four ranges at
+  // a time.  Where that is more than a wave of warps, more lanes and fewer ranges (64
+  // requests with 32 heads of 128: sixteen 41.3 us, thirty-two 42.1, eight 42.4).
   const int64_t heads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group;
   const int64_t wave = 32 * static_cast<int64_t>(sms);
   constexpr int kWide = D / 4;
-  const bool narrow = heads * (D / 32) <= wave;
-  const int64_t grid = ((narrow ? heads * (D / 32) : heads) + 7) / 8;
-  return launch_programmatic(narrow ? join_mxfp4_kernel<D, 8> : join_mxfp4_kernel<D, kWide>,
+  const int lanes = heads * (D / 32) <= wave ? 8 : heads * (D / 64) <= wave ? 16 : kWide;
+  const int64_t grid = (heads * (D / (4 * lanes)) + 7) / 8;
+  return launch_programmatic(lanes == 8    ? join_mxfp4_kernel<D, 8>
+                             : lanes == 16 ? join_mxfp4_kernel<D, 16>
+                                           : join_mxfp4_kernel<D, kWide>,
                              dim3(static_cast<unsigned>(grid < wave / 4 ? grid : wave / 4)),
                              dim3(256), 0, stream, p);
 }

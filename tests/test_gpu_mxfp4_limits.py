@@ -30,6 +30,19 @@ def test_many_kv_heads(reqs, heads, hkv, d):
     check(got, *s.reference())
 
 
+@pytest.mark.parametrize("n", [30, 45, 90])
+def test_joins_of_every_width(n):
+    """960, 1440 and 2880 query heads of 128 in a step: their ranges are joined by 8, 16 and
+    32 lanes."""
+    pkv = _pkv()
+    rng = np.random.default_rng(n)
+    s = Step(70 + n, [(1, int(p)) for p in rng.integers(0, 400, n)] + [(1, 3000)], 32, 8, 128).upload()
+    ws = pkv.new_workspace_mxfp4(32, 8, 128)
+    got = pkv.paged_attention_varlen_mxfp4(*s.args(), workspace=ws, max_query_len=1)
+    assert pkv.read_error_word(ws) == 0
+    check(got, *s.reference())
+
+
 def test_the_most_requests():
     """8192 requests: decode rows, short chunks, and a few that are converted ahead."""
     pkv = _pkv()
