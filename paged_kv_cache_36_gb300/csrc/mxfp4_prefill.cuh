@@ -319,7 +319,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 // What only some key tiles need is done to the scores in tensor memory, in short loops:
 // unrolled over the registers, code that hardly ever runs took instruction cache from
-// the code that always does (a prompt of 4096 tokens: 177 us instead of 152).
+// the code that always does (a prompt of 4096 tokens: 177 us, in loops 167).
 
 // Scores of N columns from `cols` on times a factor plus an offset by key: qf kf[c] (f
 // where kf is null) and kv[c] (v).
