@@ -430,7 +430,9 @@ int pkv_gather_cache_mxfp4(const void* key_cache, const void* value_cache,
  * tokens of 8 KV heads of 128) is converted again for every 128 / G query
  * tokens.  Both products take f16 with float32 sums: queries keep their 8 bits
  * over 30 binades, a 4-bit value is exact unless its scale is 2^26 times below
- * the largest of the keys around it, weights are rounded to 11 bits.
+ * the largest of the keys around it, weights are rounded to 11 bits.  A row's
+ * products of weight and scale may span all of float32's exponents and more; of
+ * those 2^100 times below its largest nothing is kept.
  *
  * The workspace is pkv_mxfp4_attention_workspace_bytes() bytes whatever the
  * batch (all but its last 256 MiB are needed), its first 256 bytes zero before

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
       const int u = row / G;
       const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
       const int pos_min = t.nc + t.u0;
-      float m_used = -INFINITY, l = 0.f, qf = 0.f, vref = 0.f;
+      float m_used = -INFINITY, ml = kNoScore, l = 0.f, qf = 0.f;
       uint32_t nan_groups = 0u;  // V groups that are NaN for this row
       bool ok = true;
       for (int j = 0; j < t.nkt && ok; ++j, ++count) {
@@ -432,10 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           break;
         }
         const Meta& meta = metas[ms];
-        if (j == 0) {
-          qf = meta.qf[row];
-          vref = meta.vb[0];
-        }
+        if (j == 0) qf = meta.qf[row];
         float f[2], vb[2];
         const uint4 kfl = *reinterpret_cast<const uint4*>(meta.k_flags);
         const uint4 vfl = *reinterpret_cast<const uint4*>(meta.v_flags);
@@ -454,9 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         }
         tc_fence_after();
         const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
-        float lw[2];  // what brings a weight with its V base back: 2^(vref - vb)
-        lw[0] = pow2(static_cast<int>(vref - vb[0]));
-        lw[1] = pow2(static_cast<int>(vref - vb[1]));
         uint32_t keyed = 0u;  // this warp's groups of 32 keys with bases by key
         if (__builtin_expect(flags != 0u, 0)) {
 #pragma unroll
@@ -487,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
           tmem_wait_ld();
         }
-        float mg[2];
+        float mg[2], mw[2];  // the groups' largest s + v, and s
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           float m4[4];
@@ -500,14 +494,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           float x = fmax3(m4[0], m4[1], fmax3(m4[2], m4[3], sv[32 * g + 28]));
           x = fmax3(x, sv[32 * g + 29], fmax3(sv[32 * g + 30], sv[32 * g + 31], x));
           mg[g] = fmaf(x, f[g], vb[g]);
+          mw[g] = x * f[g];
         }
         const float m_mine = fmaxf(mg[0], mg[1]);
         const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
-        if (j == 0) {
-          m_used = mx;  // key 0 is visible to every row
-        } else {
-          // both warps of the quadrant see the same mx and m_used
-          const bool grow = mx > m_used + kRescaleThreshold;
+        if (j == 0) m_used = mx;  // key 0 is visible to every row
+        float up[2] = {m_used - vb[0], m_used - vb[1]};
+        // both warps of the quadrant see the same mx and m_used
+        const bool grow = mx > m_used + kRescaleThreshold;
+        uint32_t summed = 0u;  // groups whose weights are summed already
+        // one vote for everything that is rare
+        if (__any_sync(0xffffffffu, grow || keyed != 0u || fmaxf(mw[0], mw[1]) > ml + kRescaleThreshold ||
+                                        fmaxf(up[0], up[1]) - ml > kApart)) {
           if (__any_sync(0xffffffffu, grow)) {
             // O must hold PV of the previous key tile before it is rescaled
             const uint32_t prev = count - 1;
@@ -518,28 +516,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
             tc_fence_after();
             const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
             if (grow) m_used = mx;
-            l *= alpha;
             rescale<D / 2>(o_cols, alpha);
           }
-        }
-        if (__builtin_expect(keyed != 0u, 0)) {
-          // The weights from the scores themselves: with a small enough V scale P is 0.
+          const float* key_vb[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            if (!((keyed >> g) & 1u)) continue;
-            const bool by_v = (meta.v_flags[2 * half + g] & 2u) != 0u;
-            l += sum_scores<32>(s_cols + 32 * g, by_v ? meta.key_vb + half * 64 + g * 32 : nullptr,
-                                meta.vb[2 * half + g], vref - m_used);
-            lw[g] = 0.f;  // and not again below
+            up[g] = m_used - vb[g];
+            key_vb[g] = (meta.v_flags[2 * half + g] & 2u) ? meta.key_vb + half * 64 + g * 32 : nullptr;
+            if ((keyed >> g) & 1u) mw[g] = max_scores<32>(s_cols + 32 * g, key_vb[g], meta.vb[2 * half + g]);
+          }
+          move_reference(fmaxf(mw[0], mw[1]), ml, l);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const bool by_key = (keyed >> g) & 1u;
+            if (!__any_sync(0xffffffffu, by_key || weights_lost(mw[g], vb[g], m_used, ml))) continue;
+            l += sum_scores<32>(s_cols + 32 * g, f[g], by_key ? key_vb[g] : nullptr,
+                                by_key ? meta.vb[2 * half + g] : 0.f, ml);
+            summed |= 1u << g;
           }
         }
+        float lw[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) lw[g] = (summed >> g) & 1u ? 0.f : weight_factor(up[g], ml);
         // P = 2^(s f + vb - m_used) as f16 pairs over the first 32 of this
         // warp's 64 S columns
         uint32_t w[32];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const float2 f2 = make_float2(f[g], f[g]);
-          const float2 c2 = make_float2(vb[g] - m_used, vb[g] - m_used);
+          const float2 c2 = make_float2(-up[g], -up[g]);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -560,12 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
         }
       }
       if (!ok) break;
-      // ---- epilogue: O 2^vref / (l_0 + l_1) -> out ----
+      // ---- epilogue: O 2^m / (l_0 2^ml_0 + l_1 2^ml_1) -> out ----
       if (!held_warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
       ++tiles_done;
       tc_fence_after();
-      // (two factors: their product may be too small for a float)
-      const float inv = 1.f / (l + exchange(l)), unit = pow2(static_cast<int>(vref));
+      const float ml_other = exchange(ml), l_other = exchange(l);
+      const float top = fmaxf(ml, ml_other);  // a score: key 0 is visible to every row
+      const float inv = 1.f / fmaf(l, exp2_approx(ml - top), l_other * exp2_approx(ml_other - top));
+      const float root = exp2_approx(0.5f * (m_used - top));  // its square may be too small for a float
       // This warp holds output dims [half * D/2, half * D/2 + D/2) of its 32
       // rows: NV 16-byte pieces per row, transposed among groups of NV lanes so
       // that every store instruction writes whole rows' segments.
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
           uint4& v = seg[c * 4 + q4];
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r0[q4 * 8 + e]) * s * unit;
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r0[q4 * 8 + e]) * s * root * root;
           v.x = pack_bf16(x[0], x[1]);
           v.y = pack_bf16(x[2], x[3]);
           v.z = pack_bf16(x[4], x[5]);

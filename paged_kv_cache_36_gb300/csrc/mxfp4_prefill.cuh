@@ -5,8 +5,8 @@
 // V: a value is code 2^(e - base + kUp) in f16, exact for scales down to 2^-26 of the
 // base's and then rounded at f16's 2^-25.  The softmax puts the bases back for free:
 // x = s f + (v - M), with f = 2^(K base) times the query's factor and v the V base in
-// log2 units, so that P carries 2^v, the running maximum M is one of s + v, and l sums
-// P 2^(vref - v).  Where those keys differ by more than 2^kWide (an outlier, perhaps
+// log2 units, so that P carries 2^v and the running maximum M is one of s + v (see
+// move_reference for the sum of the weights).  Where those keys differ by more than 2^kWide (an outlier, perhaps
 // one that the row may not even see), every key gets a base of its own, and the softmax
 // a factor and an offset per column: no key's precision depends on another's.
 #pragma once
@@ -342,9 +342,24 @@ __device__ __forceinline__ void scale_scores(uint32_t cols, float qf, const floa
   tmem_wait_st();
 }
 
-// The sum of 2^(x - kv[c] + add) over N columns of such scores (v where kv is null).
+// Over N columns of scores x f - kv[c] (v where kv is null): the largest, and the sum of
+// 2^(score - ml).
 template <int N>
-__device__ __forceinline__ float sum_scores(uint32_t cols, const float* kv, float v, float add) {
+__device__ __forceinline__ float max_scores(uint32_t cols, const float* kv, float v) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < N; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(cols + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      mx = fmaxf(mx, __uint_as_float(r[e]) - (kv != nullptr ? kv[c + e] : v));
+  }
+  return mx;
+}
+template <int N>
+__device__ __forceinline__ float sum_scores(uint32_t cols, float f, const float* kv, float v, float ml) {
   float sum = 0.f;
 #pragma unroll 1
   for (int c = 0; c < N; c += 8) {
@@ -353,10 +368,30 @@ __device__ __forceinline__ float sum_scores(uint32_t cols, const float* kv, floa
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      sum += exp2_approx(__uint_as_float(r[e]) - (kv != nullptr ? kv[c + e] : v) + add);
+      sum += exp2_approx(fmaf(__uint_as_float(r[e]), f, kv != nullptr ? -kv[c + e] : -v) - ml);
   }
   return sum;
 }
+
+// The sum of the weights, l = sum 2^(s - ml), has a reference of its own beside O's, M,
+// because values may be further apart than float32's exponents: M follows s + v, ml
+// follows s (both only when that grows by 2^15).  From the products' weights P = 2^(s +
+// vb - M) a group of keys with largest score mw adds sum(P) 2^(M - vb - ml).  Where P has
+// underflowed although the keys count, the sum is made from the scores: P below 2^-90
+// (its lesser ones would be lost), and weights above 2^-45 (n keys below that are n 2^-45
+// at most, less than n float32 additions round off).  Then M - vb - ml is above kApart.
+constexpr float kNoScore = -1e30f;  // ml before the first key
+constexpr float kApart = 45.f;
+__device__ __forceinline__ void move_reference(float mw, float& ml, float& l) {
+  const float to = mw > ml + kRescaleThreshold ? mw : ml;
+  l *= exp2_approx(ml - to);
+  ml = to;
+}
+__device__ __forceinline__ bool weights_lost(float mw, float vb, float m, float ml) {
+  return mw + vb - m < -90.f && mw - ml > -45.f;
+}
+// 2^(up - ml), up = M - vb.  (The limit: above it only weights that do not count.)
+__device__ __forceinline__ float weight_factor(float up, float ml) { return exp2_approx(fminf(up - ml, 110.f)); }
 
 // -inf into this row's columns from `visible` on, of 64; `first` is the smallest such
 // column of the warp's rows.

@@ -19,8 +19,8 @@
 // What bounds it: the chain of a key tile, S from tensor memory, its maximum, the
 // exchange between the two warps of a row, exponentials, P back, at eight softmax warps
 // an SM; the tensor core is busy 40 % of the time.  A prompt of 4096 tokens with 32
-// query and 8 KV heads of 128 takes 152 us, 903 TFLOP/s, about 8 us of them for the images; of
-// 16384 tokens 1659 us, 1326 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
+// query and 8 KV heads of 128 takes 155 us, 887 TFLOP/s, about 8 us of them for the images; of
+// 16384 tokens 1627 us, 1352 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
 //
 // Warp roles (16 warps): warp 0 copies K and Meta, warp 1 V; warp 2 owns the tensor
 // memory and issues Q K^T, warp 3 issues P V; warps 4-11 run the softmax and the
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
       const int u = row / G;
       const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
       const int pos_min = t.nc + t.u0;
-      float m_used = -INFINITY, l = 0.f, vref = 0.f;
+      float m_used = -INFINITY, ml = kNoScore, l = 0.f;
       uint32_t nan_groups = 0u;  // V groups that are NaN for this row
       bool ok = warp_wait(&bars[kQf0 + tiles_done % kQfs], (tiles_done / kQfs) & 1, p.err, abort_flag);
       const float qf = qfs[tiles_done % kQfs * kRows + row];
@@ -354,8 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
         float f = qf * __uint_as_float(head.x), vb = __uint_as_float(head.y);
         f = f < 1.17549435e-38f ? 1.17549435e-38f : f;
         const uint32_t flags = head.z;
-        if (j == 0) vref = vb;
-        float lw = pow2(static_cast<int>(vref - vb));  // what brings a weight with its V base back
         if (!warp_wait(&bars[kSFull0 + b], (count / kSBufs) & 1, p.err, abort_flag)) {
           ok = false;
           break;
@@ -391,13 +389,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
           for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], sv[c + k], sv[c + 4 + k]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], sv[60 + k]);
-        const float m_mine = fmaf(fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])), f, vb);
+        const float x_max = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+        const float m_mine = fmaf(x_max, f, vb);
         const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
-        if (j == 0) {
-          m_used = mx;  // key 0 is visible to every row
-        } else {
-          // both warps of the quadrant see the same mx and m_used
-          const bool grow = mx > m_used + kRescaleThreshold;
+        const bool keyed = (flags & 3u) != 0u;
+        float mw = x_max * f;
+        if (j == 0) m_used = mx;  // key 0 is visible to every row
+        float up = m_used - vb;
+        // both warps of the quadrant see the same mx and m_used
+        const bool grow = mx > m_used + kRescaleThreshold;
+        bool summed = false;
+        // one vote for everything that is rare
+        if (__any_sync(0xffffffffu, grow || keyed || mw > ml + kRescaleThreshold || up - ml > kApart)) {
           if (__any_sync(0xffffffffu, grow)) {
             // O must hold PV of the previous key tile before it is rescaled
             const uint32_t prev = count - 1;
@@ -408,19 +411,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
             tc_fence_after();
             const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
             if (grow) m_used = mx;
-            l *= alpha;
             rescale<D / 2>(o_cols, alpha);
+            up = m_used - vb;
           }
+          const float* key_vb = (flags & 2u) ? meta.key_vb + half * 64 : nullptr;
+          if (keyed) mw = max_scores<64>(s_cols, key_vb, __uint_as_float(head.y));
+          move_reference(mw, ml, l);
+          summed = __any_sync(0xffffffffu, keyed || weights_lost(mw, vb, m_used, ml));
+          if (summed)
+            l += sum_scores<64>(s_cols, f, keyed ? key_vb : nullptr, keyed ? __uint_as_float(head.y) : 0.f, ml);
         }
-        if (__builtin_expect((flags & 3u) != 0u, 0)) {
-          // The weights from the scores themselves: with a small enough V scale P is 0.
-          l += sum_scores<64>(s_cols, (flags & 2u) ? meta.key_vb + half * 64 : nullptr,
-                              __uint_as_float(head.y), vref - m_used);
-          lw = 0.f;  // and not again below
-        }
+        const float lw = summed ? 0.f : weight_factor(up, ml);
         // P = 2^(s f + vb - m_used) as f16 pairs over the first 32 of this warp's 64 S
         // columns
-        const float2 f2 = make_float2(f, f), c2 = make_float2(vb - m_used, vb - m_used);
+        const float2 f2 = make_float2(f, f), c2 = make_float2(-up, -up);
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t w[32];
 #pragma unroll
@@ -441,12 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
         }
       }
       if (!ok) break;
-      // ---- epilogue: O 2^vref / (l_0 + l_1) -> out ----
+      // ---- epilogue: O 2^m / (l_0 2^ml_0 + l_1 2^ml_1) -> out ----
       if (!warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
       ++tiles_done;
       tc_fence_after();
-      // (two factors: their product may be too small for a float)
-      const float inv = 1.f / (l + exchange(l)), unit = pow2(static_cast<int>(vref));
+      const float ml_other = exchange(ml), l_other = exchange(l);
+      const float top = fmaxf(ml, ml_other);  // a score: key 0 is visible to every row
+      const float inv = 1.f / fmaf(l, exp2_approx(ml - top), l_other * exp2_approx(ml_other - top));
+      const float root = exp2_approx(0.5f * (m_used - top));  // its square may be too small for a float
       // This warp holds output dims [half * D/2, half * D/2 + D/2) of its 32
       // rows: NV 16-byte pieces per row, transposed among groups of NV lanes so
       // that every store instruction writes whole rows' segments.
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
           uint4& v = seg[c * 4 + q4];
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r0[q4 * 8 + e]) * s * unit;
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r0[q4 * 8 + e]) * s * root * root;
           v.x = pack_bf16(x[0], x[1]);
           v.y = pack_bf16(x[2], x[3]);
           v.z = pack_bf16(x[4], x[5]);

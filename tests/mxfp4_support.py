@@ -100,7 +100,8 @@ class Step:
             2^-22 of |v_j| where p_j is below the normal f16 range (its least
             step is 2^-24; a weight may have been scaled by 2^-3 before);
           sums: 2 n u of A for n keys, at worst;
-          the result: half a bfloat16 step, 2^-8 |out|.
+          the result: half a bfloat16 step, 2^-8 |out|; below 2^-126 a step is
+            2^-133 whatever the value (8 bits down from 2^-126), half of it 2^-134.
         """
         ref = torch.zeros(self.T, self.H, self.d, dtype=torch.float64)
         tol = torch.zeros_like(ref)
@@ -129,7 +130,7 @@ class Step:
                 tol[a:b, h] = (2.0 ** -8 * ref[a:b, h].abs()
                                + mean[:, h] * (2.0 ** -11 + 2.0 ** -20 + 4 * (self.d + 32) * u * s
                                                + 2 * n * u)
-                               + 2.0 ** -22 * total)
+                               + 2.0 ** -22 * total + 2.0 ** -134)
         return ref, tol
 
 
