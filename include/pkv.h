@@ -433,6 +433,8 @@ int pkv_gather_cache_mxfp4(const void* key_cache, const void* value_cache,
  * the largest of the keys around it, weights are rounded to 11 bits.  A row's
  * products of weight and scale may span all of float32's exponents and more; of
  * those 2^100 times below its largest nothing is kept.
+ * Scores (scale <q, k>) are float32: from 2^22 in magnitude on their last bit is
+ * as large as the weights' range, and rows may become NaN.
  *
  * The workspace is pkv_mxfp4_attention_workspace_bytes() bytes whatever the
  * batch (all but its last 256 MiB are needed), its first 256 bytes zero before

@@ -368,7 +368,8 @@ __device__ __forceinline__ float sum_scores(uint32_t cols, float f, const float*
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      sum += exp2_approx(fmaf(__uint_as_float(r[e]), f, kv != nullptr ? -kv[c + e] : -v) - ml);
+      // (fused as in the products' weights: large scores must not round differently here)
+      sum += exp2_approx(fmaf(__uint_as_float(r[e]), f, -(ml + (kv != nullptr ? kv[c + e] : v))));
   }
   return sum;
 }

@@ -65,3 +65,26 @@ def test_scores_and_values_far_apart(reqs, big):
         s.pools.scales(s.rng, slots[~low], -40 if big else 40, -40 if big else 40, k=False)
     s.upload()
     check(_attend(s), *s.reference())
+
+
+@pytest.mark.parametrize("reqs", REQS)
+def test_scores_of_a_million(reqs):
+    """One key takes all of a row's weight, wherever it is: its value is the result."""
+    s = Step(84, reqs, 16, 1, 64, lo=14, hi=16)
+    s.pools.scales(s.rng, np.concatenate(s.slots), -3, 2, k=False)
+    s.upload()
+    ref, tol = s.reference()
+    got = _attend(s)
+    check(got, ref, tol)
+    # rows whose first two scores are 64 apart or more have one weight that counts
+    one = torch.ones(s.T, s.H, dtype=torch.bool)
+    for r in range(s.R):
+        k, _ = s.history(r)
+        for i in range(s.q_len[r]):
+            t, n = int(s.qsl[r]) + i, s.past[r] + i + 1
+            top = (s.q[t].double() @ k[:n, 0].T * s.scale).topk(min(2, n), 1).values
+            one[t] = top[:, 0] - top[:, -1] > 64.0
+    assert one.float().mean() > 0.9
+    # (the others' weights are e^-64 = 1.6e-28 at most, 960 keys of values up to 24: below
+    # 1e-20 together, which is all there is where that one's value is zero)
+    assert ((got.cpu().double() - ref).abs()[one] <= 2.0 ** -6 * ref.abs()[one] + 1e-20).all()
