@@ -13,9 +13,9 @@
 // range q is the units [floor(qN/Q), floor((q+1)N/Q)).  (64 requests of some 2000
 // tokens, 8 KV heads of 128: counting blocks alone, warps with no change were
 // through after 31.5 us, those with one after 34.3, with two after 37.1.)  A request that crosses ranges leaves one
-// partial (m, l, o) per range and head in the workspace, and a second kernel
+// partial (m, l, o / l) per range and head in the workspace, and a second kernel
 // joins them,
-//   M = max_s m_s,  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
+//   M = max_s (m_s + floor(log2 l_s)),  w_s = 2^(m_s - M) l_s,  out = sum_s w_s (o_s / l_s) / sum_s w_s,
 // in an order that the ranges fix: no counters, no atomics, the same bits every
 // time.  (Joining in this kernel, by the warp that
 // came last, took about 18 us of a 230 us call: one warp reads the partials of
@@ -39,10 +39,11 @@
 //     each group of dimensions, `base` a running exponent per group.  Scales
 //     in the 16 binades from it up, which is nearly always, cost one f16x2
 //     product per group; a tile outside the window takes the slow path below,
-//     which moves the base and splits the tile into windows so that no weight
-//     leaves f16's range.
-//   - The running maximum moves only when a score exceeds it by 2^3: the common
-//     tile needs a vote, and no shuffle.
+//     which brings each product of weight and scale to f16 as a whole, relative to
+//     the largest of its 16 tokens, group and head.
+//   - The reference m of the weights lies 2^11 below a score that was the largest
+//     and moves when one exceeds it by 2^14: the common tile needs a vote, and no
+//     shuffle.
 //
 // What bounds it.  8 requests of 131072 tokens with 64 query and 8 KV heads of 128
 // take 199 us, 5.7 TB/s, where the copies alone (the same ring, nothing computed)
@@ -65,14 +66,21 @@ namespace pkv {
 namespace {
 
 constexpr int kMinUnits = 8;     // units in a range, nearly: at least 4
-// Weights stay below 2^kMaxSlack (the running maximum moves when a score
-// exceeds it by more), and a V scale multiplies them by 2^(e - base + kLow) with
-// e - base in [0, 15]: at most 2^(3 + 12), inside f16, and at the window's lower
-// end a weight of 1 still has 11 bits and all weights a resolution of 2^-21.
-constexpr float kMaxSlack = 3.f;
-constexpr int kLow = -3;
+// The weights 2^(s - m) of a head: m moves when a weight exceeds 2^kMaxWeight, to where
+// it is 2^kLargest.  A V scale multiplies them by 2^(e - base + kLow) with e - base in
+// [0, 15]: 2^(14 + 1) at most, inside f16.  Each rounding to f16 is off by 2^-25 at most
+// where it is below f16's normal numbers, 2^-36 of the largest weight before the scale
+// and, at the window's lower end (where that weight's product is 2^-3), 2^-22 of it
+// after: n keys that count for less lose n 2^-21 of the largest product, at worst.
+constexpr float kLargest = 11.f;
+constexpr float kMaxWeight = 14.f;
+constexpr int kLow = -14;
 constexpr int kBelow = 11;       // where a new base goes below the largest scale of its tile
 constexpr int kTopBase = 239;
+// A product of weight and scale, of 16 tokens, that the slow path lets the sums grow by
+// (log2), and what it leaves them below when it lowers a base.
+constexpr float kMostProduct = 60.f;
+constexpr float kMostSum = 1.2379400e27f;  // 2^90
 
 template <int NT>
 constexpr int warps_per_cta() { return NT == 1 ? 16 : 8; }
@@ -104,7 +112,7 @@ struct Params {
   uint32_t* err;
   int2* plan;        // [num_reqs]: what there is to join (see slot_of)
   float2* part_ml;   // [2 * ranges][hkv][group]
-  float* part_o;     // [2 * ranges][hkv][group][D]
+  float* part_o;     // [2 * ranges][hkv][group][D], divided by l
   int32_t stages;
 };
 
@@ -459,7 +467,6 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     float o[2 * NB][NT][4];
     float m[NT][2], l[NT][2];
     uint32_t base[NW];  // running scale byte per group, as the V scale words have them: b0 b1 b0 b1
-    uint32_t top[NW];   // the highest base so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       l[nt][0] = l[nt][1] = 0.f;
     }
 #pragma unroll
-    for (int w = 0; w < NW; ++w) base[w] = top[w] = 0u;
+    for (int w = 0; w < NW; ++w) base[w] = 0u;
 
     int left = at.run;             // units of the run to go
     // tokens the request has from the stage's first on
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         for (int cc = 0; cc < 2; ++cc) {
           mx[nt][cc] = fmaxf(fmaxf(s[0][nt][cc], s[0][nt][2 + cc]),
                              fmaxf(s[1][nt][cc], s[1][nt][2 + cc])) * qs[nt][cc];
-          grow |= mx[nt][cc] > m[nt][cc] + kMaxSlack;
+          grow |= mx[nt][cc] > m[nt][cc] + kMaxWeight;
         }
       // P^T fragments of a unit: the weights of tokens 2 tid, + 1 (and + 8) for
       // head gid, and their sums
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                   sw[u][i][w] = (sw[u][i][w] & keep) | (to & ~keep);
                 }
             }
-            base[w] = top[w] = to;
+            base[w] = to;
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[nt][cc], x);
+            const float mn = fmaxf(m[nt][cc], x - kLargest);
             const float alpha = mn == m[nt][cc] ? 1.f : exp2_approx(m[nt][cc] - mn);
             m[nt][cc] = mn;
             l[nt][cc] *= alpha;
@@ -686,46 +693,79 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           }
         if (__any_sync(0xffffffffu, ((far[0] | far[1]) & 0xf0f0f0f0u) != 0u)) {
           // ---- slow path: scales outside the window ----
+          // The weight and the scale of a token make one power of two before anything is
+          // rounded: for 16 tokens, a group and a head, 2^(z - zm + 12) goes into the product
+          // as f16, z = s - m + e - base, zm the largest of them, and the result comes
+          // back by 2^(zm - 12 + kLow) in float32.  What is further below goes into products
+          // of its own, so a key's precision depends on no other key's score or scale.
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             if (u == 1 && tokens <= 16) break;
-            uint32_t pt[NT][2], ev[2][NW], od[2][NW];
-            weights(u, pt);
+            uint32_t ev[2][NW], od[2][NW];
             codes(u, ev, od);
-            // Tokens with no weight left in f16 (for every head) count for nothing
-            // here, as they do in the product.
-            uint32_t live = 0u;  // bit i: token 2 tid + (i & 1) + 8 (i >> 1)
+            // This lane has the scores of tokens gid and gid + 8 (i = 0, 1) and heads 2 tid, + 1.
+            // The largest weight of each token (log2), of any head there is:
+            float live[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if ((pt[nt][i >> 1] >> (16 * (i & 1))) & 0x7fffu) live |= 1u << i;
+              for (int c = 0; c < 4; ++c) {
+                const float x = fmaf(s[u][nt][c], qs[nt][c & 1], -m[nt][c & 1]);
+                l[nt][c & 1] += exp2_approx(x);
+                if (nt * 8 + 2 * tid + (c & 1) < G) live[c >> 1] = fmaxf(live[c >> 1], x);
+              }
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) live |= __shfl_xor_sync(0xffffffffu, live, x);
+            for (int i = 0; i < 2; ++i) {
+              live[i] = fmaxf(live[i], __shfl_xor_sync(0xffffffffu, live[i], 1));
+              live[i] = fmaxf(live[i], __shfl_xor_sync(0xffffffffu, live[i], 2));
+            }
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                int e[4];       // scale bytes of this lane's tokens in group 2 w + b
-                int hi = -1;
+                const uint8_t* scales = st + u * kUnit + kChunk + mx_vscale_off<D>(gid, 2 * w + b);
+                int bs = (base[w] >> (8 * b)) & 0xff, hi = -1;
                 bool nan = false;
+                float e[2];  // of the tokens, above the base; -inf where there is nothing to add
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  e[i] = (sw[u][i >> 1][w] >> (16 * (i & 1) + 8 * b)) & 0xff;
-                  const bool in = u * 16 + 2 * tid + (i & 1) + 8 * (i >> 1) < tokens;
-                  nan |= in && e[i] == 255;
-                  if (!in || e[i] == 255 || !((live >> i) & 1u)) e[i] = -1;
-                  hi = max(hi, e[i]);
+                for (int i = 0; i < 2; ++i) {
+                  const int byte = scales[i * (D / 4)];  // 8 tokens on: four pairs
+                  const bool in = u * 16 + gid + 8 * i < tokens;
+                  nan |= in && byte == 255;
+                  e[i] = in && byte != 255 ? static_cast<float>(byte - bs) : -INFINITY;
+                  if (in && byte != 255 && live[i] > -25.f) hi = max(hi, byte);
                 }
-                hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-                hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
                 nan = __any_sync(0xffffffffu, nan);
-                // the base follows the largest scale; down again only while what is
-                // summed up stays far from overflow
-                int bs = (base[w] >> (8 * b)) & 0xff, tp = (top[w] >> (8 * b)) & 0xff;
-                const int to = min(max(hi - kBelow, 0), kTopBase);
-                if (hi >= 0 && (to > bs || (hi < bs && tp - to <= 60))) {
-                  const float f = bs > to ? pow2(bs - to) : pow2(max(bs - to, -127));
+                float most = -INFINITY;  // of z, any token and head
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    most = fmaxf(most, fmaf(s[u][nt][c], qs[nt][c & 1], -m[nt][c & 1]) + e[c >> 1]);
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                  hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
+                  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+                }
+                // the base follows the largest scale that f16 weights still count for; down
+                // only while what is summed up stays far from overflow, up too for the sake
+                // of the sums
+                int to = hi < 0 ? bs : min(max(hi - kBelow, 0), kTopBase);
+                if (to < bs) {
+                  to = hi < bs ? max(to, bs - 100) : bs;
+                  float sum = 0.f;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                      for (int c = 0; c < 4; ++c) sum = fmaxf(sum, fabsf(o[4 * w + 2 * b + k][nt][c]));
+                  if (__any_sync(0xffffffffu, sum * pow2(bs - to) > kMostSum)) to = bs;
+                }
+                if (most - static_cast<float>(to - bs) > kMostProduct)
+                  to = min(bs + static_cast<int>(most - kMostProduct) + 1, kTopBase);
+                if (to != bs) {
+                  const float f = pow2(bs - to);
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -734,53 +774,66 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                       for (int c = 0; c < 4; ++c) o[4 * w + 2 * b + k][nt][c] *= f;
                   const uint32_t hold = ~(0x00ff00ffu << (8 * b));
                   base[w] = (base[w] & hold) | (static_cast<uint32_t>(to) * 0x00010001u) << (8 * b);
-                  tp = max(tp, to);
-                  top[w] = (top[w] & hold) | (static_cast<uint32_t>(tp) * 0x00010001u) << (8 * b);
-                  bs = to;
+                  e[0] += static_cast<float>(bs - to);
+                  e[1] += static_cast<float>(bs - to);
                 }
-                // windows of 16 binades, from the base down
-                for (int below = 0; below < 256; below += 16) {
-                  uint32_t f[2] = {0u, 0u};
-                  bool rest = false;
+                uint32_t a[2][4];  // fragments of the group's two m-tiles
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int d = e[i] < 0 ? -1000 : e[i] - bs + below;
-                    if (d >= 0 && d < 16)
-                      f[i >> 1] |= static_cast<uint32_t>(d + kLow + 15) << (10 + 16 * (i & 1));
-                    rest |= e[i] >= 0 && d < 0;
+                for (int k = 0; k < 2; ++k) {
+                  const int at8 = 8 * (2 * b + k);
+                  a[k][0] = e2m1x2_to_f16x2(ev[0][w] >> at8);
+                  a[k][1] = e2m1x2_to_f16x2(od[0][w] >> at8);
+                  a[k][2] = e2m1x2_to_f16x2(ev[1][w] >> at8);
+                  a[k][3] = e2m1x2_to_f16x2(od[1][w] >> at8);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float z[4];  // below the head's largest
+                  float zm[2];
+#pragma unroll
+                  for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                      z[2 * i + cc] = fmaf(s[u][nt][2 * i + cc], qs[nt][cc], -m[nt][cc]) + e[i];
+                    float x = fmaxf(fmaxf(z[cc], z[2 + cc]), -1e30f);
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                    z[cc] -= x;
+                    z[2 + cc] -= x;
+                    zm[cc] = x;
                   }
-                  const float back = pow2(-below);
-                  uint32_t a[2][4];  // fragments of the group's two m-tiles
+                  // 26 binades of them at a time: f16's normal numbers below 2^13
+                  bool more = true;
+                  for (float down = 0.f; more && down < 120.f; down += 26.f) {
+                    float p16[4];
+                    more = false;
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const int at8 = 8 * (2 * b + k);
-                    a[k][0] = e2m1x2_to_f16x2(ev[0][w] >> at8);
-                    a[k][1] = e2m1x2_to_f16x2(od[0][w] >> at8);
-                    a[k][2] = e2m1x2_to_f16x2(ev[1][w] >> at8);
-                    a[k][3] = e2m1x2_to_f16x2(od[1][w] >> at8);
-                  }
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t b0 = mul_f16x2(pt[nt][0], f[0]), b1 = mul_f16x2(pt[nt][1], f[1]);
+                    for (int c = 0; c < 4; ++c) {
+                      const float y = z[c] + down;  // (NaN goes on)
+                      more |= y <= -26.f;
+                      p16[c] = y > 0.f || y <= -26.f ? 0.f : exp2_approx(y + 12.f);
+                    }
+                    const uint32_t b0 = transpose_8x8(pack_f16(p16[0], p16[1]));
+                    const uint32_t b1 = transpose_8x8(pack_f16(p16[2], p16[3]));
+                    const float back[2] = {exp2_approx(zm[0] - down + (kLow - 12)),
+                                           exp2_approx(zm[1] - down + (kLow - 12))};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                       float t[4];
                       mma_f16_first(t, a[k][0], a[k][1], a[k][2], a[k][3], b0, b1);
 #pragma unroll
                       for (int c = 0; c < 4; ++c)
-                        o[4 * w + 2 * b + k][nt][c] = fmaf(t[c], back, o[4 * w + 2 * b + k][nt][c]);
+                        o[4 * w + 2 * b + k][nt][c] = fmaf(t[c], back[c & 1], o[4 * w + 2 * b + k][nt][c]);
                     }
+                    more = __any_sync(0xffffffffu, more);
                   }
-                  if (!__any_sync(0xffffffffu, rest)) break;
-                }
-                if (nan) {
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
+                  if (nan) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                       for (int c = 0; c < 4; ++c)
                         o[4 * w + 2 * b + k][nt][c] = __uint_as_float(0x7fffffffu);
+                  }
                 }
               }
             }
@@ -854,10 +907,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
           const float f = mx_scale((base[b >> 1] >> (8 * (b & 1))) & 0xffu) * pow2(-kLow);
           float x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = o[2 * b + (i >> 1)][nt][2 * (i & 1) + cc] * f;
+          for (int i = 0; i < 4; ++i) x[i] = o[2 * b + (i >> 1)][nt][2 * (i & 1) + cc] * inv * f;
           if (whole)
             *reinterpret_cast<uint2*>(dst + 32 * b) =
-                make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+                make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
           else
             *reinterpret_cast<float4*>(po + 32 * b) = make_float4(x[0], x[1], x[2], x[3]);
         }
@@ -870,6 +923,11 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   }
   // every copy of this pass has been waited for by its stage; none is in flight
   }
+}
+
+// log2 of a range's weight 2^m l, to the binade.
+__device__ __forceinline__ float range_weight(float2 ml) {
+  return ml.x + static_cast<float>(static_cast<int>(__float_as_uint(ml.y) >> 23) - 127);
 }
 
 // Joins the partials of every request that crosses ranges.  kLanes lanes take 4
@@ -913,7 +971,7 @@ __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
       }
       float mx = big;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, ml[k].x);
+      for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, range_weight(ml[k]));
       const float keep = big == mx ? 1.f : exp2_approx(big - mx);
       big = mx;
       den *= keep;
@@ -924,8 +982,9 @@ __global__ void __launch_bounds__(256, 4) join_mxfp4_kernel(const Params p) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (k0 + kParts * k >= splits) break;
-        const float w = ml[k].x == mx ? 1.f : exp2_approx(ml[k].x - mx);
-        den = fmaf(ml[k].y, w, den);
+        // 2^-9 at most: some hundred values near float32's end may be added up
+        const float w = exp2_approx(ml[k].x - mx - 10.f) * ml[k].y;
+        den += w;
         acc.x = fmaf(x[k].x, w, acc.x);
         acc.y = fmaf(x[k].y, w, acc.y);
         acc.z = fmaf(x[k].z, w, acc.z);
