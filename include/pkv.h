@@ -426,13 +426,20 @@ int pkv_gather_cache_mxfp4(const void* key_cache, const void* value_cache,
  * Bytes of tokens past a request's end may hold anything.
  *
  * Requests with many query tokens have their keys and values converted to f16
- * once, in the workspace's last 256 MiB; what finds no room there (some 65000
+ * once, in the workspace's last 256 MiB; what finds no room there (some 64000
  * tokens of 8 KV heads of 128) is converted again for every 128 / G query
- * tokens.  Both products take f16 with float32 sums: queries keep their 8 bits
- * over 30 binades, a 4-bit value is exact unless its scale is 2^26 times below
- * the largest of the keys around it, weights are rounded to 11 bits.  A row's
- * products of weight and scale may span all of float32's exponents and more; of
- * those 2^100 times below its largest nothing is kept.
+ * tokens.  Both products take f16 with float32 sums.  Queries keep their 8 bits
+ * over 30 binades; a key is exact unless its scale is 2^26 times below the
+ * largest of its own, or of those of the keys around it that are within 2^14;
+ * values are exact.  Weights are rounded to 11 bits, and where weight times
+ * scale is below 2^-14 of the largest of the row so far to the same absolute
+ * step, so that nothing is left below 2^-26 (decode rows: 2^-25 and 2^-36); of
+ * keys near one another, scales within 2^8 (decode rows: of one group of
+ * dimensions, within 2^15) count as one in that.  Where they are further apart,
+ * in a decode row between keys and in longer ones within a key, the sums take
+ * every product of weight and value as it is (longer rows: with 16 bits, in a
+ * second pass over the row's keys).  Of products 2^100 times below a row's
+ * largest nothing is kept.
  * Scores (scale <q, k>) are float32: from 2^22 in magnitude on their last bit is
  * as large as the weights' range, and rows may become NaN.
  *

@@ -91,7 +91,7 @@ MxWorkspace mx_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   w.ml = w.plan + up(static_cast<size_t>(step_metadata_max_reqs()) * 8);
   w.o = w.ml + up(slots * group * 8);
   w.image_base = w.o + up(slots * group * head_dim * 4);
-  w.images = w.image_base + up(static_cast<size_t>(step_metadata_max_reqs() + 2) * 4);
+  w.images = w.image_base + up(static_cast<size_t>(2 * step_metadata_max_reqs() + 2) * 4);
   w.tile = static_cast<size_t>(prefill_mxfp4_image_bytes(num_kv_heads, head_dim));
   w.total = w.images + kImageRoom / w.tile * w.tile;
   return w;

@@ -203,7 +203,7 @@ cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream)
 // Scratch of the 4-bit prefill: key tiles converted ahead of it.
 struct MxPrefillScratch {
   uint8_t* images;
-  int32_t* image_base;        // [2 + num_reqs]
+  int32_t* image_base;        // [2 + 2 num_reqs]
   int32_t image_tiles;        // key tiles (of all KV heads) that images has room for
 };
 

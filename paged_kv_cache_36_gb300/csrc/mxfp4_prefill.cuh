@@ -5,10 +5,21 @@
 // V: a value is code 2^(e - base + kUp) in f16, exact for scales down to 2^-26 of the
 // base's and then rounded at f16's 2^-25.  The softmax puts the bases back for free:
 // x = s f + (v - M), with f = 2^(K base) times the query's factor and v the V base in
-// log2 units, so that P carries 2^v and the running maximum M is one of s + v (see
-// move_reference for the sum of the weights).  Where those keys differ by more than 2^kWide (an outlier, perhaps
-// one that the row may not even see), every key gets a base of its own, and the softmax
-// a factor and an offset per column: no key's precision depends on another's.
+// log2 units, so that P carries 2^v and the running reference M follows s + v (see
+// move_reference for the sum of the weights).  Where those keys differ by more than 2^kWide
+// (an outlier, perhaps one that the row may not even see), every key gets a base of its own,
+// that of its largest group, and the softmax a factor and an offset per column.
+//
+// What f16 loses: a weight below 2^-14 keeps fewer than 11 bits, off by 2^-25 at most, where
+// the largest s + v has 2 or more.  A base that keys share may be 2^8 above a key's own (2^14,
+// but then M starts lower), and a group's scale is 2^-kUneven of its key's largest at least:
+// n keys that count for little lose n 2^-26 2^(8 + 8) of a group's largest product, at worst.
+//
+// Groups of one key further apart than that (a reference M that one of them sets says
+// nothing about another) take another way: the direct kernel goes through such query tiles
+// again with V as bfloat16 below a base by key (a code has two bits and is exact) and P as
+// two bfloat16, the second what the first rounds off: 16 bits, and 2^-126 below M before
+// anything is lost, at the cost of a second product and of the slower path by key.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,9 +42,13 @@ constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr uint32_t kRegion = 16384;  // 128 rows x 128 bytes
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleThreshold = 15.0f;  // log2 units: weights below 2^15 are inside f16
+constexpr float kRescaleThreshold = 15.9f;  // log2 units: weights up to 2^15.9 are inside f16
+constexpr float kFirst = 1.0f;       // where a row's first M puts its largest weight: room to grow
+constexpr float kMoved = 8.0f;       // and where a later one does: hardly any row needs a third
 constexpr int kUp = 12;              // a base's scale becomes 2^kUp: 6 2^12 is inside f16
 constexpr int kWide = 14;            // binades between keys before each has its base
+constexpr int kLoose = 8;            // and before their V lets M start at kMoved
+constexpr int kUneven = 8;           // binades between the groups of one key's V in f16
 constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;  // a whole key tile more is still an int
 // Query tiles (of a KV head) and key tiles from which on a request has its key tiles
@@ -70,9 +85,12 @@ struct Params {
   int32_t entry_shift;  // requests per plan entry, as a power of two
   // Key tiles converted ahead (null: none): request r's are images image_base[r] hkv
   // on, its key tiles in order, KV head fastest; -1: none, its rows are the direct
-  // kernel's.  any[0]: whether there are such; any[1]: whether there are images.
+  // kernel's.  uneven[r]: the images' kernel has found V that is not for f16, and leaves its
+  // rows to the direct kernel too.  any[0]: whether there are such; any[1]: whether there are
+  // images.
   uint8_t* images;
   int32_t* image_base;
+  int32_t* uneven;
   int32_t* any;
   int32_t image_tiles;  // key tiles (of all KV heads) there is room for
 };
@@ -105,7 +123,9 @@ template <bool kImages>
 __device__ __forceinline__ int own_tiles(const Params& p, int r, int tpt, bool* bad) {
   const int n = request_tiles(p, r, tpt, bad);
   if (n == 0 || p.images == nullptr) return kImages ? 0 : n;
-  return (__ldcg(p.image_base + r) >= 0) == kImages ? n : 0;
+  const bool has = __ldcg(p.image_base + r) >= 0;
+  if (kImages) return has ? n : 0;
+  return !has || __ldcg(p.uneven + r) != 0 ? n : 0;
 }
 
 // Tile `ct` -> (request, KV head, query rows).  prefix[i] counts the tiles before
@@ -208,6 +228,21 @@ __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// Eight codes times their group's scale as bfloat16.
+__device__ __forceinline__ uint4 convert8_bf16(uint32_t w, uint32_t f) {
+  uint32_t x[4];
+  e2m1x8_to_f16(w, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+    const uint32_t code = pack_bf16(v.x, v.y);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&code),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&f));
+    x[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // Eight codes times their group's scale, to one 16-byte piece of a tile row.
 __device__ __forceinline__ uint4 convert8(uint32_t w, uint32_t f) {
   uint32_t x[4];
@@ -243,6 +278,42 @@ __device__ __forceinline__ uint32_t load_scale_bytes(const uint8_t* at) {
   }
 }
 
+// Scale bytes of a row of V with 255 for the groups whose codes are all zero.
+template <int D>
+__device__ __forceinline__ uint32_t without_zeros(uint32_t e, const uint4 (&c)[D / 32]) {
+  uint32_t even = 0u, odd = 0u;  // of the words of codes
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    even |= c[i].x | c[i].z;
+    odd |= c[i].y | c[i].w;
+  }
+  if (D == 64) even |= odd;
+  if ((even & 0x00007777u) == 0u) e |= 0xffu;
+  if ((even & 0x77770000u) == 0u) e |= 0xff00u;
+  if (D == 128 && (odd & 0x00007777u) == 0u) e |= 0xff0000u;
+  if (D == 128 && (odd & 0x77770000u) == 0u) e |= 0xff000000u;
+  return e;
+}
+
+// Whether a row's groups, NaN aside, are more than 2^kUneven apart.
+template <int D>
+__device__ __forceinline__ bool uneven_groups(uint32_t e) {
+  const uint32_t b0 = e & 0xffu, b1 = (e >> 8) & 0xffu, b2 = (e >> 16) & 0xffu, b3 = e >> 24;
+  const uint32_t least = D == 128 ? min(min(b0, b1), min(b2, b3)) : min(b0, b1);
+  return largest_scale<D>(e) - static_cast<int>(least) > kUneven;  // (-1 - 255 where all are NaN)
+}
+
+// The groups' factors 2^(e - base) as bfloat16, in both halves, down to 2^-133 (V).
+template <int D>
+__device__ __forceinline__ void row_factors_bf16(uint32_t scales, bool real, int base, uint32_t (&f)[D / 32]) {
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b) {
+    const int e = (scales >> (8 * b)) & 0xff, x = e - base;
+    const uint32_t power = x >= -126 ? static_cast<uint32_t>(x + 127) << 7 : x >= -133 ? 1u << (x + 133) : 0u;
+    f[b] = !real || e == 255 ? 0u : power * 0x00010001u;
+  }
+}
+
 // The groups' factors 2^(e - base + kUp) as f16, in both halves.
 template <int D, bool kIsV>
 __device__ __forceinline__ void row_factors(uint32_t scales, bool real, int base, uint32_t (&f)[D / 32]) {
@@ -270,7 +341,7 @@ __device__ __forceinline__ void row_factors(uint32_t scales, bool real, int base
 // 2i + e / 2, group e % 2).  V: the half-words of two words are 8 dimensions; 128:
 // words (group / 2) of lane groups 2i and 2i + 1; 64: of lane groups 4i + 2 (e / 2)
 // and + 1.
-template <int D, bool kIsV>
+template <int D, bool kIsV, bool kBf16 = false>
 __device__ __forceinline__ void store_piece(uint8_t* dst, int i, const uint4& codes,
                                             const uint32_t (&f)[D / 32], int sw) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
@@ -286,16 +357,17 @@ __device__ __forceinline__ void store_piece(uint8_t* dst, int i, const uint4& co
     }
     // dims 32 b + 8 q .. + 7: piece 4 b + q of the row
     const uint32_t at = (static_cast<uint32_t>(q ^ sw) << 4) ^ ((b & 1) << 6);
-    *reinterpret_cast<uint4*>(dst + (b >> 1) * 1024 + at) = convert8(eight, f[b]);
+    *reinterpret_cast<uint4*>(dst + (b >> 1) * 1024 + at) =
+        kBf16 ? convert8_bf16(eight, f[b]) : convert8(eight, f[b]);
   }
 }
 
 // The base exponent of a warp's 32 keys, `mine` being each lane's largest scale (-1:
-// none), and whether the keys are too far apart for one.
-__device__ __forceinline__ int common_base(int mine, bool& wide) {
+// none), and how far (binades) the keys are apart.
+__device__ __forceinline__ int common_base(int mine, int& apart) {
   const int base = __reduce_max_sync(0xffffffffu, mine);
   const int least = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine));  // -1: largest
-  wide = least >= 0 && base - least > kWide;
+  apart = least >= 0 ? base - least : 0;
   return base < 0 ? 127 : base;
 }
 
@@ -393,6 +465,32 @@ __device__ __forceinline__ bool weights_lost(float mw, float vb, float m, float 
 }
 // 2^(up - ml), up = M - vb.  (The limit: above it only weights that do not count.)
 __device__ __forceinline__ float weight_factor(float up, float ml) { return exp2_approx(fminf(up - ml, 110.f)); }
+
+// Weights 2^(x - up) of the 64 scores x from `cols` on, over their columns: as pairs of
+// bfloat16 in the first 32, and what those round off in the others.
+__device__ __forceinline__ void split_weights(uint32_t cols, float up) {
+  uint32_t r[32], w[32];
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    tmem_ld32(cols + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float x = exp2_approx(__uint_as_float(r[2 * e]) - up);
+      const float y = exp2_approx(__uint_as_float(r[2 * e + 1]) - up);
+      w[e] = pack_bf16(x, y);
+      w[16 + e] = pack_bf16(x - __uint_as_float(w[e] << 16), y - __uint_as_float(w[e] & 0xffff0000u));
+    }
+    tmem_st32(cols + c, w);
+  }
+  tmem_wait_st();
+  // the second 16 columns and the third change places
+  tmem_ld32(cols + 16, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 32; ++e) w[e] = r[e ^ 16];
+  tmem_st32(cols + 16, w);
+}
 
 // -inf into this row's columns from `visible` on, of 64; `first` is the smallest such
 // column of the warp's rows.

@@ -68,7 +68,7 @@ enum Bar {
 struct alignas(16) Meta {
   float kf;            // K base: 2^(base - 127 - kUp)
   float vb;            // V base: base - 127 - kUp, log2 units
-  uint32_t flags;      // 1: K by key, 2: V by key, 4: NaN in V
+  uint32_t flags;      // 1: K by key, 2: V by key, 4: NaN in V, 8: V of uneven groups, 16: loose V
   uint32_t unused;
   int32_t nan_pos[4];  // first key position with a NaN V group, by group
   float key_kf[kKeys];
@@ -361,6 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
         tc_fence_after();
         const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
         if (__builtin_expect(flags != 0u, 0)) {
+          if ((flags & 8u) && warp == 4 && lane == 0) {
+            p.uneven[t.r] = 1;  // for the direct kernel
+            p.any[0] = 1;
+          }
           if (flags & 3u) {  // bases by key
             scale_scores<64>(s_cols, qf, (flags & 1u) ? meta.key_kf + half * 64 : nullptr, f,
                              (flags & 2u) ? meta.key_vb + half * 64 : nullptr, vb);
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
         const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
         const bool keyed = (flags & 3u) != 0u;
         float mw = x_max * f;
-        if (j == 0) m_used = mx;  // key 0 is visible to every row
+        if (j == 0) m_used = mx - ((flags & 16u) ? kMoved : kFirst);  // key 0 is visible to every row
         float up = m_used - vb;
         // both warps of the quadrant see the same mx and m_used
         const bool grow = mx > m_used + kRescaleThreshold;
@@ -409,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_images_kernel(const
               break;
             }
             tc_fence_after();
-            const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
-            if (grow) m_used = mx;
+            const float alpha = grow ? exp2_approx(m_used - mx + kMoved) : 1.f;
+            if (grow) m_used = mx - kMoved;
             rescale<D / 2>(o_cols, alpha);
             up = m_used - vb;
           }
@@ -510,6 +514,7 @@ __global__ void __launch_bounds__(256) expand_mxfp4_kernel(const Params p) {
   int32_t* prefix = reinterpret_cast<int32_t*>(parts + 8 * kPart);  // [R + 1]: key tiles
   struct Found {
     int most, least;  // of the warp's rows' largest scales (least: as unsigned, -1 none)
+    int uneven;       // whether a row of V has uneven groups
     int nan_pos[4];   // by group; 0x7fffffff: none
   };
   __shared__ Found found[2][8];
@@ -534,6 +539,7 @@ __global__ void __launch_bounds__(256) expand_mxfp4_kernel(const Params p) {
     for (int r = threadIdx.x; r < R; r += blockDim.x) {
       const bool has = prefix[r + 1] > prefix[r] && prefix[r + 1] <= p.image_tiles;
       p.image_base[r] = has ? prefix[r] : -1;
+      p.uneven[r] = 0;
       images |= has;
       direct |= !has && request_tiles(p, r, tpt, &bad) > 0;
     }
@@ -582,10 +588,14 @@ __global__ void __launch_bounds__(256) expand_mxfp4_kernel(const Params p) {
     const int mine = real ? largest_scale<D>(scales) : -1;
     const int most = __reduce_max_sync(0xffffffffu, mine);
     const int least = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(mine));  // -1: largest
+    bool uneven = is_v && real && uneven_groups<D>(scales);
+    if (__any_sync(0xffffffffu, uneven))
+      uneven = __any_sync(0xffffffffu, uneven && uneven_groups<D>(without_zeros<D>(scales, c)));
     Found* mates = found[turn] + (is_v ? 4 : 0);
     if (lane == 0) {
       mates[cw].most = most;
       mates[cw].least = least;
+      mates[cw].uneven = uneven ? 1 : 0;
     }
     if (__any_sync(0xffffffffu, is_v && real && nan_scale(scales))) {
 #pragma unroll
@@ -621,6 +631,10 @@ __global__ void __launch_bounds__(256) expand_mxfp4_kernel(const Params p) {
           k_low = min(k_low, static_cast<unsigned>(found[turn][w].least));
         }
         if (k_low != 0xffffffffu && k_base - static_cast<int>(k_low) > kWide) flags |= 1u;
+        if (low != 0xffffffffu && base - static_cast<int>(low) > kLoose) flags |= 16u;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (mates[w].uneven) flags |= 8u;
         if (k_base < 0) k_base = 127;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -717,6 +731,7 @@ cudaError_t launch_prefill_mxfp4(const AttnArgs& a, const MxPrefillScratch& ws, 
   p.entry_shift = 0;
   p.images = nullptr;
   p.image_base = nullptr;
+  p.uneven = nullptr;
   p.any = nullptr;
   p.image_tiles = ws.image_tiles;
   // where the longest query, the room or the table's width says that no request can have
@@ -726,6 +741,7 @@ cudaError_t launch_prefill_mxfp4(const AttnArgs& a, const MxPrefillScratch& ws, 
     p.images = ws.images;
     p.any = ws.image_base;
     p.image_base = ws.image_base + 2;
+    p.uneven = p.image_base + a.num_reqs;
     const cudaError_t e = launch_images(p, a.head_dim, sms, stream);
     if (e != cudaSuccess) return e;
   }

@@ -51,26 +51,23 @@ def _decode_floor(p, v, e):
 
 def _prefill_floor(p, v, e):
     """The same of a prefill row.  With x = weight times the largest scale of a key's groups:
-    the weights of a tile of 128 keys are f16 with 2^8 or more for the largest x so far (a
-    shared base of the tile may be 2^8 above a key's own scale), off by 2^-25 each below
-    f16's normal numbers.  Where the keys' scales, or one key's groups, are more than 2^8
-    apart the tile's weights are pairs of bfloat16, without a floor; from the first tile on
-    in which one key's groups are, the reference is each tile's own (2^72 below the row's at
-    most)."""
-    n = e.shape[0]
-    most, least = e.amax(1), torch.where(e < -500, 1000.0, e).amin(1)
-    x = p * torch.exp2(most)
+    weights are f16 with 2 or more for the largest x so far, off by 2^-25 each below f16's
+    normal numbers, over a base that keys share, up to 2^8 above a key's own scale (up to 2^14
+    with 2^8 or more for the largest x: 2^7 from x either way).  A row that sees a key whose
+    groups (those with a code that is not zero) are more than 2^8 apart has weights of two
+    bfloat16, without a floor."""
+    most = e.amax(1)
+    some = (v.nan_to_num(0.0).unflatten(1, (-1, 32)).abs().amax(2) > 0) & (e > -500)
+    apart = torch.where(some, e, -1000.0).amax(1) - torch.where(some, e, 1000.0).amin(1)
     floor = torch.zeros(p.shape[0], v.shape[1], dtype=torch.float64)
-    so_far, own = torch.zeros(p.shape[0], dtype=torch.float64), False
-    for j in range(0, n, 128):
+    if bool((apart > 8).any()):
+        return floor
+    x = p * torch.exp2(most)
+    so_far = torch.zeros(p.shape[0], dtype=torch.float64)
+    for j in range(0, e.shape[0], 128):
         m, keys = most[j:j + 128], slice(j, j + 128)
         so_far = torch.maximum(so_far, x[:, keys].amax(1))
-        uneven = bool((m - least[keys] > 8).any())
-        own = own or uneven
-        if uneven or float(m.amax() - m.amin()) > 8:
-            continue
-        ref = torch.maximum(x[:, keys].amax(1), so_far * 2.0 ** -72) if own else so_far
-        floor += 2.0 ** -25 * ref[:, None] * (v[keys].abs() * torch.exp2(-m)[:, None]).sum(0)
+        floor += 2.0 ** -18 * so_far[:, None] * (v[keys].abs() * torch.exp2(-m)[:, None]).sum(0)
     return floor
 
 

@@ -40,7 +40,7 @@ def _step(seed, kind, d, octaves, heads=4):
     return s
 
 
-@pytest.mark.parametrize("kind", ["decode"])
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("octaves, up", [(24, 24), (32, 40), (32, 24), (48, 48), (96, 90)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_unlikely_keys_with_large_values(kind, octaves, up, d):
@@ -53,7 +53,7 @@ def test_unlikely_keys_with_large_values(kind, octaves, up, d):
     check(_attend(s), *reference(s))
 
 
-@pytest.mark.parametrize("kind", ["decode"])
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("octaves, down", [(12, 12), (24, 24), (24, 40)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_one_likely_key_with_small_values(kind, octaves, down, d):
@@ -67,7 +67,7 @@ def test_one_likely_key_with_small_values(kind, octaves, down, d):
     check(_attend(s), *reference(s), tight=0.6)
 
 
-@pytest.mark.parametrize("kind", ["decode"])
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("octaves", [4, 48])
 def test_values_near_the_end_of_float32(kind, octaves):
     """Sums and joins of values of 2^120 stay finite."""
@@ -76,3 +76,114 @@ def test_values_near_the_end_of_float32(kind, octaves):
         s.pools.scales(s.rng, slots, 120, 122, k=False)
     s.upload()
     check(_attend(s), *reference(s))
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("which", ["one", "first", "third", "all"])
+@pytest.mark.parametrize("above", [20, 30, 40, 70, -30])
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_of_dimensions_far_apart(kind, which, above, d):
+    """In one key, the first one, a third of them or all of them the first group of dimensions is
+    2^above times the others: those keep their own precision."""
+    s = Step(4, KINDS[kind], 4, 1, d)
+    for slots in s.slots:
+        s.pools.scales(s.rng, slots, -1, 1, k=False)
+        n = len(slots)
+        some = {"one": slice(n // 3, n // 3 + 1), "first": slice(0, 1), "third": slice(0, n, 3),
+                "all": slice(0, n)}[which]
+        at = slots[some]
+        place = np.array([mxfp4.scale_place(t, 0, d, False) for t in range(16)])
+        s.pools.v[at // 16, place[at % 16]] = 127 + above
+    s.upload()
+    check(_attend(s), *reference(s))
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_groups_of_two_kinds_of_keys(kind):
+    """Even keys have their large values in the first group, odd ones in the last."""
+    s = Step(5, KINDS[kind], 16, 1, 128)
+    for slots in s.slots:
+        s.pools.scales(s.rng, slots, -1, 1, k=False)
+        for part, group in ((slots[::2], 0), (slots[1::2], 3)):
+            place = np.array([mxfp4.scale_place(t, group, 128, False) for t in range(16)])
+            s.pools.v[part // 16, place[part % 16]] = 127 + 50
+    s.upload()
+    check(_attend(s), *reference(s))
+
+
+def _uneven(s, r, where=slice(None)):
+    """Group 0 of the request's values (of some tokens) 2^40 times the others."""
+    at = s.slots[r][where]
+    for h in range(s.hkv):
+        place = np.array([mxfp4.scale_place(t, 0, s.d, False) for t in range(16)])
+        s.pools.v[at // 16, place[at % 16] + h * mxfp4.chunk_bytes(s.d)] = 127 + 40
+
+
+def test_one_request_of_uneven_values_among_others():
+    """More query tiles than SMs, the keys that are uneven in the middle of one request."""
+    s = Step(6, [(9, 30), (700, 40), (1, 100), (150, 0)], 32, 2, 64)
+    _uneven(s, 1, slice(300, 420, 7))
+    s.upload()
+    check(_attend(s), *reference(s))
+
+
+@pytest.mark.parametrize("reqs", [[(20, 270), (40, 3)], [(60, 900), (57, 950)]])
+def test_uneven_values_leave_nothing_behind(reqs):
+    """A workspace through uneven and even batches, captured and replayed."""
+    import paged_kv_cache_36_gb300 as pkv
+    ws = pkv.new_workspace_mxfp4(16, 1, 64)
+    steps = [Step(7 + i, reqs, 16, 1, 64) for i in range(3)]
+    _uneven(steps[0], 0)
+    _uneven(steps[1], 1, slice(5, 6))
+    alone = [_attend(s.upload()) for s in steps]
+    for s, a in zip(steps, alone):
+        check(a, *reference(s))
+    graphs, outs = [], []
+    for s in steps:
+        out = torch.zeros_like(s.dq)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pkv.paged_attention_varlen_mxfp4(*s.args(), workspace=ws, out=out)
+        graphs.append(g)
+        outs.append(out)
+    for i in (0, 2, 1, 1, 0, 2):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], alone[i])
+    assert pkv.read_error_word(ws) == 0
+
+
+@pytest.mark.parametrize("reqs", [[(20, 270)], [(60, 900)]])
+def test_nan_among_uneven_values(reqs):
+    s = Step(8, reqs, 16, 1, 128)
+    _uneven(s, 0, slice(0, None, 5))
+    tok = s.past[0] + 7
+    slot = int(s.slots[0][tok])
+    s.pools.v[slot // 16, mxfp4.scale_place(slot % 16, 2, 128, False)] = 255
+    for dim in range(64, 96):
+        byte, _ = mxfp4.code_place(slot % 16, dim, 128, False)
+        s.pools.v[slot // 16, byte] = 0
+    got = _attend(s.upload()).double().cpu()
+    ref, tol = reference(s)
+    bad = torch.zeros_like(ref, dtype=torch.bool)
+    bad[7:, :, 64:96] = True
+    assert torch.isnan(got[bad]).all() and torch.isnan(ref[bad]).all()
+    assert ((got - ref).abs() <= tol)[~bad].all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_dimensions_that_are_zero(kind):
+    """The last group is zero in every token (scale 1, as the cache write leaves it), the
+    others' values are 2^-20."""
+    s = Step(9, KINDS[kind], 4, 1, 128)
+    for slots in s.slots:
+        s.pools.scales(s.rng, slots, -21, -19, k=False)
+        for t in range(16):
+            at = slots[slots % 16 == t] // 16
+            s.pools.v[at, mxfp4.scale_place(t, 3, 128, False)] = 127
+            for dim in range(96, 128):
+                s.pools.v[at, mxfp4.code_place(t, dim, 128, False)[0]] = 0
+    got = _attend(s.upload())
+    ref, tol = reference(s)
+    assert (got[..., 96:] == 0).all()
+    check(got[..., :96], ref[..., :96], tol[..., :96])
