@@ -309,8 +309,9 @@ def _device_call(where: str, name: str, index: int, stream, *args) -> None:
     global _raw_stream, _current_device
     if _raw_stream is None:
         import torch
-        _raw_stream = torch._C._cuda_getCurrentRawStream
+        # (the one that is asked for above last: another thread may be here too)
         _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream
     if stream is None:
         ptr = _raw_stream(index)
     else:
