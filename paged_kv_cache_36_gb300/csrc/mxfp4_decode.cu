@@ -238,10 +238,11 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
     const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
     int nb = 0;
-    if (q1 - q0 == 1) {
+    // (unsigned: offsets that are garbage may be anything apart)
+    if (static_cast<uint32_t>(q1) - static_cast<uint32_t>(q0) == 1u) {
       nb = (seq - 1) / kMxBlock + 1;
       if (nc < 0 || nc > 0x7ffffffe || seq != nc + 1 || nb > p.bt_width || q0 < 0 ||
-          q1 > p.num_tokens) {
+          q0 >= p.num_tokens) {
         if (blockIdx.x == 0) atomicOr(p.err, PKV_ERR_METADATA);
         nb = 0;
       }

@@ -107,7 +107,8 @@ struct Tile {
 // metadata is wrong (*bad).
 __device__ __forceinline__ int request_tiles(const Params& p, int r, int tpt, bool* bad) {
   const int q0 = __ldg(p.qsl + r), q1 = __ldg(p.qsl + r + 1);
-  const int qlen = q1 - q0;
+  // (offsets that are garbage may be anything apart: those that wrap fail q1 < q0)
+  const int qlen = static_cast<int>(static_cast<uint32_t>(q1) - static_cast<uint32_t>(q0));
   if (qlen <= 1) return 0;
   const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
   if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || nc < 0 || nc > kMaxKeys - qlen ||
