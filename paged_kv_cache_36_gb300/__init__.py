@@ -290,6 +290,15 @@ def _check_device(where: str, index: int, *tensors) -> None:
         raise ValueError(f"{where}: all tensors must be on one CUDA device")
 
 
+def _error_ptr(where: str, t):
+    """Address of an error word (None: none), a 32-bit integer."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() < 1:
+        raise TypeError(f"{where}: error_word must be int32 with at least one entry")
+    return t.data_ptr()
+
+
 def _expect(where: str, name: str, t, dtype, shape) -> None:
     """t is a contiguous tensor of this dtype and shape."""
     if t.dtype is not dtype:
@@ -400,12 +409,12 @@ def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, slot_mapping, er
     """Quantise key/value [T, Hkv, D] (bfloat16 or float32) into the 4-bit caches
     (new_cache_mxfp4) at slot_mapping[T] (int64; negative: padding)."""
     where = "reshape_and_cache_mxfp4"
+    err = _error_ptr(where, error_word)
     dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key, value, key_cache, value_cache,
                                                 slot_mapping, error_word)
     _device_call(where, "pkv_reshape_and_cache_mxfp4", dev, stream, key.data_ptr(),
                  value.data_ptr(), _token_stride(key), _token_stride(value), key_cache.data_ptr(),
-                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d, dtype,
-                 error_word.data_ptr() if error_word is not None else None)
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d, dtype, err)
 
 
 def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out, error_word=None,
@@ -414,12 +423,13 @@ def gather_cache_mxfp4(key_cache, value_cache, slot_mapping, key_out, value_out,
     is left alone) back from the 4-bit caches into key_out and value_out
     [T, Hkv, D], bfloat16 or float32; exact.  Returns (key_out, value_out)."""
     where = "gather_cache_mxfp4"
+    err = _error_ptr(where, error_word)
     dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key_out, value_out, key_cache, value_cache,
                                                 slot_mapping, error_word)
     _device_call(where, "pkv_gather_cache_mxfp4", dev, stream, key_cache.data_ptr(),
                  value_cache.data_ptr(), slot_mapping.data_ptr(), key_out.data_ptr(),
                  value_out.data_ptr(), _token_stride(key_out), _token_stride(value_out), T, nb, 16,
-                 hkv, d, dtype, error_word.data_ptr() if error_word is not None else None)
+                 hkv, d, dtype, err)
     return key_out, value_out
 
 
@@ -514,6 +524,7 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
     refused whole: an empty step, with the reason's bit in error_word."""
     import torch
     where = "build_step_metadata"
+    err = _error_ptr(where, error_word)
     R, T = query_lens.shape[0], int(num_tokens)
     i32, i64 = torch.int32, torch.int64
     dev = query_lens.get_device()
@@ -571,7 +582,7 @@ def build_step_metadata(query_lens, num_computed_tokens, block_table, free_ring,
                  free_ring.numel(),
                  free_state.data_ptr(), free_state_out.data_ptr(), block_size, T,
                  query_start_loc.data_ptr(), seq_lens.data_ptr(), slot_mapping.data_ptr(),
-                 positions.data_ptr(), error_word.data_ptr() if error_word is not None else None)
+                 positions.data_ptr(), err)
     return query_start_loc, seq_lens, slot_mapping, positions
 
 

@@ -2,6 +2,7 @@
 
 import threading
 
+import pytest
 import torch
 
 
@@ -48,3 +49,21 @@ def test_two_threads_in_the_first_call(monkeypatch):
     call()
     assert not errors
     assert set(library.streams) == {77} and len(library.streams) >= 2
+
+
+@pytest.mark.parametrize("word", [torch.zeros(8, dtype=torch.uint8)[1:2], torch.zeros(1, dtype=torch.int64),
+                                  torch.zeros(1), torch.zeros(0, dtype=torch.int32)])
+def test_error_words_that_are_not_32_bits(word):
+    """What the kernels would set bits of is a 32-bit integer, at an address of one."""
+    import paged_kv_cache_36_gb300 as pkv
+    i32, i64 = torch.int32, torch.int64
+    k, slots = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=i64)
+    kc, vc = pkv.new_cache_mxfp4(4, 2, 64, device="cpu")
+    with pytest.raises(TypeError, match="error_word"):
+        pkv.reshape_and_cache_mxfp4(k, k, kc, vc, slots, error_word=word)
+    with pytest.raises(TypeError, match="error_word"):
+        pkv.gather_cache_mxfp4(kc, vc, slots, k, k, error_word=word)
+    one = torch.ones(1, dtype=i32)
+    with pytest.raises(TypeError, match="error_word"):
+        pkv.build_step_metadata(one, one, torch.zeros(1, 2, dtype=i32), torch.zeros(8, dtype=i32),
+                                torch.zeros(4, dtype=i64), 4, error_word=word)
