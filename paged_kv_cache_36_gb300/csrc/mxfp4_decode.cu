@@ -34,7 +34,8 @@
 //     bits of a bfloat16 over 30 binades below the head's largest element, so
 //     what is lost is below 2^-38 of it.
 //   - K scales multiply the partial sums of each group of 32 dimensions, in
-//     float32: any scale is exact.
+//     float32.  Those sums are up to 2^22, so the scales go 2^24 down first, unless
+//     a query is above 2^20 (then keys that this keeps in range have scores beyond it).
 //   - V scales go onto the weights: P^T (f16, 11 bits) times 2^(e - base) for
 //     each group of dimensions, `base` a running exponent per group.  Scales
 //     in the 16 binades from it up, which is nearly always, cost one f16x2
@@ -157,6 +158,12 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// NaN for NaN.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
@@ -427,7 +434,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     // B fragments of Q^T in f16: k-step 2b + s of lane tid holds dims 32 b + 8
     // tid + 4 s .. + 3, the order of the K codes
     uint32_t qb[NT][KS][2];
-    float qs[NT][2];  // what undoes the power of two, times scale log2(e), of heads 2 tid, + 1
+    float qs[NT][2];  // what undoes the powers of two, times scale log2(e), of heads 2 tid, + 1
+    uint32_t key_down = 0x33803380u;  // 2^-24, bfloat16
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int head = nt * 8 + gid;
@@ -447,12 +455,10 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       // largest element to [2^14, 2^15)
       const uint32_t ex = min(max(mx >> 7, 15u), 254u);
       const int up = 141 - static_cast<int>(ex);  // in [-113, 126]
-      const float f = copysignf(pow2(up), p.scale_log2);
-      // the scale's sign is Q's; never zero, for the masked scores' infinities
-      float undo = fabsf(p.scale_log2) * pow2(-up);
-      undo = undo < 1.17549435e-38f ? 1.17549435e-38f : undo;
-      qs[nt][0] = __shfl_sync(0xffffffffu, undo, 8 * tid);
-      qs[nt][1] = __shfl_sync(0xffffffffu, undo, 8 * tid + 4);
+      const float f = copysignf(pow2(up), p.scale_log2);  // the scale's sign is Q's
+      if (__any_sync(0xffffffffu, ex > 147u)) key_down = 0x3f803f80u;  // 1
+      qs[nt][0] = __int_as_float(__shfl_sync(0xffffffffu, up, 8 * tid));
+      qs[nt][1] = __int_as_float(__shfl_sync(0xffffffffu, up, 8 * tid + 4));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
@@ -465,6 +471,15 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       }
     }
 
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const float undo =
+            fabsf(p.scale_log2) * pow2((key_down == 0x3f803f80u ? 0 : 24) - __float_as_int(qs[nt][cc]));
+        // (never zero, for the masked scores' infinities)
+        qs[nt][cc] = undo < 1.17549435e-38f ? 1.17549435e-38f : undo;
+      }
     float o[2 * NB][NT][4];
     float m[NT][2], l[NT][2];
     uint32_t base[NW];  // running scale byte per group, as the V scale words have them: b0 b1 b0 b1
@@ -518,8 +533,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         uint32_t ks[2][NW];  // K scales as bfloat16 pairs, NaN for 255
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          ks[0][w] = e8m0x2_to_bf16x2(slo >> (16 * w));
-          ks[1][w] = e8m0x2_to_bf16x2(shi >> (16 * w));
+          ks[0][w] = mul_bf16x2(e8m0x2_to_bf16x2(slo >> (16 * w)), key_down);
+          ks[1][w] = mul_bf16x2(e8m0x2_to_bf16x2(shi >> (16 * w)), key_down);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

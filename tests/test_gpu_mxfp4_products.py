@@ -187,3 +187,17 @@ def test_dimensions_that_are_zero(kind):
     ref, tol = reference(s)
     assert (got[..., 96:] == 0).all()
     check(got[..., :96], ref[..., :96], tol[..., :96])
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("keys, queries", [(100, -100), (115, -118), (122, -110), (-100, 100), (-110, 118), (80, -60)])
+def test_large_keys_with_small_queries(kind, keys, queries):
+    """Scores of ordinary size from keys of 2^keys and queries of 2^queries, or the reverse."""
+    s = Step(10, KINDS[kind], 4, 1, 64)
+    for slots in s.slots:
+        s.pools.scales(s.rng, slots, keys - 1, keys + 1, v=False)
+    s.q = (s.q.double() * 2.0 ** queries).to(torch.bfloat16)
+    s.q[:, 1] = 0
+    s.scale = 2.0 ** min(3 - keys - queries, 8) / 8
+    s.upload()
+    check(_attend(s), *reference(s))
