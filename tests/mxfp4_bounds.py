@@ -77,7 +77,8 @@ def reference(step):
       score: D products and a few scalings in float32, u S each; a weight is off by
         2 (D + 32) u S of itself, numerator and denominator;
       weight: f16 twice, or a pair of bfloat16, 2^-11 of A (and an exponential, 2^-21);
-        what is below f16's normal numbers: the floors above;
+        what is below f16's normal numbers: the floors above, and 2^-100 of the row's
+        largest weight times scale for each key;
       sums: 2 n u A of n keys;
       the result: 2^-8 of it, or 2^-134."""
     ref = torch.zeros(step.T, step.H, step.d, dtype=torch.float64)
@@ -97,6 +98,9 @@ def reference(step):
                 p = torch.softmax(q @ kg.T * step.scale, 1)
                 worst = (q.abs() @ kg.abs().T * abs(step.scale)).amax(1, keepdim=True)
                 floor = (_decode_floor if rows == 1 else _prefill_floor)(p, vg, e[:n, g])
+                # of products 2^100 below the row's largest nothing is kept
+                most = (p * torch.exp2(e[:n, g].amax(1))).amax(1, keepdim=True)
+                floor = floor + 2.0 ** -100 * most * 6 * n
                 out = p @ vg
                 ref[a + i, heads] = out
                 tol[a + i, heads] = (2.0 ** -8 * out.abs() + 2.0 ** -134 + floor + (p @ vg.abs()) * (
