@@ -555,6 +555,14 @@ __device__ __forceinline__ void softmax_sweep(const Params& p, uint8_t* smem, co
   }
 }
 
+// Out of the way of the code that always runs, for head_dim 64: 512 tokens of 16/4 heads take
+// 18.4 us instead of 18.9, 128 behind 23190 243 instead of 274.  (128: 41.0 instead of 35.6
+// for 64 tokens behind 2048.)
+__device__ __noinline__ void convert_again_64(const Params& p, uint8_t* smem, const int32_t* prefix, int entries,
+                                              int total, int tpt, int cw, uint32_t count, uint32_t tiles) {
+  convert_sweep<64, true, true>(p, smem, prefix, entries, total, tpt, cw, count, tiles);
+}
+
 }  // namespace
 
 template <int D>
@@ -651,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
               if (!ok) break;
               tc_fence_after();
               const uint64_t kd = k_desc0 + ((ks * L::kHalf) >> 4);
-#pragma unroll
+              // (a loop: unrolled, 4096 tokens of 32/8 heads of 128 took 254 us instead of 240)
+#pragma unroll 1
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t q_off = ((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
                 const uint64_t k_off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
@@ -680,8 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mxfp4_kernel(const Params
     uint32_t count = 0, tiles = 0;
     if (!only_second_sweep<D>(smem))
       convert_sweep<D, true, false>(p, smem, prefix, entries, total, tpt, warp - 16, count, tiles);
-    if (second_sweep<D>(smem))
-      convert_sweep<D, true, true>(p, smem, prefix, entries, total, tpt, warp - 16, count, tiles);
+    if (second_sweep<D>(smem)) {
+      if constexpr (D == 64) convert_again_64(p, smem, prefix, entries, total, tpt, warp - 16, count, tiles);
+      else convert_sweep<D, true, true>(p, smem, prefix, entries, total, tpt, warp - 16, count, tiles);
+    }
   } else if (warp >= 12) {
     set_registers<kConvertRegs, false>();
     uint32_t count = 0, tiles = 0;
