@@ -77,7 +77,7 @@ struct MxWorkspace {
   size_t plan, ml, o, image_base, images, tile, total;
 };
 
-// Room for the prefill's converted key tiles: 65408 tokens of 8 KV heads of 128.
+// Room for the prefill's converted key tiles: 503 of 8 KV heads of 128, 64384 tokens.
 constexpr size_t kImageRoom = 256u << 20;
 
 // The error word's 256 bytes, then the decode's plan (for the largest batch) and

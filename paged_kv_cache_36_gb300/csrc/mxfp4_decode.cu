@@ -47,10 +47,10 @@
 //     shuffle.
 //
 // What bounds it.  8 requests of 131072 tokens with 64 query and 8 KV heads of 128
-// take 199 us, 5.7 TB/s, where the copies alone (the same ring, nothing computed)
+// take 201 us, 5.7 TB/s, where the copies alone (the same ring, nothing computed)
 // reach 6.9: the warps' issue slots are half full, mostly with the conversion of
 // codes, and a warp that computes late asks for its next bytes late.  64 requests of
-// 128 to 4096 tokens take 41.3 us (150 MB): 2.5 us for the plan, 4.5 until the first
+// 128 to 4096 tokens take 42.0 us (150 MB): 2.5 us for the plan, 4.5 until the first
 // bytes are there, 27 at 4.8 TB/s, 4 for the join with its launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1047,7 +1047,7 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // Few requests have many ranges each: eight lanes take 32 dimensions, four ranges at
   // a time.  Where that is more than a wave of warps, more lanes and fewer ranges (64
-  // requests with 32 heads of 128: sixteen 41.3 us, thirty-two 42.1, eight 42.4).
+  // requests with 32 heads of 128: sixteen take 0.8 us less than thirty-two, 1.1 less than eight).
   const int64_t heads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group;
   const int64_t wave = 32 * static_cast<int64_t>(sms);
   constexpr int kWide = D / 4;

@@ -28,8 +28,8 @@
 // the others: 512 tokens 48 us (23 without), behind 2048 138 (43), 4096 tokens 756 (147).
 //
 // What bounds it: the conversion, which runs again for every query tile and takes issue
-// slots and instruction cache from the softmax.  32 query and 8 KV heads of 128: 512
-// tokens 22.4 us, 2048 67 us, 4096 209 us; converted ahead 27, 62 and 152.
+// slots and instruction cache from the softmax.  32 query and 8 KV heads of 128, in a graph:
+// 512 tokens 23 us, 2048 75 us, 4096 242 us; converted ahead 2048 62 and 4096 161.
 //
 // Warp roles (20 warps): warp 0 owns the tensor memory and issues Q K^T; warp 1 issues P
 // V; warps 4-11 run the softmax and the epilogue, two per 32-lane quadrant of tensor

@@ -53,11 +53,13 @@ constexpr int kPrefixMax = 4096;     // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;  // a whole key tile more is still an int
 // Query tiles (of a KV head) and key tiles from which on a request has its key tiles
 // converted ahead.  That saves the conversion for every query tile but one, and costs two
-// kernels more, which also run, for 5 us, where no request turns out to have enough.  32
-// query and 8 KV heads of 128: 128 new tokens (4 query tiles) behind 4096 take 54 us that
-// way and 61 directly, behind 32768 276 and 370; 512 behind 0, 2048 and 16384 take 27, 43
-// and 153 us and 22 (27 behind the two kernels), 43 and 197; 1024 and 2048 behind 0 take 36
-// and 62, and 32 (38) and 67.
+// kernels more, which also run, for 5 us, where no request turns out to have enough.  In a
+// graph, us ahead / directly:
+//   32 query and 8 KV heads of 128: 128 new tokens (4 query tiles) behind 3874 54 / 64, behind
+//   17513 157 / 228; 512 behind 1223 37 / 39, behind 11539 115 / 164; 1024 (8 key tiles)
+//   behind 0 36 / 35, behind 914 49 / 58; 2048 and 4096 behind 0 62 / 75 and 161 / 242.
+//   16 query and 4 KV heads of 64: 128 behind 3789 44 / 58; 512 behind 1069 29 / 34; 1024 and
+//   4096 behind 0 25 / 25 and 74 / 122.
 constexpr int kImageQueryTiles = 4;
 constexpr int kImageKeyTiles = 8;
 constexpr size_t kSmemLimit = 232448;

@@ -19,8 +19,8 @@
 // What bounds it: the chain of a key tile, S from tensor memory, its maximum, the
 // exchange between the two warps of a row, exponentials, P back, at eight softmax warps
 // an SM; the tensor core is busy 40 % of the time.  A prompt of 4096 tokens with 32
-// query and 8 KV heads of 128 takes 155 us, 887 TFLOP/s, about 8 us of them for the images; of
-// 16384 tokens 1627 us, 1352 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
+// query and 8 KV heads of 128 takes 158 us, 870 TFLOP/s, about 8 us of them for the images; of
+// 16384 tokens 1662 us, 1323 TFLOP/s.  (bfloat16 caches: 116 and 1455 us.)
 //
 // Warp roles (16 warps): warp 0 copies K and Meta, warp 1 V; warp 2 owns the tensor
 // memory and issues Q K^T, warp 3 issues P V; warps 4-11 run the softmax and the
