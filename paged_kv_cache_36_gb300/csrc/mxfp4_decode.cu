@@ -814,8 +814,9 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
                     float x = fmaxf(fmaxf(z[cc], z[2 + cc]), -1e30f);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-                    z[cc] -= x;
-                    z[2 + cc] -= x;
+                    // (above the largest: not in any product)
+                    z[cc] = z[cc] < -1e29f ? 1.f : z[cc] - x;
+                    z[2 + cc] = z[2 + cc] < -1e29f ? 1.f : z[2 + cc] - x;
                     zm[cc] = x;
                   }
                   // 26 binades of them at a time: f16's normal numbers below 2^13

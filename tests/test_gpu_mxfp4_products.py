@@ -201,3 +201,16 @@ def test_large_keys_with_small_queries(kind, keys, queries):
     s.scale = 2.0 ** min(3 - keys - queries, 8) / 8
     s.upload()
     check(_attend(s), *reference(s))
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("lo, hi", [(-20, 3), (-60, 3), (0, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_far_apart_with_uneven_values(kind, lo, hi, d):
+    """Keys whose scales are 2^lo to 2^hi, values whose first group is 2^40 above the others."""
+    s = Step(11, KINDS[kind], 8, 2, d)
+    for r, slots in enumerate(s.slots):
+        s.pools.scales(s.rng, slots, lo, hi, v=False)
+        _uneven(s, r, slice(0, None, 3))
+    s.upload()
+    check(_attend(s), *reference(s))
