@@ -462,6 +462,133 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
                                      size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The 8-bit paged cache (e4m3, a scale for each block and KV head)  [the same paged
+ * layout and slot rule as above, half the bytes of bfloat16: AI Infra, section "Paged
+ * Attention"]
+ *
+ * One layer's key cache and value cache are each uint8 [num_blocks,
+ * pkv_fp8_block_bytes()], contiguous and 16-byte aligned, and zero (or another valid
+ * cache) before their first use; block_size 16, head_dim 64 or 128, any number of KV
+ * heads.  The 16 rows of a block of one KV head share a scale byte e, and a value is code
+ * * 2^(e - 127) with an 8-bit e4m3 code (four significant bits, up to 448, code 0x7f and
+ * 0xff NaN); a byte outside [10, 246] counts as the nearer end.  Every value is exact in
+ * bfloat16.
+ *
+ * Block bytes.  KV head h owns bytes [h C, (h + 1) C), C = 16 head_dim + 16: the codes,
+ * byte 16 head_dim the scale, 15 zero bytes.  With D = head_dim and P = D / 8
+ *   the K code of row t, dimension d is byte ((t / 8) (D / 64) + d / 64) 512 + (t % 8) 64 + d % 64,
+ *   the V code byte (d % P) / 4 512 + ((d / P) 4 + (t % 8) / 2) 16 + (d % 4) 4 + (t / 8) 2 + t % 2.
+ * A block is self-contained, so pkv_copy_blocks moves blocks of such pools
+ * (block_bytes = pkv_fp8_block_bytes()).
+ * ---------------------------------------------------------------------- */
+/* Bytes of one block of one cache, or 0 for a shape that is not supported. */
+int64_t pkv_fp8_block_bytes(int32_t block_size, int32_t num_kv_heads, int32_t head_dim);
+
+/* pkv_reshape_and_cache into the 8-bit cache.  Arguments, padding (a negative slot) and
+ * PKV_ERR_SLOT as there; dtype is the one of key and value (PKV_BF16 or PKV_F32).  In each
+ * block, KV head and cache (K or V) that gets rows, for the rows x of this call
+ *   e = max(e of the block, the smallest e' >= 10 with max |x| <= 448 2^(e' - 127)), 246 at most;
+ *   code = x 2^(127 - e), rounded to nearest even, saturating at +-448,
+ * where NaN and infinities do not count for the maximum and become NaN codes.  Rows that the
+ * block holds already keep their codes, or where e has grown are rounded to the new scale
+ * (which changes nothing but codes that fall below 2^-6: an absolute error of 2^(e - 127)
+ * 2^-10 each time, less than 2^(e - 127) 2^-9 in all).  A call that writes row 0 of a block
+ * begins it anew: the block's own e does not count, and rows that the call does not write
+ * become zero.  (Blocks fill from row 0, so a recycled one forgets its old scale.)
+ * Of a slot given twice the last of its tokens counts; the result does not depend on the
+ * order of the others.  A call whose tokens are not in the order of their blocks costs a
+ * search of all slots for each token: num_tokens^2 / 32 steps of a warp. */
+int pkv_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_stride,
+                              int64_t value_stride, void* key_cache, void* value_cache,
+                              const int64_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                              int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t dtype, uint32_t* error_word, void* stream);
+
+/* pkv_rope_reshape_and_cache into the 8-bit cache: query [num_tokens, num_heads, head_dim]
+ * is rotated to query_out (which may be query itself, with its stride; else it shares no
+ * byte with query, key or value, and dimensions >= rotary_dim are copied), and the rotated
+ * keys and the values are quantised as by pkv_reshape_and_cache_fp8, from the rotation's
+ * float32.  Table, layouts, rotary_dim and alignment as there.  A token whose position is
+ * outside [0, max_position) sets PKV_ERR_POSITION, and neither its query_out row nor its slot is written. */
+int pkv_rope_reshape_and_cache_fp8(const int64_t* positions, const void* query, int64_t query_stride,
+                                   void* query_out, int64_t query_out_stride, int32_t num_heads,
+                                   const void* key, int64_t key_stride, const void* value,
+                                   int64_t value_stride, void* key_cache, void* value_cache,
+                                   const int64_t* slot_mapping, const float* cos_sin_cache,
+                                   int64_t max_position, int32_t rotary_dim, int32_t is_neox,
+                                   int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                                   uint32_t* error_word, void* stream);
+
+/* The inverse: key_out[t] and value_out[t] (dtype PKV_BF16 or PKV_F32, token strides in
+ * elements) receive the values at slot_mapping[t], exactly.  A negative slot leaves the
+ * token's output rows as they were; a slot past the pool gives zeros and sets
+ * PKV_ERR_SLOT. */
+int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
+                         const int64_t* slot_mapping, void* key_out, void* value_out,
+                         int64_t key_out_stride, int64_t value_out_stride, int64_t num_tokens,
+                         int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t dtype, uint32_t* error_word, void* stream);
+
+/* pkv_paged_attention_varlen over 8-bit caches: the same definition with K and V the
+ * values the caches stand for, sums and softmax in float32.  q and out are bfloat16;
+ * num_heads / num_kv_heads may be any integer up to 16; at most 8192 requests.  A
+ * block_table row has max_blocks_per_req <= block_table_stride entries.  max_query_len as
+ * there (1: every row is a decode row; longer ones are then not computed).  Rows of a
+ * request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
+ * request, are left as they were; a block id outside the pool reads as zeros
+ * (PKV_ERR_BLOCK_ID).  A request with several query tokens has 2^31 - 256 keys at most.
+ * Bytes of tokens past a request's end may hold anything; a NaN in a key or value counts
+ * for the rows that see it, and for no others.
+ *
+ * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch, its first
+ * 256 bytes zero before its first use, word 0 the error word; two calls that overlap on the
+ * GPU must not share one.  All arguments, the metadata among them, are read only after the
+ * work before the call on `stream`. */
+size_t pkv_fp8_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
+int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* key_cache,
+                                   const void* value_cache, const int32_t* block_table,
+                                   int32_t block_table_stride, int32_t max_blocks_per_req,
+                                   const int32_t* query_start_loc, const int32_t* seq_lens,
+                                   const int32_t* num_computed_tokens, float scale, void* out,
+                                   int64_t out_stride, int64_t num_tokens, int32_t num_reqs,
+                                   int64_t num_blocks, int32_t block_size, int32_t num_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t max_query_len,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The table of rotary angles  [AI Infra, section "Attention Module (以标准GQA + RoPE为例)":
+ * the precomputed cos_sin_cache [max_position_embeddings, rotary_dim]]
+ *
+ * out [num_positions, rotary_dim] float32, 16-byte aligned: row p is attention_factor times
+ * the cosines, then the sines, of the angles (start + p) f_i, i < rotary_dim / 2, with
+ * w_i = base^(-2 i / rotary_dim), s = factor, L = original_max_position and
+ *   PKV_ROPE_NONE    f_i = w_i;
+ *   PKV_ROPE_LINEAR  f_i = w_i / s (positions interpolated);
+ *   PKV_ROPE_NTK     w_i of the base  base s^(rotary_dim / (rotary_dim - 2));
+ *   PKV_ROPE_PARTS   f_i = g_i w_i + (1 - g_i) w_i / s, g_i = clamp((L w_i / 2 pi - low) /
+ *                    (high - low), 0, 1): what turns often within L stays, what turns
+ *                    seldom is interpolated;
+ *   PKV_ROPE_YARN    the same with g_i = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1), a ramp over the
+ *                    pairs: a = floor(c(high)), 0 at least, b = ceil(c(low)), rotary_dim - 1
+ *                    at most, c(n) = rotary_dim log(L / 2 pi n) / (2 log base), the pair
+ *                    that makes n turns.
+ * Frequencies, angles and their remainders are 64-bit; entries are off by 2^-23 of
+ * attention_factor at most.  base > 1; factor >= 1 (but for PKV_ROPE_NONE); 0 < low < high and L > 0
+ * (PARTS and YARN); rotary_dim even, 512 at most (NTK: 4 at least); start + num_positions <= 2^26.
+ * ---------------------------------------------------------------------- */
+#define PKV_ROPE_NONE 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_NTK 2
+#define PKV_ROPE_PARTS 3
+#define PKV_ROPE_YARN 4
+
+int pkv_build_cos_sin_cache(float* out, int64_t num_positions, int64_t start, int32_t rotary_dim,
+                            double base, int32_t scaling, double factor,
+                            int64_t original_max_position, double low, double high,
+                            double attention_factor, void* stream);
+
+/* ------------------------------------------------------------------------
  * Step metadata (device)  [显存调度, section "分配是词元计划的一部分": delta_i =
  * ceil((T_i + s_i) / B) - ceil(T_i / B), all of a plan's blocks from the front of
  * the free list or none; AI Infra, section "Paged Attention": the slot rule]

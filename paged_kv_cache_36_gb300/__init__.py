@@ -25,6 +25,9 @@ __all__ = [
     "PreparedCall", "prepare_reshape_and_cache_paged_attention",
     "mxfp4_block_bytes", "new_cache_mxfp4", "reshape_and_cache_mxfp4", "gather_cache_mxfp4",
     "mxfp4_attention_workspace_bytes", "new_workspace_mxfp4", "paged_attention_varlen_mxfp4",
+    "fp8_block_bytes", "new_cache_fp8", "reshape_and_cache_fp8", "rope_reshape_and_cache_fp8",
+    "gather_cache_fp8", "fp8_attention_workspace_bytes", "new_workspace_fp8",
+    "paged_attention_varlen_fp8", "build_cos_sin_cache",
     "build_step_metadata",
     "build_slot_mapping", "Allocator", "Scheduler",
 ]
@@ -368,23 +371,26 @@ def new_cache_mxfp4(num_blocks: int, num_kv_heads: int, head_dim: int, device="c
             torch.zeros(shape, dtype=torch.uint8, device=device))
 
 
-def _check_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int) -> None:
+def _check_pools(where: str, key_cache, value_cache, num_kv_heads: int, head_dim: int,
+                 block_bytes=mxfp4_block_bytes) -> None:
     import torch
     if head_dim != 64 and head_dim != 128:
         raise ValueError(f"{where}: head_dim must be 64 or 128, not {head_dim}")
-    shape = (key_cache.shape[0], mxfp4_block_bytes(num_kv_heads, head_dim))
+    shape = (key_cache.shape[0], block_bytes(num_kv_heads, head_dim))
     _expect(where, "key_cache", key_cache, torch.uint8, shape)
     _expect(where, "value_cache", value_cache, torch.uint8, shape)
 
 
-def _rows_and_pools(where: str, key, value, key_cache, value_cache, slot_mapping, error_word):
+def _rows_and_pools(where: str, key, value, key_cache, value_cache, slot_mapping, error_word,
+                    block_bytes=mxfp4_block_bytes):
     """(device index, T, num_blocks, Hkv, D, dtype code) of K and V rows [T, Hkv, D]
     with their caches and slots."""
     import torch
     T, hkv, d = key.shape
     nb = key_cache.shape[0]
-    # 16 tokens of head_dim / 2 code bytes and head_dim / 32 scale bytes per KV head
-    pool = (nb, hkv * d * 17 // 2)
+    # 16 tokens of head_dim / 2 code bytes and head_dim / 32 scale bytes per KV head, or of
+    # head_dim code bytes and 16 for the scale
+    pool = (nb, hkv * d * 17 // 2 if block_bytes is mxfp4_block_bytes else hkv * (d + 1) * 16)
     dev = key.get_device()
     u8, dtype = torch.uint8, key.dtype
     if not (dev >= 0 and value.shape == key.shape and value.dtype is dtype
@@ -398,7 +404,7 @@ def _rows_and_pools(where: str, key, value, key_cache, value_cache, slot_mapping
             and (error_word is None or error_word.get_device() == dev)):
         if value.shape != key.shape or value.dtype is not dtype:
             raise ValueError(f"{where}: the K and the V rows must have one shape and dtype")
-        _check_pools(where, key_cache, value_cache, hkv, d)
+        _check_pools(where, key_cache, value_cache, hkv, d, block_bytes)
         _expect(where, "slot_mapping", slot_mapping, torch.int64, (T,))
         _check_device(where, dev, value, key_cache, value_cache, slot_mapping, error_word)
     return dev, T, nb, hkv, d, PKV_BF16 if dtype is torch.bfloat16 else _dtype_code(key)
@@ -459,12 +465,22 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
     flattened batch q [T, H, D] (bfloat16), up to 16 query heads per KV head.
     The number of KV heads is the one the caches' block size gives.  Returns
     out [T, H, D]; rows that belong to no request are left as they were."""
+    return _attend_quantised("paged_attention_varlen_mxfp4", "pkv_paged_attention_varlen_mxfp4",
+                             mxfp4_block_bytes, new_workspace_mxfp4, lambda D: 17 * D // 2, q, key_cache,
+                             value_cache, block_table, query_start_loc, seq_lens, num_computed_tokens,
+                             scale, out, workspace, max_query_len, stream)
+
+
+def _attend_quantised(where: str, name: str, block_bytes, new_workspace_of, head_bytes, q, key_cache,
+                      value_cache, block_table, query_start_loc, seq_lens, num_computed_tokens, scale,
+                      out, workspace, max_query_len, stream):
+    """The attention call over 4-bit or 8-bit caches whose blocks hold head_bytes(D) a KV head."""
     import torch
-    where = "paged_attention_varlen_mxfp4"
     T, H, D = q.shape
-    hkv = max(1, key_cache.shape[1] * 2 // (17 * max(1, D)))
+    chunk = head_bytes(max(2, D))
+    hkv = max(1, key_cache.shape[1] // chunk)
     nb, R = key_cache.shape[0], seq_lens.shape[0]
-    pool = (nb, hkv * D * 17 // 2)
+    pool = (nb, hkv * chunk)
     dev = q.get_device()
     u8, i32 = torch.uint8, torch.int32
     if not (dev >= 0 and q.dtype is torch.bfloat16
@@ -480,7 +496,7 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
             and key_cache.get_device() == dev == value_cache.get_device()
             and block_table.get_device() == dev == query_start_loc.get_device()
             and seq_lens.get_device() == dev == num_computed_tokens.get_device()):
-        _check_pools(where, key_cache, value_cache, hkv, D)
+        _check_pools(where, key_cache, value_cache, hkv, D, block_bytes)
         if q.dtype is not torch.bfloat16:
             raise TypeError(f"{where}: q must be bfloat16")
         if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != R:
@@ -495,17 +511,174 @@ def paged_attention_varlen_mxfp4(q, key_cache, value_cache, block_table, query_s
             if out is None:
                 out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
             if workspace is None:
-                workspace = new_workspace_mxfp4(H, hkv, D, q.device)
+                workspace = new_workspace_of(H, hkv, D, q.device)
     if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError(f"{where}: out must have q's shape and dtype")
     if out.get_device() != dev or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"{where}: out and a contiguous workspace must be on q's CUDA device")
-    _device_call(where, "pkv_paged_attention_varlen_mxfp4", dev, stream, q.data_ptr(),
+    _device_call(where, name, dev, stream, q.data_ptr(),
                  _token_stride(q), key_cache.data_ptr(), value_cache.data_ptr(),
                  block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
                  query_start_loc.data_ptr(), seq_lens.data_ptr(), num_computed_tokens.data_ptr(),
                  float(scale), out.data_ptr(), _token_stride(out), T, R, nb, 16, H, hkv, D, int(max_query_len),
                  workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit paged cache and the table of rotary angles
+# ---------------------------------------------------------------------------
+def fp8_block_bytes(num_kv_heads: int, head_dim: int, block_size: int = 16) -> int:
+    """Bytes of one block of one 8-bit cache."""
+    n = int(lib().pkv_fp8_block_bytes(block_size, num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no 8-bit cache of {num_kv_heads} KV heads of {head_dim} in blocks of "
+                         f"{block_size}: head_dim is 64 or 128, block_size 16")
+    return n
+
+
+def new_cache_fp8(num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """(key_cache, value_cache): zeroed 8-bit caches, uint8 [num_blocks, block bytes]."""
+    import torch
+    shape = (num_blocks, fp8_block_bytes(num_kv_heads, head_dim))
+    return (torch.zeros(shape, dtype=torch.uint8, device=device),
+            torch.zeros(shape, dtype=torch.uint8, device=device))
+
+
+def reshape_and_cache_fp8(key, value, key_cache, value_cache, slot_mapping, error_word=None,
+                          stream=None) -> None:
+    """Quantise key/value [T, Hkv, D] (bfloat16 or float32) into the 8-bit caches
+    (new_cache_fp8) at slot_mapping[T] (int64; negative: padding).  The rows of a block and
+    KV head share a scale, which grows with them; writing row 0 begins the block anew."""
+    where = "reshape_and_cache_fp8"
+    err = _error_ptr(where, error_word)
+    dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key, value, key_cache, value_cache,
+                                                slot_mapping, error_word, fp8_block_bytes)
+    _device_call(where, "pkv_reshape_and_cache_fp8", dev, stream, key.data_ptr(),
+                 value.data_ptr(), _token_stride(key), _token_stride(value), key_cache.data_ptr(),
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), T, nb, 16, hkv, d, dtype, err)
+
+
+def rope_reshape_and_cache_fp8(positions, query, key, value, key_cache, value_cache, slot_mapping,
+                               cos_sin_cache, is_neox: bool = True, query_out=None,
+                               error_word=None, stream=None) -> None:
+    """Rotate query [T, H, D] (in place, or to query_out) and key [T, Hkv, D] by
+    cos_sin_cache[positions] (float32 [max_position, rotary_dim], as build_cos_sin_cache
+    makes it), and quantise the rotated key and the value into the 8-bit caches at
+    slot_mapping (int64 [T]) as reshape_and_cache_fp8 does."""
+    import torch
+    where = "rope_reshape_and_cache_fp8"
+    err = _error_ptr(where, error_word)
+    if query_out is None:
+        query_out = query
+    T, d, dev = key.shape[0], key.shape[2], key.get_device()
+    if not (query.dim() == 3 and query.shape[0] == T and query.shape[2] == d
+            and query.dtype is key.dtype and query_out.shape == query.shape
+            and query_out.dtype is query.dtype and positions.dtype is torch.int64
+            and positions.shape == (T,) and positions.is_contiguous()
+            and cos_sin_cache.dtype is torch.float32 and cos_sin_cache.dim() == 2
+            and cos_sin_cache.is_contiguous() and query.get_device() == dev == positions.get_device()
+            and query_out.get_device() == dev == cos_sin_cache.get_device()):
+        if query.dim() != 3 or query.shape[0] != T or query.shape[2] != d or query.dtype is not key.dtype:
+            raise ValueError(f"{where}: query must be [{T}, H, {d}] of key's dtype")
+        if query_out.shape != query.shape or query_out.dtype is not query.dtype:
+            raise ValueError(f"{where}: query_out must have query's shape and dtype")
+        _expect(where, "positions", positions, torch.int64, (T,))
+        if cos_sin_cache.dtype is not torch.float32:
+            raise TypeError(f"{where}: cos_sin_cache must be float32, not {cos_sin_cache.dtype}")
+        if cos_sin_cache.dim() != 2 or not cos_sin_cache.is_contiguous():
+            raise ValueError(f"{where}: cos_sin_cache must be a contiguous [max_position, rotary_dim]")
+        _check_device(where, dev, query, query_out, positions, cos_sin_cache)
+    dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key, value, key_cache, value_cache,
+                                                slot_mapping, error_word, fp8_block_bytes)
+    _device_call(where, "pkv_rope_reshape_and_cache_fp8", dev, stream, positions.data_ptr(),
+                 query.data_ptr(), _token_stride(query), query_out.data_ptr(), _token_stride(query_out),
+                 query.shape[1], key.data_ptr(), _token_stride(key), value.data_ptr(),
+                 _token_stride(value), key_cache.data_ptr(), value_cache.data_ptr(),
+                 slot_mapping.data_ptr(), cos_sin_cache.data_ptr(), cos_sin_cache.shape[0],
+                 cos_sin_cache.shape[1], int(bool(is_neox)), T, nb, 16, hkv, d, dtype, err)
+
+
+def gather_cache_fp8(key_cache, value_cache, slot_mapping, key_out, value_out, error_word=None,
+                     stream=None):
+    """Read the rows at slot_mapping[T] (int64; negative: the row of the outputs is left
+    alone) back from the 8-bit caches into key_out and value_out [T, Hkv, D], bfloat16 or
+    float32; exact.  Returns (key_out, value_out)."""
+    where = "gather_cache_fp8"
+    err = _error_ptr(where, error_word)
+    dev, T, nb, hkv, d, dtype = _rows_and_pools(where, key_out, value_out, key_cache, value_cache,
+                                                slot_mapping, error_word, fp8_block_bytes)
+    _device_call(where, "pkv_gather_cache_fp8", dev, stream, key_cache.data_ptr(),
+                 value_cache.data_ptr(), slot_mapping.data_ptr(), key_out.data_ptr(),
+                 value_out.data_ptr(), _token_stride(key_out), _token_stride(value_out), T, nb, 16,
+                 hkv, d, dtype, err)
+    return key_out, value_out
+
+
+def fp8_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    n = int(lib().pkv_fp8_attention_workspace_bytes(num_heads, num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no attention over 8-bit caches of {num_heads}/{num_kv_heads} heads of "
+                         f"{head_dim}: up to 16 whole query heads per KV head, head_dim 64 or 128")
+    return n
+
+
+def new_workspace_fp8(num_heads: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """A workspace of paged_attention_varlen_fp8, for any batch."""
+    import torch
+    ws = torch.empty(fp8_attention_workspace_bytes(num_heads, num_kv_heads, head_dim),
+                     dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the error word
+    return ws
+
+
+def paged_attention_varlen_fp8(q, key_cache, value_cache, block_table, query_start_loc, seq_lens,
+                               num_computed_tokens, scale: float, out=None, workspace=None,
+                               max_query_len: int = 0, stream=None):
+    """paged_attention_varlen over the 8-bit caches: causal GQA attention of the flattened
+    batch q [T, H, D] (bfloat16), up to 16 query heads per KV head.  The number of KV heads
+    is the one the caches' block size gives.  Returns out [T, H, D]; rows that belong to no
+    request are left as they were."""
+    return _attend_quantised("paged_attention_varlen_fp8", "pkv_paged_attention_varlen_fp8",
+                             fp8_block_bytes, new_workspace_fp8, lambda D: 16 * (D + 1), q, key_cache,
+                             value_cache, block_table, query_start_loc, seq_lens, num_computed_tokens,
+                             scale, out, workspace, max_query_len, stream)
+
+
+def build_cos_sin_cache(max_position: int, rotary_dim: int, base: float = 10000.0,
+                        scaling: str = "none", factor: float = 1.0, original_max_position: int = 0,
+                        low: float = 1.0, high: float = 32.0, attention_factor: float | None = None,
+                        start: int = 0, out=None, device="cuda", stream=None):
+    """The table that the RoPE calls read, float32 [max_position, rotary_dim]: row p has the
+    cosines, then the sines, of position start + p (start: to extend a table), times
+    attention_factor.  scaling for contexts `factor` times as long: "none"; "linear"
+    (positions interpolated); "ntk" (a larger base); "parts" (pairs that turn less than `low`
+    times within original_max_position interpolated, those that turn more than `high` times
+    kept, mixed in between); "yarn" (mixed over the pairs' indices instead;
+    attention_factor is 0.1 ln(factor) + 1 unless given, else 1)."""
+    import math
+
+    import torch
+    where = "build_cos_sin_cache"
+    if scaling not in _ffi.ROPE_SCALINGS:
+        raise ValueError(f"{where}: scaling must be one of {', '.join(_ffi.ROPE_SCALINGS)}, not {scaling!r}")
+    n, rd = int(max_position), int(rotary_dim)
+    if n < 0 or rd <= 0:
+        raise ValueError(f"{where}: a table of {n} positions of {rd}")
+    if attention_factor is None:
+        attention_factor = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor >= 1.0 else 1.0
+    if out is None:
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"{where}: the table is made on a CUDA device, not on {device}")
+        index = torch.cuda.current_device() if device.index is None else device.index
+        with _allocating_on(index, stream):
+            out = torch.empty((n, rd), dtype=torch.float32, device=torch.device("cuda", index))
+    _expect(where, "out", out, torch.float32, (n, rd))
+    _check_device(where, out.get_device())
+    _device_call(where, "pkv_build_cos_sin_cache", out.get_device(), stream, out.data_ptr(), n, int(start),
+                 rd, float(base), _ffi.ROPE_SCALINGS[scaling], float(factor), int(original_max_position),
+                 float(low), float(high), float(attention_factor))
     return out
 
 

@@ -17,6 +17,7 @@ ERRORS = {
     -5: "PKV_E_STATE", -6: "PKV_E_UNKNOWN_REQ", -7: "PKV_E_CUDA", -8: "PKV_E_CAPACITY",
 }
 PKV_F32, PKV_BF16 = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
 ERR_BLOCK_ID, ERR_SLOT, ERR_METADATA, ERR_TIMEOUT, ERR_POSITION, ERR_NO_BLOCKS = \
     1, 2, 4, 8, 16, 32
 
@@ -83,6 +84,18 @@ SIGNATURES = {
     "pkv_paged_attention_varlen_mxfp4": (C.c_int, [vp, i64, vp, vp, vp, i32, i32, vp, vp, vp, f32, vp,
                                                    i64, i64, i32, i64, i32, i32, i32, i32, i32,
                                                    vp, sz, vp]),
+    "pkv_fp8_block_bytes": (i64, [i32, i32, i32]),
+    "pkv_reshape_and_cache_fp8": (C.c_int, [vp, vp, i64, i64, vp, vp, vp, i64, i64, i32, i32,
+                                            i32, i32, vp, vp]),
+    "pkv_rope_reshape_and_cache_fp8": (C.c_int, [vp, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, vp, vp,
+                                                 vp, i64, i32, i32, i64, i64, i32, i32, i32, i32, vp, vp]),
+    "pkv_gather_cache_fp8": (C.c_int, [vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, i32,
+                                       i32, vp, vp]),
+    "pkv_fp8_attention_workspace_bytes": (sz, [i32, i32, i32]),
+    "pkv_paged_attention_varlen_fp8": (C.c_int, [vp, i64, vp, vp, vp, i32, i32, vp, vp, vp, f32, vp,
+                                                 i64, i64, i32, i64, i32, i32, i32, i32, i32,
+                                                 vp, sz, vp]),
+    "pkv_build_cos_sin_cache": (C.c_int, [vp, i64, i64, i32, f64, i32, f64, i64, f64, f64, f64, vp]),
     "pkv_build_step_metadata": (C.c_int, [vp, vp, i32, vp, i32, i32, vp, i64, vp, vp, i32, i64, vp, vp,
                                           vp, vp, vp, vp]),
     "pkv_build_slot_mapping": (C.c_int, [vp, i32, vp, vp, i32, i32, vp, i64]),

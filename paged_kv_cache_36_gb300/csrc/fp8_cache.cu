@@ -1,0 +1,561 @@
+// reshape_and_cache into the 8-bit paged cache, alone or with RoPE, and its inverse.
+//
+// The rows that a call writes to one block and KV head share a scale (fp8.cuh), and with
+// those that the block holds already:
+//   e = max(e_old, smallest e' with max |x| <= 448 2^(e' - 127)),  code = RNE_e4m3(x 2^(127 - e)).
+// A call that writes row 0 of a block begins it anew: there is no e_old, and rows that it
+// does not write become zero.  Where e grows, the rows that stay are rounded again,
+// RNE(code 2^(e_old - e)); being powers of two, scales move only what falls below e4m3's
+// normal numbers.  A NaN or an infinity has the code for NaN, which reads as NaN, and does
+// not count for the scale.
+//
+// Who writes what.  A block is written by one warp per (KV head, K or V), whichever tokens
+// of the call go to it: a CTA takes a window of tokens, finds those whose block the token
+// before them does not share, and searches the call's slots for the blocks' other tokens.
+// The block is its own if none of them comes earlier.  So there are no atomics and no
+// second pass, the result depends on no order, and of a slot given twice the last token
+// counts.  A batch in the order of its requests has one search per 16 tokens; in the worst
+// order there is one per token, T^2 / 32 steps of a warp.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fp8.cuh"
+#include "kernels.h"
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWindow = 16;  // tokens of a window, at most
+
+enum Rope { kNone, kHalf, kInterleaved };
+
+// Sixteen (or, D 64 values, eight) consecutive elements of a row.
+template <typename T, int N>
+struct Piece {
+  static constexpr int kVecs = N * sizeof(T) / 16;
+  static constexpr int kPer = 16 / sizeof(T);  // elements of a vector
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ float at(int i) const {  // i known when compiled
+    const uint4& u = v[i / kPer];
+    const int k = i % kPer;
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w);
+    } else {
+      const uint32_t w = k < 2 ? u.x : k < 4 ? u.y : k < 6 ? u.z : u.w;
+      return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+    }
+  }
+};
+
+// |x| as bits, 0 where x is NaN or infinite.
+__device__ __forceinline__ uint32_t magnitude(float x) {
+  const uint32_t m = __float_as_uint(x) & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
+}
+
+// x times a power of two, for the codes: infinities become NaN.
+__device__ __forceinline__ float scaled(float x, float inv) {
+  return (__float_as_uint(x) & 0x7fffffffu) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x * inv;
+}
+
+struct WriteParams {
+  const void* key;
+  const void* value;
+  int64_t key_stride;    // elements
+  int64_t value_stride;
+  uint8_t* key_cache;
+  uint8_t* value_cache;
+  const int64_t* slot_mapping;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t hkv;
+  int32_t window;        // tokens of a window
+  int32_t splits;        // CTAs of a window
+  int32_t cache_ctas;    // the CTAs after them rotate the queries
+  uint32_t* err;
+  // RoPE
+  const int64_t* positions;
+  const float* table;    // [max_position][rotary_dim]: cosines, sines
+  int64_t max_position;
+  int32_t rotary_dim;
+  int32_t heads;
+  const void* query;
+  void* query_out;
+  int64_t query_stride;
+  int64_t query_out_stride;
+};
+
+// M floats of the table (M even).
+template <int M>
+__device__ __forceinline__ void load_table(const float* p, float (&x)[M]) {
+  if constexpr (M % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < M; i += 4) *reinterpret_cast<float4*>(x + i) = __ldg(reinterpret_cast<const float4*>(p + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; i += 2) *reinterpret_cast<float2*>(x + i) = __ldg(reinterpret_cast<const float2*>(p + i));
+  }
+}
+
+// The vector of elements d .. of a row, rotated by the angles of its table row `cs`.
+template <typename T, Rope kRope>
+__device__ __forceinline__ void rotated(const T* row, int d, const float* cs, int rd,
+                                        float (&y)[16 / sizeof(T)]) {
+  constexpr int N = 16 / sizeof(T);
+  Piece<T, N> a;
+  a.load(row + d);
+  if (d >= rd) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = a.at(i);
+    return;
+  }
+  const int half = rd >> 1;
+  if constexpr (kRope == kHalf) {
+    const bool upper = d >= half;
+    const int at = upper ? d - half : d;
+    Piece<T, N> b;
+    b.load(row + (upper ? at : d + half));
+    float c[N], s[N];
+    load_table<N>(cs + at, c);
+    load_table<N>(cs + half + at, s);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      y[i] = upper ? a.at(i) * c[i] + b.at(i) * s[i] : a.at(i) * c[i] - b.at(i) * s[i];
+  } else {
+    float c[N / 2], s[N / 2];
+    load_table<N / 2>(cs + d / 2, c);
+    load_table<N / 2>(cs + half + d / 2, s);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      y[i] = a.at(i) * c[i / 2] - a.at(i + 1) * s[i / 2];
+      y[i + 1] = a.at(i + 1) * c[i / 2] + a.at(i) * s[i / 2];
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// The scale of a chunk that gets rows of magnitude `amax`; *grown: by how much the rows
+// that stay have to come down (0 where there are none).  One warp.
+__device__ __forceinline__ int new_scale(const uint8_t* head, bool anew, uint32_t amax, int* grown) {
+  const int e_new = f8_scale_of(amax);
+  if (anew) {
+    *grown = 0;
+    return e_new;
+  }
+  const int e_old = f8_scale(*head);
+  *grown = max(e_new - e_old, 0);
+  return max(e_new, e_old);
+}
+
+// One block's keys of KV head h: rows[t] is the token whose key row t becomes, or -1.
+template <typename T, int D, Rope kRope>
+__device__ __forceinline__ void write_keys(const WriteParams& p, int64_t blk, int h, const int* rows, int lane) {
+  constexpr int NV = D / 32;  // pieces of 16 codes a lane
+  uint8_t* chunk = p.key_cache + (blk * p.hkv + h) * f8_chunk_bytes(D);
+  const T* key = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D + (lane & 3) * 16;
+  int tok[2] = {rows[lane >> 2], rows[(lane >> 2) + 8]};
+  const bool anew = rows[0] >= 0;
+  Piece<T, 16> raw[kRope == kNone ? NV : 1];
+  float rot[kRope == kNone ? 1 : NV][16];
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int t = tok[j / (D / 64)], d = 64 * (j % (D / 64));
+    if constexpr (kRope == kNone) {
+      if (t >= 0) raw[j].load(key + t * p.key_stride + d);
+      else raw[j].zero();
+    } else {
+      constexpr int N = 16 / sizeof(T);
+      if (t >= 0) {
+        const float* cs = p.table + __ldg(p.positions + t) * p.rotary_dim;
+        const T* row = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D + t * p.key_stride;
+#pragma unroll
+        for (int i = 0; i < 16; i += N)
+          rotated<T, kRope>(row, d + (lane & 3) * 16 + i, cs, p.rotary_dim,
+                            *reinterpret_cast<float(*)[N]>(&rot[j][i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rot[j][i] = 0.f;
+      }
+    }
+  }
+  auto x = [&](int j, int i) -> float {
+    if constexpr (kRope == kNone) return raw[j].at(i); else return rot[j][i];
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max(amax, magnitude(x(j, i)));
+  int grown;
+  const int e = new_scale(chunk + f8_code_bytes(D), anew, warp_max(amax), &grown);
+  const float inv = f8_pow2(127 - e);
+  const float down = f8_pow2(max(-grown, -126));
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    uint4* at = reinterpret_cast<uint4*>(chunk + j * 512 + lane * 16);
+    if (tok[j / (D / 64)] >= 0) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = f32x4_to_e4m3(scaled(x(j, 4 * i), inv), scaled(x(j, 4 * i + 1), inv),
+                             scaled(x(j, 4 * i + 2), inv), scaled(x(j, 4 * i + 3), inv));
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (anew) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else if (grown) {
+      const uint4 o = *at;
+      *at = make_uint4(e4m3x4_rescale(o.x, down), e4m3x4_rescale(o.y, down), e4m3x4_rescale(o.z, down),
+                       e4m3x4_rescale(o.w, down));
+    }
+  }
+  __syncwarp();
+  if (lane == 0)
+    *reinterpret_cast<uint4*>(chunk + f8_code_bytes(D)) = make_uint4(static_cast<uint32_t>(e), 0u, 0u, 0u);
+}
+
+// One block's values of KV head h.
+template <typename T, int D>
+__device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, int h, const int* rows, int lane) {
+  constexpr int P = D / 8;  // dimensions a lane has of each of its four tokens
+  uint8_t* chunk = p.value_cache + (blk * p.hkv + h) * f8_chunk_bytes(D);
+  const T* value = static_cast<const T*>(p.value) + static_cast<int64_t>(h) * D + (lane >> 2) * P;
+  const bool anew = rows[0] >= 0;
+  Piece<T, P> raw[4];
+  uint32_t keep = 0u;  // bytes of a word that stay
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = rows[2 * (lane & 3) + (i >> 1) * 8 + (i & 1)];
+    if (t >= 0) {
+      raw[i].load(value + t * p.value_stride);
+    } else {
+      raw[i].zero();
+      keep |= 0xffu << (8 * i);
+    }
+  }
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int d = 0; d < P; ++d) amax = max(amax, magnitude(raw[i].at(d)));
+  int grown;
+  const int e = new_scale(chunk + f8_code_bytes(D), anew, warp_max(amax), &grown);
+  const float inv = f8_pow2(127 - e);
+  const float down = f8_pow2(max(-grown, -126));
+  if (anew || grown || keep != 0xffffffffu) {
+#pragma unroll
+    for (int j = 0; j < P / 4; ++j) {
+      uint4* at = reinterpret_cast<uint4*>(chunk + j * 512 + lane * 16);
+      uint4 o = make_uint4(0u, 0u, 0u, 0u);
+      if (!anew && keep != 0u) o = *at;
+      uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (grown) w[i] = e4m3x4_rescale(w[i], down);
+        const uint32_t n = f32x4_to_e4m3(scaled(raw[0].at(4 * j + i), inv), scaled(raw[1].at(4 * j + i), inv),
+                                         scaled(raw[2].at(4 * j + i), inv), scaled(raw[3].at(4 * j + i), inv));
+        w[i] = (w[i] & keep) | (n & ~keep);
+      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __syncwarp();
+  if (lane == 0)
+    *reinterpret_cast<uint4*>(chunk + f8_code_bytes(D)) = make_uint4(static_cast<uint32_t>(e), 0u, 0u, 0u);
+}
+
+// Rotates the query heads of every token whose position is in the table: a thread takes a
+// vector of them, or two that hold the pairs.
+template <typename T, int D, Rope kRope>
+__device__ __forceinline__ void rotate_queries(const WriteParams& p, int64_t first, int64_t step) {
+  constexpr int N = 16 / sizeof(T);
+  const int rot = p.rotary_dim / N / (kRope == kHalf ? 2 : 1);  // items of a head that rotate
+  const bool in_place = p.query == p.query_out;
+  const int items = rot + (in_place ? 0 : (D - p.rotary_dim) / N);
+  const int64_t per_token = static_cast<int64_t>(p.heads) * items;
+  const int64_t total = p.num_tokens * per_token;
+  for (int64_t i = first; i < total; i += step) {
+    const int64_t t = i / per_token;
+    const int rem = static_cast<int>(i - t * per_token);
+    const int h = rem / items, j = rem - h * items;
+    const int64_t pos = __ldg(p.positions + t);
+    if (pos < 0 || pos >= p.max_position) continue;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + t * p.query_stride +
+                                                      static_cast<int64_t>(h) * D);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.query_out) + t * p.query_out_stride +
+                                          static_cast<int64_t>(h) * D);
+    // (plain loads: the rows may be rewritten in place)
+    if (j >= rot) {
+      const int at = p.rotary_dim / N + j - rot;
+      dst[at] = src[at];
+      continue;
+    }
+    auto store = [&](int at, const float (&y)[N]) {
+      if constexpr (sizeof(T) == 4)
+        dst[at] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+      else
+        dst[at] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    };
+    const float* cs = p.table + pos * p.rotary_dim;
+    const int half = p.rotary_dim >> 1;
+    Piece<T, N> a;
+    a.v[0] = src[j];
+    float y[N];
+    if constexpr (kRope == kHalf) {
+      Piece<T, N> b;
+      b.v[0] = src[j + rot];
+      float c[N], s[N], z[N];
+      load_table<N>(cs + j * N, c);
+      load_table<N>(cs + half + j * N, s);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        y[k] = a.at(k) * c[k] - b.at(k) * s[k];
+        z[k] = b.at(k) * c[k] + a.at(k) * s[k];
+      }
+      store(j, y);
+      store(j + rot, z);
+    } else {
+      float c[N / 2], s[N / 2];
+      load_table<N / 2>(cs + j * (N / 2), c);
+      load_table<N / 2>(cs + half + j * (N / 2), s);
+#pragma unroll
+      for (int k = 0; k < N; k += 2) {
+        y[k] = a.at(k) * c[k / 2] - a.at(k + 1) * s[k / 2];
+        y[k + 1] = a.at(k + 1) * c[k / 2] + a.at(k) * s[k / 2];
+      }
+      store(j, y);
+    }
+  }
+}
+
+template <typename T, int D, Rope kRope>
+__global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const WriteParams p) {
+  // a programmatic dependent of the kernel before it, which may still read the cache or
+  // write the new rows
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  if constexpr (kRope != kNone) {
+    if (static_cast<int>(blockIdx.x) >= p.cache_ctas) {
+      rotate_queries<T, D, kRope>(
+          p, static_cast<int64_t>(blockIdx.x - p.cache_ctas) * kThreads + threadIdx.x,
+          static_cast<int64_t>(gridDim.x - p.cache_ctas) * kThreads);
+      return;
+    }
+  }
+  __shared__ int block_of[kWindow], first_of[kWindow], taken[kWindow];
+  __shared__ int rows[kWindow][kF8Block];
+  __shared__ int found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int win = blockIdx.x / p.splits, split = blockIdx.x - win * p.splits;
+  const int T0 = win * p.window, n = min(p.window, p.num_tokens - T0);
+  // the block of token t, or -1 where it is not written
+  auto block_at = [&](int t, bool report) -> int {
+    const int64_t slot = __ldg(p.slot_mapping + t);
+    bool ok = slot >= 0 && slot < p.num_slots;
+    if constexpr (kRope != kNone) {
+      const int64_t pos = __ldg(p.positions + t);
+      if (pos < 0 || pos >= p.max_position) {
+        if (report && p.err) atomicOr(p.err, PKV_ERR_POSITION);
+        return -1;
+      }
+    }
+    if (report && slot >= p.num_slots && p.err) atomicOr(p.err, PKV_ERR_SLOT);
+    return ok ? static_cast<int>(slot / kF8Block) : -1;
+  };
+  if (warp == 0) {
+    int b = -1;
+    bool first = false;
+    if (lane < n) {
+      b = block_at(T0 + lane, split == 0);
+      first = b >= 0 && (T0 + lane == 0 || block_at(T0 + lane - 1, false) != b);
+    }
+    const unsigned leads = __ballot_sync(0xffffffffu, first);
+    if (first) {
+      const int k = __popc(leads & ((1u << lane) - 1u));
+      block_of[k] = b;
+      first_of[k] = T0 + lane;
+      taken[k] = 0;
+    }
+    if (lane == 0) found = __popc(leads);
+  }
+  for (int i = threadIdx.x; i < kWindow * kF8Block; i += kThreads) rows[i / kF8Block][i % kF8Block] = -1;
+  __syncthreads();
+  const int leads = found;
+  if (leads == 0) return;
+  // ---- the other tokens of those blocks ----
+  constexpr int kAhead = 4;
+  for (int base = threadIdx.x; base < p.num_tokens; base += kThreads * kAhead) {
+    int64_t slot[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = base + u * kThreads;
+      slot[u] = t < p.num_tokens ? __ldg(p.slot_mapping + t) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (slot[u] < 0 || slot[u] >= p.num_slots) continue;
+      const int b = static_cast<int>(slot[u] / kF8Block), t = base + u * kThreads;
+      for (int k = 0; k < leads; ++k) {
+        if (b != block_of[k]) continue;
+        if constexpr (kRope != kNone) {
+          if (block_at(t, false) < 0) continue;  // its position
+        }
+        if (t < first_of[k]) taken[k] = 1;
+        atomicMax(&rows[k][slot[u] % kF8Block], t);
+      }
+    }
+  }
+  __syncthreads();
+  const int per = 2 * p.hkv;
+  for (int i = split * (kThreads / 32) + warp; i < leads * per; i += p.splits * (kThreads / 32)) {
+    const int k = i / per, item = i - k * per;
+    if (taken[k]) continue;
+    if (item & 1) write_values<T, D>(p, block_of[k], item >> 1, rows[k], lane);
+    else write_keys<T, D, kRope>(p, block_of[k], item >> 1, rows[k], lane);
+  }
+}
+
+// One warp per token; every value is exact in either output type.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(
+    const uint8_t* __restrict__ key_cache, const uint8_t* __restrict__ value_cache,
+    const int64_t* __restrict__ slot_mapping, T* __restrict__ key_out, T* __restrict__ value_out,
+    int64_t key_stride, int64_t value_stride, int64_t num_tokens, int64_t num_slots, int32_t hkv,
+    uint32_t* __restrict__ err) {
+  grid_dependency_wait();  // the kernel before it may write the cache
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t wpb = kThreads / 32;
+  const int n = hkv * D / 4;  // fours of dimensions in a row
+  for (int64_t t = blockIdx.x * wpb + (threadIdx.x >> 5); t < num_tokens; t += gridDim.x * wpb) {
+    const int64_t slot = __ldg(slot_mapping + t);
+    if (slot < 0) continue;
+    const bool in = slot < num_slots;
+    if (!in && lane == 0 && err) atomicOr(err, PKV_ERR_SLOT);
+    const int row = static_cast<int>(slot & (kF8Block - 1));
+    const int64_t blk = in ? slot / kF8Block : 0;
+    for (int i = lane; i < n; i += 32) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
+      float k[4] = {}, v[4] = {};
+      if (in) {
+        const int64_t at = (blk * hkv + h) * f8_chunk_bytes(D);
+        const uint8_t* kc = key_cache + at;
+        const uint8_t* vc = value_cache + at;
+        e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(kc + f8_key_at<D>(row, d)), k);
+        uint32_t w = 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w |= static_cast<uint32_t>(vc[f8_value_at<D>(row, d + c)]) << (8 * c);
+        e4m3x4_to_f32(w, v);
+        const float ks = f8_pow2(f8_scale(kc[f8_code_bytes(D)]) - 127);
+        const float vs = f8_pow2(f8_scale(vc[f8_code_bytes(D)]) - 127);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          k[c] *= ks;
+          v[c] *= vs;
+        }
+      }
+      T* ko = key_out + t * key_stride + 4 * i;
+      T* vo = value_out + t * value_stride + 4 * i;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(ko) = make_float4(k[0], k[1], k[2], k[3]);
+        *reinterpret_cast<float4*>(vo) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        *reinterpret_cast<uint2*>(ko) = make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
+        *reinterpret_cast<uint2*>(vo) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      }
+    }
+  }
+}
+
+template <typename T, int D, Rope kRope>
+cudaError_t write_t(const F8WriteArgs& a, cudaStream_t stream) {
+  WriteParams p;
+  p.key = a.cache.key;
+  p.value = a.cache.value;
+  p.key_stride = a.cache.key_stride;
+  p.value_stride = a.cache.value_stride;
+  p.key_cache = a.cache.key_cache;
+  p.value_cache = a.cache.value_cache;
+  p.slot_mapping = a.cache.slot_mapping;
+  p.num_slots = a.cache.num_slots;
+  p.num_tokens = static_cast<int32_t>(a.cache.num_tokens);
+  p.hkv = a.cache.num_kv_heads;
+  p.err = a.cache.err;
+  p.positions = a.positions;
+  p.table = a.cos_sin_cache;
+  p.max_position = a.max_position;
+  p.rotary_dim = a.rotary_dim;
+  p.heads = a.num_heads;
+  p.query = a.query;
+  p.query_out = a.query_out;
+  p.query_stride = a.query_stride;
+  p.query_out_stride = a.query_out_stride;
+  const int sms = current_sm_count();
+  // a token a window while there are SMs for them; 16 where a batch is long
+  const int64_t want = (a.cache.num_tokens + 2 * sms - 1) / (2 * sms);
+  p.window = static_cast<int32_t>(want < kWindow ? want : kWindow);
+  const int windows = (p.num_tokens + p.window - 1) / p.window;
+  p.splits = (2 * p.hkv + kThreads / 32 - 1) / (kThreads / 32);
+  const int most = (8 * sms + windows - 1) / windows;
+  if (p.splits > most) p.splits = most;
+  p.cache_ctas = windows * p.splits;
+  int64_t grid = p.cache_ctas;
+  if (kRope != kNone) {
+    const int64_t items = a.cache.num_tokens * a.num_heads * (D / 16);
+    const int64_t ctas = (items + kThreads - 1) / kThreads, cap = 16 * static_cast<int64_t>(sms);
+    grid += ctas < cap ? ctas : cap;
+  }
+  return launch_programmatic(reshape_and_cache_fp8_kernel<T, D, kRope>, dim3(static_cast<unsigned>(grid)),
+                             dim3(kThreads), 0, stream, p);
+}
+
+template <typename T, int D>
+cudaError_t write_d(const F8WriteArgs& a, cudaStream_t stream) {
+  if (a.positions == nullptr) return write_t<T, D, kNone>(a, stream);
+  return a.is_neox ? write_t<T, D, kHalf>(a, stream) : write_t<T, D, kInterleaved>(a, stream);
+}
+
+template <typename T, int D>
+cudaError_t gather_t(const MxCacheArgs& a, cudaStream_t stream) {
+  const int64_t blocks = (a.num_tokens + 7) / 8, cap = static_cast<int64_t>(current_sm_count()) * 64;
+  return launch_programmatic(
+      gather_cache_fp8_kernel<T, D>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kThreads), 0,
+      stream, static_cast<const uint8_t*>(a.key_cache), static_cast<const uint8_t*>(a.value_cache),
+      a.slot_mapping, static_cast<T*>(const_cast<void*>(a.key)),
+      static_cast<T*>(const_cast<void*>(a.value)), a.key_stride, a.value_stride, a.num_tokens,
+      a.num_slots, a.num_kv_heads, a.err);
+}
+
+}  // namespace
+
+cudaError_t launch_write_fp8(const F8WriteArgs& a, cudaStream_t stream) {
+  if (a.cache.num_tokens == 0) return cudaSuccess;
+  if (a.cache.head_dim == 128)
+    return a.cache.bf16 ? write_d<__nv_bfloat16, 128>(a, stream) : write_d<float, 128>(a, stream);
+  if (a.cache.head_dim == 64)
+    return a.cache.bf16 ? write_d<__nv_bfloat16, 64>(a, stream) : write_d<float, 64>(a, stream);
+  return cudaErrorNotSupported;
+}
+
+cudaError_t launch_gather_cache_fp8(const MxCacheArgs& a, cudaStream_t stream) {
+  if (a.num_tokens == 0) return cudaSuccess;
+  if (a.head_dim == 128)
+    return a.bf16 ? gather_t<__nv_bfloat16, 128>(a, stream) : gather_t<float, 128>(a, stream);
+  if (a.head_dim == 64)
+    return a.bf16 ? gather_t<__nv_bfloat16, 64>(a, stream) : gather_t<float, 64>(a, stream);
+  return cudaErrorNotSupported;
+}
+
+}  // namespace pkv

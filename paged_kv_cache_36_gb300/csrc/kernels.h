@@ -87,7 +87,7 @@ struct AttnArgs {
   int32_t head_dim;
   float scale;
   uint32_t* err;              // device error word
-  int32_t bt_width;           // entries of a block-table row (4-bit caches only)
+  int32_t bt_width;           // entries of a block-table row (4- and 8-bit caches only)
 };
 
 // Scratch carved out of the caller's workspace for the split-KV decode.
@@ -179,7 +179,7 @@ cudaError_t launch_varlen_bf16(const AttnArgs& a, const CUtensorMap& qmap, const
 // or only rows of requests with query length > 1 when skip_decode is set.
 cudaError_t launch_attn_rows(const AttnArgs& a, bool bf16, bool skip_decode, cudaStream_t stream);
 
-// Rows of K and V into (or out of) the 4-bit paged cache; strides in elements.
+// Rows of K and V into (or out of) the 4-bit and 8-bit paged caches; strides in elements.
 // The gather writes through key / value.
 struct MxCacheArgs {
   const void* key;
@@ -234,6 +234,35 @@ int64_t decode_mxfp4_slots(int sms, int num_kv_heads);
 // Split-KV decode over the 4-bit cache of the rows of requests with query length 1.
 cudaError_t launch_decode_mxfp4(const AttnArgs& a, const MxDecodeScratch& ws, int sms,
                                 cudaStream_t stream);
+
+// The write into the 8-bit cache: with positions not null, RoPE of query and key first.
+struct F8WriteArgs {
+  MxCacheArgs cache;
+  const int64_t* positions;
+  const float* cos_sin_cache;
+  int64_t max_position;
+  int32_t rotary_dim;
+  bool is_neox;
+  int32_t num_heads;
+  const void* query;
+  void* query_out;            // may be query
+  int64_t query_stride;       // elements
+  int64_t query_out_stride;
+};
+
+cudaError_t launch_write_fp8(const F8WriteArgs& a, cudaStream_t stream);
+cudaError_t launch_gather_cache_fp8(const MxCacheArgs& a, cudaStream_t stream);
+
+// Attention over the 8-bit cache.
+cudaError_t launch_attention_fp8(const AttnArgs& a, bool decode_only, int sms, cudaStream_t stream);
+
+// A rotary table's frequencies, in turns per position.
+constexpr int kMaxRotaryPairs = 256;
+struct RotaryFrequencies {
+  double turns[kMaxRotaryPairs];
+};
+cudaError_t launch_rotary_table(const RotaryFrequencies& f, float* out, int64_t rows, int64_t start,
+                                int32_t rotary_dim, float factor, cudaStream_t stream);
 
 // A step's metadata built on the device.
 struct StepMetadataArgs {
