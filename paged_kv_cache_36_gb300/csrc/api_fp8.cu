@@ -27,7 +27,22 @@ bool rows_overlap(const void* a, int64_t sa, int64_t na, const void* b, int64_t 
   return m < na || m + nb > sa;
 }
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+struct F8Workspace {
+  size_t plan, ml, o, total;
+};
+
+// The error word's 256 bytes, then the decode's plan (for the largest batch) and partials.
+F8Workspace f8_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
+  const size_t slots = static_cast<size_t>(decode_fp8_slots(sms, num_kv_heads));
+  const size_t group = static_cast<size_t>(num_heads / num_kv_heads);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  F8Workspace w;
+  w.plan = 256;
+  w.ml = w.plan + up(static_cast<size_t>(step_metadata_max_reqs()) * 8);
+  w.o = w.ml + up(slots * group * 8);
+  w.total = w.o + up(slots * group * head_dim * 4);
+  return w;
+}
 
 }  // namespace
 }  // namespace pkv
@@ -133,7 +148,7 @@ size_t pkv_fp8_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads
   if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       num_heads / num_kv_heads > kMaxGroup || (head_dim != 64 && head_dim != 128))
     return 0;
-  return up256(4);
+  return f8_workspace(current_sm_count(), num_heads, num_kv_heads, head_dim).total;
 }
 
 int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* key_cache,
@@ -157,10 +172,11 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
     return fail(PKV_E_UNSUPPORTED, "%s: at most %d requests and 2^31 - 1 tokens", where,
                 step_metadata_max_reqs());
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
-  const size_t need = pkv_fp8_attention_workspace_bytes(num_heads, num_kv_heads, head_dim);
-  if (workspace_bytes < need || !aligned16(workspace))
+  const int sms = current_sm_count();
+  const F8Workspace w = f8_workspace(sms, num_heads, num_kv_heads, head_dim);
+  if (workspace_bytes < w.total || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,
-                workspace_bytes, need);
+                workspace_bytes, w.total);
   if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
   if (!q || !key_cache || !value_cache || !block_table || !query_start_loc || !seq_lens ||
       !num_computed_tokens || !out)
@@ -174,7 +190,7 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   if (max_blocks_per_req <= 0 || (num_reqs > 1 && block_table_stride < max_blocks_per_req))
     return fail(PKV_E_INVALID, "%s: block_table rows of %d entries, %d apart", where,
                 max_blocks_per_req, block_table_stride);
-  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kMxRequestCost) > 0x7fffffffLL)
+  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kF8RequestCost) > 0x7fffffffLL)
     return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
   AttnArgs a;
   a.q = q;
@@ -199,7 +215,14 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   a.scale = scale;
   a.err = static_cast<uint32_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_attention_fp8(a, max_query_len == 1, current_sm_count(), st);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxDecodeScratch ds;
+  ds.plan = reinterpret_cast<int32_t*>(ws + w.plan);
+  ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  ds.part_o = reinterpret_cast<float*>(ws + w.o);
+  cudaError_t e = cudaSuccess;
+  if (max_query_len != 1) e = launch_attention_fp8(a, sms, st);
+  if (e == cudaSuccess) e = launch_decode_fp8(a, ds, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_fp8 launch");
   return validate_error_word(a.err, st, "paged_attention_varlen_fp8");
 }

@@ -1,4 +1,5 @@
-// Attention over the 8-bit paged cache, one warp per (token, query head): each lane takes
+// Attention over the 8-bit paged cache of the rows of requests with several query tokens, one
+// warp per (token, query head): each lane takes
 // a key for the scores and D / 32 dimensions of the values, with a running maximum and sum.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,7 +27,6 @@ struct Params {
   int32_t num_reqs, num_blocks, hkv, group;
   float scale_log2;
   uint32_t* err;
-  bool decode_only;
 };
 
 template <int D>
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) attention_fp8_kernel(const Params p) {
     const int q0 = __ldg(p.qsl + r);
     const int qlen = static_cast<int>(static_cast<uint32_t>(__ldg(p.qsl + r + 1)) - static_cast<uint32_t>(q0));
     const int seq = __ldg(p.seq_lens + r), nc = __ldg(p.num_computed + r);
-    if (p.decode_only && qlen != 1) continue;
+    if (qlen == 1) continue;
     if (q0 < 0 || qlen <= 0 || nc < 0 || nc > 0x7fffff00 - qlen || seq != nc + qlen || (seq - 1) / kF8Block >= p.bt_width ||
         q0 + qlen > p.num_tokens) {
       if (lane == 0) atomicOr(p.err, PKV_ERR_METADATA);
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) attention_fp8_kernel(const Params p) {
 
 }  // namespace
 
-cudaError_t launch_attention_fp8(const AttnArgs& a, bool decode_only, int sms, cudaStream_t stream) {
+cudaError_t launch_attention_fp8(const AttnArgs& a, int sms, cudaStream_t stream) {
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.q_stride = a.q_stride;
@@ -128,7 +128,6 @@ cudaError_t launch_attention_fp8(const AttnArgs& a, bool decode_only, int sms, c
   p.group = a.num_heads / a.num_kv_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
-  p.decode_only = decode_only;
   const int64_t want = (a.num_tokens * a.num_heads + 7) / 8, cap = 8 * static_cast<int64_t>(sms);
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
   return a.head_dim == 128 ? launch_programmatic(attention_fp8_kernel<128>, grid, dim3(256), 0, stream, p)

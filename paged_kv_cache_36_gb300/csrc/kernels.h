@@ -216,7 +216,7 @@ int64_t prefill_mxfp4_image_bytes(int num_kv_heads, int head_dim);
 cudaError_t launch_prefill_mxfp4(const AttnArgs& a, const MxPrefillScratch& ws, int max_query_len,
                                  int sms, cudaStream_t stream);
 
-// Scratch of the 4-bit decode: the plan that its join follows, and slots that
+// Scratch of the 4-bit and the 8-bit decode: the plan that its join follows, and slots that
 // hold one range's partial of the query heads of one KV head.
 struct MxDecodeScratch {
   int32_t* plan;              // [num_reqs][2]
@@ -253,8 +253,17 @@ struct F8WriteArgs {
 cudaError_t launch_write_fp8(const F8WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_cache_fp8(const MxCacheArgs& a, cudaStream_t stream);
 
-// Attention over the 8-bit cache.
-cudaError_t launch_attention_fp8(const AttnArgs& a, bool decode_only, int sms, cudaStream_t stream);
+// Attention over the 8-bit cache of the rows of requests with query length > 1.
+cudaError_t launch_attention_fp8(const AttnArgs& a, int sms, cudaStream_t stream);
+
+// What the change to a request costs a warp of the 8-bit decode, in blocks.
+constexpr int kF8RequestCost = 2;
+
+// Slots of the 8-bit decode on a device of `sms` SMs.
+int64_t decode_fp8_slots(int sms, int num_kv_heads);
+
+// Split-KV decode over the 8-bit cache of the rows of requests with query length 1.
+cudaError_t launch_decode_fp8(const AttnArgs& a, const MxDecodeScratch& ws, int sms, cudaStream_t stream);
 
 // A rotary table's frequencies, in turns per position.
 constexpr int kMaxRotaryPairs = 256;
