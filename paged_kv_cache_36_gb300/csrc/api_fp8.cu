@@ -28,10 +28,14 @@ bool rows_overlap(const void* a, int64_t sa, int64_t na, const void* b, int64_t 
 }
 
 struct F8Workspace {
-  size_t plan, ml, o, total;
+  size_t plan, ml, o, image_base, images, tile, total;
 };
 
-// The error word's 256 bytes, then the decode's plan (for the largest batch) and partials.
+// Room for the prefill's converted key tiles: 511 of 8 KV heads of 128, 65408 tokens.
+constexpr size_t kImageRoom = 256u << 20;
+
+// The error word's 256 bytes, then the decode's plan (for the largest batch) and partials,
+// then where each request has the prefill's images, and those.
 F8Workspace f8_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
   const size_t slots = static_cast<size_t>(decode_fp8_slots(sms, num_kv_heads));
   const size_t group = static_cast<size_t>(num_heads / num_kv_heads);
@@ -40,7 +44,10 @@ F8Workspace f8_workspace(int sms, int32_t num_heads, int32_t num_kv_heads, int32
   w.plan = 256;
   w.ml = w.plan + up(static_cast<size_t>(step_metadata_max_reqs()) * 8);
   w.o = w.ml + up(slots * group * 8);
-  w.total = w.o + up(slots * group * head_dim * 4);
+  w.image_base = w.o + up(slots * group * head_dim * 4);
+  w.images = w.image_base + up(static_cast<size_t>(step_metadata_max_reqs() + 2) * 4);
+  w.tile = static_cast<size_t>(prefill_fp8_image_bytes(num_kv_heads, head_dim));
+  w.total = w.images + kImageRoom / w.tile * w.tile;
   return w;
 }
 
@@ -174,9 +181,9 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
   const int sms = current_sm_count();
   const F8Workspace w = f8_workspace(sms, num_heads, num_kv_heads, head_dim);
-  if (workspace_bytes < w.total || !aligned16(workspace))
+  if (workspace_bytes < w.images || !aligned16(workspace))
     return fail(PKV_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", where,
-                workspace_bytes, w.total);
+                workspace_bytes, w.images);
   if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
   if (!q || !key_cache || !value_cache || !block_table || !query_start_loc || !seq_lens ||
       !num_computed_tokens || !out)
@@ -221,7 +228,13 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   ds.part_ml = reinterpret_cast<float*>(ws + w.ml);
   ds.part_o = reinterpret_cast<float*>(ws + w.o);
   cudaError_t e = cudaSuccess;
-  if (max_query_len != 1) e = launch_attention_fp8(a, sms, st);
+  if (max_query_len != 1) {
+    MxPrefillScratch ps;
+    ps.images = ws + w.images;
+    ps.image_base = reinterpret_cast<int32_t*>(ws + w.image_base);
+    ps.image_tiles = static_cast<int32_t>((std::min(workspace_bytes, w.total) - w.images) / w.tile);
+    e = launch_prefill_fp8(a, ps, max_query_len, sms, st);
+  }
   if (e == cudaSuccess) e = launch_decode_fp8(a, ds, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_fp8 launch");
   return validate_error_word(a.err, st, "paged_attention_varlen_fp8");

@@ -200,7 +200,7 @@ struct MxCacheArgs {
 cudaError_t launch_reshape_and_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_cache_mxfp4(const MxCacheArgs& a, cudaStream_t stream);
 
-// Scratch of the 4-bit prefill: key tiles converted ahead of it.
+// Scratch of the 4-bit and the 8-bit prefill: key tiles converted ahead of it.
 struct MxPrefillScratch {
   uint8_t* images;
   int32_t* image_base;        // [2 + 2 num_reqs]
@@ -253,8 +253,10 @@ struct F8WriteArgs {
 cudaError_t launch_write_fp8(const F8WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_cache_fp8(const MxCacheArgs& a, cudaStream_t stream);
 
-// Attention over the 8-bit cache of the rows of requests with query length > 1.
-cudaError_t launch_attention_fp8(const AttnArgs& a, int sms, cudaStream_t stream);
+// The same of the 8-bit prefill (images of bfloat16, see fp8_prefill.cu).
+int64_t prefill_fp8_image_bytes(int num_kv_heads, int head_dim);
+cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, int max_query_len,
+                               int sms, cudaStream_t stream);
 
 // What the change to a request costs a warp of the 8-bit decode, in blocks.
 constexpr int kF8RequestCost = 2;

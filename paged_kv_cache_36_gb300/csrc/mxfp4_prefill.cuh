@@ -184,51 +184,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Like mbar_wait_or_abort, but the hardware may hold the warp for a while before
-// it answers "not yet", so that waiting warps leave the issue slots to the
-// others (they wake when the phase completes).
-__device__ __forceinline__ bool held_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                          volatile int* abort) {
-  const uint32_t addr = smem_u32(bar);
-  auto ready = [&]() {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity), "r"(20000u)  // nanoseconds, at most
-        : "memory");
-    return done != 0;
-  };
-  if (ready()) return true;
-  const long long t0 = clock64();
-  while (!ready()) {
-    if (*abort) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      atomicOr(err, PKV_ERR_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool held_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                               volatile int* abort) {
-  return __all_sync(0xffffffffu, held_wait(bar, parity, err, abort));
-}
-
 // Instruction descriptor of kind::f16 with f16 A and B, float32 D.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int b_mn_major) {
   return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
-}
-
-template <int kRegs, bool kMore>
-__device__ __forceinline__ void set_registers() {
-  if constexpr (kMore)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // Eight codes times their group's scale as bfloat16.
@@ -379,19 +337,6 @@ __device__ __forceinline__ bool nan_scale(uint32_t scales) {
   return ((~scales - 0x01010101u) & scales & 0x80808080u) != 0u;
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // What only some key tiles need is done to the scores in tensor memory, in short loops:
 // unrolled over the registers, code that hardly ever runs took instruction cache from
 // the code that always does (a prompt of 4096 tokens: 177 us, in loops 167).
@@ -493,37 +438,6 @@ __device__ __forceinline__ void split_weights(uint32_t cols, float up) {
 #pragma unroll
   for (int e = 0; e < 32; ++e) w[e] = r[e ^ 16];
   tmem_st32(cols + 16, w);
-}
-
-// -inf into this row's columns from `visible` on, of 64; `first` is the smallest such
-// column of the warp's rows.
-__device__ __forceinline__ void mask_scores(uint32_t cols, int first, int visible) {
-#pragma unroll 1
-  for (int c = max(first, 0) & ~7; c < 64; c += 8) {
-    uint32_t r[8];
-    tmem_ld8(cols + c, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e >= visible) r[e] = 0xff800000u;
-    tmem_st8(cols + c, r);
-  }
-  tmem_wait_st();
-}
-
-// Rescales N columns of O from `cols` on.
-template <int N>
-__device__ __forceinline__ void rescale(uint32_t cols, float alpha) {
-#pragma unroll 1
-  for (int c = 0; c < N; c += 32) {
-    uint32_t r32[32];
-    tmem_ld32(cols + c, r32);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) r32[e] = __float_as_uint(__uint_as_float(r32[e]) * alpha);
-    tmem_st32(cols + c, r32);
-  }
-  tmem_wait_st();
 }
 
 // A row of Q (row `key` of the tile at dst_tile, one region of 128 bytes a row per 64
