@@ -1,0 +1,103 @@
+"""The 8-bit prefill of requests whose keys and values are converted ahead (four query
+tiles and eight key tiles or more), and where the room for that ends."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.fp8_support import Step, check
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(step, workspace=None, **kw):
+    import paged_kv_cache_36_gb300 as pkv
+    step.upload()
+    ws = pkv.new_workspace_fp8(step.H, step.hkv, step.d) if workspace is None else workspace
+    out = pkv.paged_attention_varlen_fp8(*step.args(), workspace=ws, **kw)
+    return out, pkv.read_error_word(ws)
+
+
+@pytest.mark.parametrize("heads, hkv, d", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (16, 1, 64), (10, 2, 64)])
+def test_parity(heads, hkv, d):
+    """Beside rows without images and decode rows; odd lengths, ends inside blocks and tiles."""
+    reqs = [(1, 50), (600, 500), (33, 40), (5, 2000), (700, 403), (0, 900), (130, 1500), (1, 3)]
+    step = Step(heads + d, reqs, heads, hkv, d, table_pad=2, stride_pad=1)
+    out, err = _run(step)
+    assert err == 0
+    check(out, *step.reference())
+
+
+@pytest.mark.parametrize("scale", [-0.2, 5.0])
+def test_scale(scale):
+    step = Step(3, [(520, 700)], 4, 1, 64)
+    step.scale = scale
+    out, err = _run(step)
+    assert err == 0
+    check(out, *step.reference())
+
+
+def test_nan():
+    """In keys and values of a request with images, early, in the middle and in the last
+    tokens, of either KV head and both halves of the dimensions."""
+    step = Step(12, [(530, 600), (520, 600)], 4, 2, 128)
+    for pos, h, dim in ((900, 0, 3), (901, 0, 100), (1129, 0, 64), (1000, 1, 127), (10, 1, 40), (900, 0, 4)):
+        step.set(step.v, False, 0, pos, h, dim, 0xFF)
+    step.set(step.k, True, 0, 1050, 1, 77, 0x7F)
+    ref, tol = step.reference()
+    assert ref[:530].isnan().any() and ref[530:].isfinite().all()
+    out, err = _run(step)
+    assert err == 0
+    check(out, ref, tol)
+
+
+@pytest.mark.parametrize("tiles", [0, 9, 20, 27])
+def test_a_shorter_workspace(tiles):
+    """Room for some of the requests' key tiles (9, 10 and 8 of them): the others are converted
+    as they are needed, the result is the same but for the order of nothing."""
+    import paged_kv_cache_36_gb300 as pkv
+    step = Step(5, [(520, 600), (600, 611), (1, 77), (530, 490)], 8, 2, 64)
+    ws = pkv.new_workspace_fp8(8, 2, 64)
+    whole, err = _run(step, ws)
+    tile = 2 * (2 * 16384 + 64 * 4 + 4)
+    need = ws.numel() - (256 << 20) // tile * tile
+    got, err = _run(step, ws[:need + tiles * tile])
+    assert err == 0 and torch.equal(got, whole)
+    check(got, *step.reference())
+    with pytest.raises(pkv.PkvError, match="PKV_E_WORKSPACE"):
+        pkv.paged_attention_varlen_fp8(*step.args(), workspace=ws[:need - 16])
+
+
+def test_block_ids_outside_the_pool_read_as_zeros():
+    import paged_kv_cache_36_gb300 as pkv
+    step = Step(6, [(520, 600), (1, 5)], 4, 2, 64)
+    blk = step.table[0, 40]
+    step.k[blk] = step.v[blk] = 0
+    ref, tol = step.reference()
+    step.table[0, 40] = len(step.k)
+    out, err = _run(step)
+    assert err == pkv.ERR_BLOCK_ID
+    check(out, ref, tol)
+
+
+def test_a_workspace_used_again():
+    """Other batches between two calls: nothing of the images stays."""
+    import paged_kv_cache_36_gb300 as pkv
+    ws = pkv.new_workspace_fp8(8, 2, 128)
+    a = Step(1, [(520, 600), (40, 3)], 8, 2, 128)
+    b = Step(2, [(300, 0), (1, 900), (800, 400)], 8, 2, 128)
+    b.set(b.v, False, 2, np.arange(500, 700)[:, None], 0, np.arange(128), 0x7F)
+    first, _ = _run(a, ws)
+    second, _ = _run(b, ws)
+    again, err = _run(a, ws)
+    assert err == 0 and torch.equal(first, again) and first.isfinite().all()
+    check(second, *b.reference())
+
+
+def test_many_requests():
+    """More requests than a plan in shared memory has entries, one of them with images."""
+    reqs = [(2, i % 5) for i in range(4500)] + [(520, 600)] + [(1, 9)] * 300
+    step = Step(8, reqs, 2, 1, 64)
+    out, err = _run(step)
+    assert err == 0
+    check(out, *step.reference())
