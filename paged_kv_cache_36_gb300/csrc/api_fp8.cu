@@ -15,7 +15,7 @@ namespace pkv {
 namespace {
 
 constexpr int kMaxGroup = 16;
-constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's angles are good to 2^-26 below it
+constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's angles are good to 2^-25 below it
 
 // Whether some of T rows of na bytes, sa apart, share a byte with rows of nb bytes, sb apart.
 // (Of rows whose strides differ, whether their extents overlap.)
@@ -281,7 +281,7 @@ int pkv_build_cos_sin_cache(float* out, int64_t num_positions, int64_t start, in
     if (scaling == PKV_ROPE_YARN) keep = 1.0 - (i - first) / std::max(last - first, 0.001);
     keep = std::min(std::max(keep, 0.0), 1.0);
     w = keep == 1.0 ? w : keep * w + (1.0 - keep) * w / factor;
-    f.turns[i] = w / tau;
+    f.turns[i] = static_cast<uint64_t>(std::ldexp(w / tau, 64));  // (below a sixth of a turn)
   }
   const cudaError_t e = launch_rotary_table(f, out, num_positions, start, rotary_dim,
                                             static_cast<float>(attention_factor), static_cast<cudaStream_t>(stream));

@@ -33,7 +33,7 @@ constexpr int kWindow = 16;  // tokens of a window, at most
 
 enum Rope { kNone, kHalf, kInterleaved };
 
-// Sixteen (or, D 64 values, eight) consecutive elements of a row.
+// N consecutive elements of a row.
 template <typename T, int N>
 struct Piece {
   static constexpr int kVecs = N * sizeof(T) / 16;
@@ -47,6 +47,16 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) {  // of the words
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      f(v[i].x);
+      f(v[i].y);
+      f(v[i].z);
+      f(v[i].w);
+    }
+  }
   __device__ __forceinline__ float at(int i) const {  // i known when compiled
     const uint4& u = v[i / kPer];
     const int k = i % kPer;
@@ -59,16 +69,47 @@ struct Piece {
   }
 };
 
-// |x| as bits, 0 where x is NaN or infinite.
-__device__ __forceinline__ uint32_t magnitude(float x) {
-  const uint32_t m = __float_as_uint(x) & 0x7fffffffu;
-  return m < 0x7f800000u ? m : 0u;
+constexpr uint32_t kInf = 0x7f800000u;
+
+// |x| as bits: their order is that of the magnitudes, infinity and NaN above everything.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// With NaN for an infinity, its finite magnitude to `most`.
+__device__ __forceinline__ float without_infinity(float x, uint32_t& most) {
+  const uint32_t m = magnitude(x);
+  if (m >= kInf) return __uint_as_float(0x7fffffffu);
+  most = max(most, m);
+  return x;
 }
 
-// x times a power of two, for the codes: infinities become NaN.
-__device__ __forceinline__ float scaled(float x, float inv) {
-  return (__float_as_uint(x) & 0x7fffffffu) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x * inv;
-}
+// What a row's vectors need on their way to codes: elements of T in the words of a vector.
+template <typename T>
+struct Words;
+template <>
+struct Words<float> {
+  __device__ __forceinline__ static void most(uint32_t w, uint32_t& m) { m = max(m, w & 0x7fffffffu); }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }  // of a float32
+  __device__ __forceinline__ static uint32_t finite(uint32_t w, uint32_t& m) {
+    return __float_as_uint(without_infinity(__uint_as_float(w), m));
+  }
+  __device__ __forceinline__ static uint32_t times(uint32_t w, float f) { return __float_as_uint(__uint_as_float(w) * f); }
+};
+template <>
+struct Words<__nv_bfloat16> {  // two elements a word
+  __device__ __forceinline__ static void most(uint32_t w, uint32_t& m) { m = __vmaxu2(m, w & 0x7fff7fffu); }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  __device__ __forceinline__ static uint32_t finite(uint32_t w, uint32_t& m) {
+    uint32_t lo = 0u, hi = 0u;
+    if ((w & 0x7f80u) == 0x7f80u) w |= 0x40u; else lo = w & 0x7fffu;
+    if ((w & 0x7f800000u) == 0x7f800000u) w |= 0x400000u; else hi = w & 0x7fff0000u;
+    m = __vmaxu2(m, lo | hi);
+    return w;
+  }
+  // (by a power of two: exact, but for what is far below any code)
+  __device__ __forceinline__ static uint32_t times(uint32_t w, float f) {
+    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
 
 struct WriteParams {
   const void* key;
@@ -160,47 +201,83 @@ __device__ __forceinline__ int new_scale(const uint8_t* head, bool anew, uint32_
   return max(e_new, e_old);
 }
 
+// The largest finite magnitude of the warp's pieces; where some are not finite, infinities
+// become NaN.
+template <typename T, typename Pc, int n>
+__device__ __forceinline__ uint32_t most_of(Pc (&raw)[n]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < n; ++j) raw[j].each([&](uint32_t& w) { Words<T>::most(w, m); });
+  m = warp_max(Words<T>::bits(m));
+  if (m >= kInf) {
+    m = 0u;
+#pragma unroll
+    for (int j = 0; j < n; ++j) raw[j].each([&](uint32_t& w) { w = Words<T>::finite(w, m); });
+    m = warp_max(Words<T>::bits(m));
+  }
+  return m;
+}
+
 // One block's keys of KV head h: rows[t] is the token whose key row t becomes, or -1.
 template <typename T, int D, Rope kRope>
 __device__ __forceinline__ void write_keys(const WriteParams& p, int64_t blk, int h, const int* rows, int lane) {
   constexpr int NV = D / 32;  // pieces of 16 codes a lane
+  constexpr int N = 16 / sizeof(T);
   uint8_t* chunk = p.key_cache + (blk * p.hkv + h) * f8_chunk_bytes(D);
-  const T* key = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D + (lane & 3) * 16;
-  int tok[2] = {rows[lane >> 2], rows[(lane >> 2) + 8]};
+  const T* key = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D;
+  const int tok[2] = {rows[lane >> 2], rows[(lane >> 2) + 8]};
   const bool anew = rows[0] >= 0;
-  Piece<T, 16> raw[kRope == kNone ? NV : 1];
-  float rot[kRope == kNone ? 1 : NV][16];
   uint32_t amax = 0u;
+  // without RoPE the rows stay in registers; with it they are rotated twice, for the scale
+  // and for the codes (64 more registers would halve the warps of an SM)
+  Piece<T, 16> raw[kRope == kNone ? NV : 1];
+  bool odd = false;  // infinities among the rotated ones
+  const float* cs[2] = {nullptr, nullptr};
+  auto rotate = [&](int j, int i, float (&y)[N]) {
+    const int t = tok[j / (D / 64)], d = 64 * (j % (D / 64)) + (lane & 3) * 16 + i;
+    rotated<T, kRope>(key + t * p.key_stride, d, cs[j / (D / 64)], p.rotary_dim, y);
+  };
+  if constexpr (kRope == kNone) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int t = tok[j / (D / 64)], d = 64 * (j % (D / 64));
-    if constexpr (kRope == kNone) {
-      if (t >= 0) raw[j].load(key + t * p.key_stride + d);
+    for (int j = 0; j < NV; ++j) {
+      const int t = tok[j / (D / 64)];
+      if (t >= 0) raw[j].load(key + t * p.key_stride + 64 * (j % (D / 64)) + (lane & 3) * 16);
       else raw[j].zero();
-    } else {
-      constexpr int N = 16 / sizeof(T);
-      if (t >= 0) {
-        const float* cs = p.table + __ldg(p.positions + t) * p.rotary_dim;
-        const T* row = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D + t * p.key_stride;
+    }
+    amax = most_of<T>(raw);
+  } else {
 #pragma unroll
-        for (int i = 0; i < 16; i += N)
-          rotated<T, kRope>(row, d + (lane & 3) * 16 + i, cs, p.rotary_dim,
-                            *reinterpret_cast<float(*)[N]>(&rot[j][i]));
-      } else {
+    for (int u = 0; u < 2; ++u)
+      if (tok[u] >= 0) cs[u] = p.table + __ldg(p.positions + tok[u]) * p.rotary_dim;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) rot[j][i] = 0.f;
+    for (int j = 0; j < NV; ++j) {
+      if (tok[j / (D / 64)] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < 16; i += N) {
+        float y[N];
+        rotate(j, i, y);
+#pragma unroll
+        for (int k = 0; k < N; ++k) amax = max(amax, magnitude(y[k]));
       }
     }
+    amax = warp_max(amax);
+    if (amax >= kInf) {  // once more, for the finite ones
+      odd = true;
+      amax = 0u;
+#pragma unroll 1
+      for (int j = 0; j < NV; ++j)
+#pragma unroll 1
+        for (int i = 0; i < 16 && tok[j / (D / 64)] >= 0; i += N) {
+          float y[N];
+          rotate(j, i, y);
+#pragma unroll
+          for (int k = 0; k < N; ++k) without_infinity(y[k], amax);
+        }
+      amax = warp_max(amax);
+    }
   }
-  auto x = [&](int j, int i) -> float {
-    if constexpr (kRope == kNone) return raw[j].at(i); else return rot[j][i];
-  };
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, magnitude(x(j, i)));
   int grown;
-  const int e = new_scale(chunk + f8_code_bytes(D), anew, warp_max(amax), &grown);
+  const int e = new_scale(chunk + f8_code_bytes(D), anew, amax, &grown);
   const float inv = f8_pow2(127 - e);
   const float down = f8_pow2(max(-grown, -126));
 #pragma unroll
@@ -209,9 +286,24 @@ __device__ __forceinline__ void write_keys(const WriteParams& p, int64_t blk, in
     if (tok[j / (D / 64)] >= 0) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = f32x4_to_e4m3(scaled(x(j, 4 * i), inv), scaled(x(j, 4 * i + 1), inv),
-                             scaled(x(j, 4 * i + 2), inv), scaled(x(j, 4 * i + 3), inv));
+      for (int i = 0; i < 16; i += N) {
+        float y[N];
+        if constexpr (kRope == kNone) {
+          if (i == 0) raw[j].each([&](uint32_t& word) { word = Words<T>::times(word, inv); });
+#pragma unroll
+          for (int k = 0; k < N; ++k) y[k] = raw[j].at(i + k);
+        } else {
+          rotate(j, i, y);
+          if (odd) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) y[k] = without_infinity(y[k], amax);
+          }
+#pragma unroll
+          for (int k = 0; k < N; ++k) y[k] *= inv;
+        }
+#pragma unroll
+        for (int k = 0; k < N; k += 4) w[(i + k) / 4] = f32x4_to_e4m3(y[k], y[k + 1], y[k + 2], y[k + 3]);
+      }
       *at = make_uint4(w[0], w[1], w[2], w[3]);
     } else if (anew) {
       *at = make_uint4(0u, 0u, 0u, 0u);
@@ -245,16 +337,14 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
       keep |= 0xffu << (8 * i);
     }
   }
-  uint32_t amax = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int d = 0; d < P; ++d) amax = max(amax, magnitude(raw[i].at(d)));
+  const uint32_t amax = most_of<T>(raw);
   int grown;
-  const int e = new_scale(chunk + f8_code_bytes(D), anew, warp_max(amax), &grown);
+  const int e = new_scale(chunk + f8_code_bytes(D), anew, amax, &grown);
   const float inv = f8_pow2(127 - e);
   const float down = f8_pow2(max(-grown, -126));
   if (anew || grown || keep != 0xffffffffu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i].each([&](uint32_t& w) { w = Words<T>::times(w, inv); });
 #pragma unroll
     for (int j = 0; j < P / 4; ++j) {
       uint4* at = reinterpret_cast<uint4*>(chunk + j * 512 + lane * 16);
@@ -264,8 +354,8 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (grown) w[i] = e4m3x4_rescale(w[i], down);
-        const uint32_t n = f32x4_to_e4m3(scaled(raw[0].at(4 * j + i), inv), scaled(raw[1].at(4 * j + i), inv),
-                                         scaled(raw[2].at(4 * j + i), inv), scaled(raw[3].at(4 * j + i), inv));
+        const uint32_t n = f32x4_to_e4m3(raw[0].at(4 * j + i), raw[1].at(4 * j + i), raw[2].at(4 * j + i),
+                                         raw[3].at(4 * j + i));
         w[i] = (w[i] & keep) | (n & ~keep);
       }
       *at = make_uint4(w[0], w[1], w[2], w[3]);
@@ -276,72 +366,79 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
     *reinterpret_cast<uint4*>(chunk + f8_code_bytes(D)) = make_uint4(static_cast<uint32_t>(e), 0u, 0u, 0u);
 }
 
-// Rotates the query heads of every token whose position is in the table: a thread takes a
-// vector of them, or two that hold the pairs.
+// Rotates the query heads of every token whose position is in the table, a warp a token: a
+// lane takes the same vector (or two that hold the pairs) of every head, so it reads its
+// cosines and sines once.  Behind the vectors that rotate come those that are copied.
 template <typename T, int D, Rope kRope>
-__device__ __forceinline__ void rotate_queries(const WriteParams& p, int64_t first, int64_t step) {
+__device__ __forceinline__ void rotate_queries(const WriteParams& p, int64_t first, int64_t step, int lane) {
   constexpr int N = 16 / sizeof(T);
-  const int rot = p.rotary_dim / N / (kRope == kHalf ? 2 : 1);  // items of a head that rotate
-  const bool in_place = p.query == p.query_out;
-  const int items = rot + (in_place ? 0 : (D - p.rotary_dim) / N);
-  const int64_t per_token = static_cast<int64_t>(p.heads) * items;
-  const int64_t total = p.num_tokens * per_token;
-  for (int64_t i = first; i < total; i += step) {
-    const int64_t t = i / per_token;
-    const int rem = static_cast<int>(i - t * per_token);
-    const int h = rem / items, j = rem - h * items;
+  constexpr int M = kRope == kHalf ? N : N / 2;  // table entries of a vector, each of cosines and sines
+  constexpr int kAhead = 4;
+  const int rot = p.rotary_dim / N / (kRope == kHalf ? 2 : 1);
+  const int items = rot + (p.query == p.query_out ? 0 : (D - p.rotary_dim) / N);  // 32 at most
+  const int per = 32 / items;  // heads at once
+  const int j = lane % items, h0 = lane / items;
+  if (h0 >= per) return;
+  const int at = j < rot ? j : p.rotary_dim / N + j - rot;
+  for (int64_t t = first; t < p.num_tokens; t += step) {
     const int64_t pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.max_position) continue;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + t * p.query_stride +
-                                                      static_cast<int64_t>(h) * D);
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.query_out) + t * p.query_out_stride +
-                                          static_cast<int64_t>(h) * D);
-    // (plain loads: the rows may be rewritten in place)
-    if (j >= rot) {
-      const int at = p.rotary_dim / N + j - rot;
-      dst[at] = src[at];
-      continue;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.query) + t * p.query_stride) + at;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.query_out) + t * p.query_out_stride) + at;
+    float c[M], s[M];
+    if (j < rot) {
+      const float* cs = p.table + pos * p.rotary_dim + j * M;
+      load_table<M>(cs, c);
+      load_table<M>(cs + (p.rotary_dim >> 1), s);
     }
-    auto store = [&](int at, const float (&y)[N]) {
-      if constexpr (sizeof(T) == 4)
-        dst[at] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-      else
-        dst[at] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-    };
-    const float* cs = p.table + pos * p.rotary_dim;
-    const int half = p.rotary_dim >> 1;
-    Piece<T, N> a;
-    a.v[0] = src[j];
-    float y[N];
-    if constexpr (kRope == kHalf) {
-      Piece<T, N> b;
-      b.v[0] = src[j + rot];
-      float c[N], s[N], z[N];
-      load_table<N>(cs + j * N, c);
-      load_table<N>(cs + half + j * N, s);
+    for (int h = h0; h < p.heads; h += kAhead * per) {
+      // (plain loads: the rows may be rewritten in place)
+      Piece<T, N> a[kAhead], b[kRope == kHalf ? kAhead : 1];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        y[k] = a.at(k) * c[k] - b.at(k) * s[k];
-        z[k] = b.at(k) * c[k] + a.at(k) * s[k];
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t off = static_cast<int64_t>(h + u * per) * (D / N);
+        if (h + u * per < p.heads) {
+          a[u].v[0] = src[off];
+          if (kRope == kHalf && j < rot) b[u].v[0] = src[off + rot];
+        }
       }
-      store(j, y);
-      store(j + rot, z);
-    } else {
-      float c[N / 2], s[N / 2];
-      load_table<N / 2>(cs + j * (N / 2), c);
-      load_table<N / 2>(cs + half + j * (N / 2), s);
 #pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        y[k] = a.at(k) * c[k / 2] - a.at(k + 1) * s[k / 2];
-        y[k + 1] = a.at(k + 1) * c[k / 2] + a.at(k) * s[k / 2];
+      for (int u = 0; u < kAhead; ++u) {
+        if (h + u * per >= p.heads) break;
+        uint4* out = dst + static_cast<int64_t>(h + u * per) * (D / N);
+        auto store = [&](uint4* to, const float (&y)[N]) {
+          if constexpr (sizeof(T) == 4)
+            *to = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+          else
+            *to = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        };
+        if (j >= rot) {
+          *out = a[u].v[0];
+          continue;
+        }
+        float y[N];
+        if constexpr (kRope == kHalf) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) y[k] = a[u].at(k) * c[k] - b[u].at(k) * s[k];
+          store(out, y);
+#pragma unroll
+          for (int k = 0; k < N; ++k) y[k] = b[u].at(k) * c[k] + a[u].at(k) * s[k];
+          store(out + rot, y);
+        } else {
+#pragma unroll
+          for (int k = 0; k < N; k += 2) {
+            y[k] = a[u].at(k) * c[k / 2] - a[u].at(k + 1) * s[k / 2];
+            y[k + 1] = a[u].at(k + 1) * c[k / 2] + a[u].at(k) * s[k / 2];
+          }
+          store(out, y);
+        }
       }
-      store(j, y);
     }
   }
 }
 
 template <typename T, int D, Rope kRope>
-__global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) reshape_and_cache_fp8_kernel(const WriteParams p) {
   // a programmatic dependent of the kernel before it, which may still read the cache or
   // write the new rows
   grid_dependency_wait();
@@ -349,8 +446,8 @@ __global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const W
   if constexpr (kRope != kNone) {
     if (static_cast<int>(blockIdx.x) >= p.cache_ctas) {
       rotate_queries<T, D, kRope>(
-          p, static_cast<int64_t>(blockIdx.x - p.cache_ctas) * kThreads + threadIdx.x,
-          static_cast<int64_t>(gridDim.x - p.cache_ctas) * kThreads);
+          p, static_cast<int64_t>(blockIdx.x - p.cache_ctas) * (kThreads / 32) + (threadIdx.x >> 5),
+          static_cast<int64_t>(gridDim.x - p.cache_ctas) * (kThreads / 32), threadIdx.x & 31);
       return;
     }
   }
@@ -360,6 +457,16 @@ __global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const W
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int win = blockIdx.x / p.splits, split = blockIdx.x - win * p.splits;
   const int T0 = win * p.window, n = min(p.window, p.num_tokens - T0);
+  // the rows are wanted once the search below is through
+  {
+    const int lines = p.hkv * D * static_cast<int>(sizeof(T)) / 128;  // of a row
+    for (int i = threadIdx.x; i < 2 * n * lines; i += kThreads) {
+      const int k = i / lines, t = T0 + (k >> 1);
+      const char* row = (k & 1) ? static_cast<const char*>(p.value) + t * p.value_stride * static_cast<int64_t>(sizeof(T))
+                                : static_cast<const char*>(p.key) + t * p.key_stride * static_cast<int64_t>(sizeof(T));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (i - k * lines) * 128));
+    }
+  }
   // the block of token t, or -1 where it is not written
   auto block_at = [&](int t, bool report) -> int {
     const int64_t slot = __ldg(p.slot_mapping + t);
@@ -382,11 +489,12 @@ __global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const W
       first = b >= 0 && (T0 + lane == 0 || block_at(T0 + lane - 1, false) != b);
     }
     const unsigned leads = __ballot_sync(0xffffffffu, first);
+    const unsigned before = __match_any_sync(0xffffffffu, b) & leads & ((1u << lane) - 1u);
     if (first) {
       const int k = __popc(leads & ((1u << lane) - 1u));
       block_of[k] = b;
       first_of[k] = T0 + lane;
-      taken[k] = 0;
+      taken[k] = before != 0u ? 1 : 0;
     }
     if (lane == 0) found = __popc(leads);
   }
@@ -394,26 +502,26 @@ __global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const W
   __syncthreads();
   const int leads = found;
   if (leads == 0) return;
-  // ---- the other tokens of those blocks ----
-  constexpr int kAhead = 4;
-  for (int base = threadIdx.x; base < p.num_tokens; base += kThreads * kAhead) {
-    int64_t slot[kAhead];
+  // ---- the other tokens of those blocks, two blocks at a time (in the order of the requests
+  // a window has hardly more) ----
+  constexpr int kAhead = 8;
+  for (int k = 0; k < leads; k += 2) {
+    const uint32_t b0 = block_of[k], b1 = block_of[min(k + 1, leads - 1)];
+    for (int base = threadIdx.x; base < p.num_tokens; base += kThreads * kAhead) {
+      int64_t slot[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int t = base + u * kThreads;
-      slot[u] = t < p.num_tokens ? __ldg(p.slot_mapping + t) : -1;
-    }
+      for (int u = 0; u < kAhead; ++u) {
+        const int t = base + u * kThreads;
+        slot[u] = t < p.num_tokens ? __ldg(p.slot_mapping + t) : -1;
+      }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (slot[u] < 0 || slot[u] >= p.num_slots) continue;
-      const int b = static_cast<int>(slot[u] / kF8Block), t = base + u * kThreads;
-      for (int k = 0; k < leads; ++k) {
-        if (b != block_of[k]) continue;
-        if constexpr (kRope != kNone) {
-          if (block_at(t, false) < 0) continue;  // its position
-        }
-        if (t < first_of[k]) taken[k] = 1;
-        atomicMax(&rows[k][slot[u] % kF8Block], t);
+      for (int u = 0; u < kAhead; ++u) {
+        const uint32_t b = static_cast<uint32_t>(slot[u] >> 4);
+        if (b != b0 && b != b1) continue;
+        const int t = base + u * kThreads, i = b == b0 ? k : k + 1;
+        if (block_at(t, false) < 0) continue;  // (a slot past 2^36 may look like another)
+        if (t < first_of[i]) taken[i] = 1;
+        atomicMax(&rows[i][slot[u] % kF8Block], t);
       }
     }
   }
@@ -427,7 +535,25 @@ __global__ void __launch_bounds__(kThreads) reshape_and_cache_fp8_kernel(const W
   }
 }
 
-// One warp per token; every value is exact in either output type.
+// Stores eight (four) values of an output row.
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// One warp per token; every value is exact in either output type.  A lane takes 16 dimensions
+// of a key at a time (a vector of codes), and 4 of a value: the vector that holds them has
+// three other tokens' too, which the warps beside this one find in L1 if their tokens follow
+// one another.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(
     const uint8_t* __restrict__ key_cache, const uint8_t* __restrict__ value_cache,
@@ -436,44 +562,68 @@ __global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(
     uint32_t* __restrict__ err) {
   grid_dependency_wait();  // the kernel before it may write the cache
   if (threadIdx.x == 0) grid_launch_dependents();
+  constexpr int P = D / 8, kAhead = 4;
   const int lane = threadIdx.x & 31;
   const int64_t wpb = kThreads / 32;
-  const int n = hkv * D / 4;  // fours of dimensions in a row
+  const int nk = hkv * D / 16, nv = hkv * D / 4;
   for (int64_t t = blockIdx.x * wpb + (threadIdx.x >> 5); t < num_tokens; t += gridDim.x * wpb) {
     const int64_t slot = __ldg(slot_mapping + t);
     if (slot < 0) continue;
     const bool in = slot < num_slots;
     if (!in && lane == 0 && err) atomicOr(err, PKV_ERR_SLOT);
     const int row = static_cast<int>(slot & (kF8Block - 1));
-    const int64_t blk = in ? slot / kF8Block : 0;
-    for (int i = lane; i < n; i += 32) {
-      const int h = i / (D / 4), d = i % (D / 4) * 4;
-      float k[4] = {}, v[4] = {};
+    const int64_t blk = (in ? slot / kF8Block : 0) * hkv * f8_chunk_bytes(D);
+    const uint8_t* kblk = key_cache + blk + (row >> 3) * (D / 64) * 512 + (row & 7) * 64;
+    const uint8_t* vblk = value_cache + blk + ((row & 7) >> 1) * 16;
+    const int byte = (row >> 3) * 2 + (row & 1);  // of a V word
+    T* ko = key_out + t * key_stride;
+    T* vo = value_out + t * value_stride;
+    for (int i = lane; i < nk; i += 32) {
+      const int h = i / (D / 16), c = i % (D / 16);
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      float scale = 0.f;
       if (in) {
-        const int64_t at = (blk * hkv + h) * f8_chunk_bytes(D);
-        const uint8_t* kc = key_cache + at;
-        const uint8_t* vc = value_cache + at;
-        e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(kc + f8_key_at<D>(row, d)), k);
-        uint32_t w = 0u;
+        const uint8_t* chunk = kblk + h * f8_chunk_bytes(D);
+        w = __ldg(reinterpret_cast<const uint4*>(chunk + (c >> 2) * 512 + (c & 3) * 16));
+        scale = f8_pow2(f8_scale(__ldg(key_cache + blk + h * f8_chunk_bytes(D) + f8_code_bytes(D))) - 127);
+      }
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w |= static_cast<uint32_t>(vc[f8_value_at<D>(row, d + c)]) << (8 * c);
-        e4m3x4_to_f32(w, v);
-        const float ks = f8_pow2(f8_scale(kc[f8_code_bytes(D)]) - 127);
-        const float vs = f8_pow2(f8_scale(vc[f8_code_bytes(D)]) - 127);
+      for (int k = 0; k < 2; ++k) {
+        float a[4], b[4];
+        e4m3x4_to_f32(words[2 * k], a);
+        e4m3x4_to_f32(words[2 * k + 1], b);
+        const float x[8] = {a[0] * scale, a[1] * scale, a[2] * scale, a[3] * scale,
+                            b[0] * scale, b[1] * scale, b[2] * scale, b[3] * scale};
+        store8(ko + 16 * i + 8 * k, x);
+      }
+    }
+    const uint32_t low = 0x0040u + 0x0011u * byte;  // bytes `byte` of two words, side by side
+    for (int base = lane; base < nv; base += 32 * kAhead) {
+      uint4 w[kAhead];
+      uint32_t e[kAhead];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          k[c] *= ks;
-          v[c] *= vs;
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = base + 32 * u;
+        const int h = i / (D / 4), c = i % (D / 4);  // dims 4 c .. + 3: lane group c / (P / 4), vector c % (P / 4)
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        e[u] = 127u;
+        if (in && i < nv) {
+          w[u] = __ldg(reinterpret_cast<const uint4*>(vblk + h * f8_chunk_bytes(D) + c % (P / 4) * 512 + c / (P / 4) * 64));
+          e[u] = __ldg(value_cache + blk + h * f8_chunk_bytes(D) + f8_code_bytes(D));
         }
       }
-      T* ko = key_out + t * key_stride + 4 * i;
-      T* vo = value_out + t * value_stride + 4 * i;
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(ko) = make_float4(k[0], k[1], k[2], k[3]);
-        *reinterpret_cast<float4*>(vo) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-        *reinterpret_cast<uint2*>(ko) = make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
-        *reinterpret_cast<uint2*>(vo) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = base + 32 * u;
+        if (i >= nv) break;
+        const uint32_t four = __byte_perm(__byte_perm(w[u].x, w[u].y, low), __byte_perm(w[u].z, w[u].w, low), 0x5410);
+        const float scale = f8_pow2(f8_scale(e[u]) - 127);
+        float x[4];
+        e4m3x4_to_f32(four, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] *= scale;
+        store4(vo + 4 * i, x);
       }
     }
   }
@@ -504,17 +654,16 @@ cudaError_t write_t(const F8WriteArgs& a, cudaStream_t stream) {
   p.query_out_stride = a.query_out_stride;
   const int sms = current_sm_count();
   // a token a window while there are SMs for them; 16 where a batch is long
-  const int64_t want = (a.cache.num_tokens + 2 * sms - 1) / (2 * sms);
+  const int64_t want = (a.cache.num_tokens + 4 * sms - 1) / (4 * sms);
   p.window = static_cast<int32_t>(want < kWindow ? want : kWindow);
   const int windows = (p.num_tokens + p.window - 1) / p.window;
   p.splits = (2 * p.hkv + kThreads / 32 - 1) / (kThreads / 32);
-  const int most = (8 * sms + windows - 1) / windows;
+  const int most = (4 * sms + windows - 1) / windows;
   if (p.splits > most) p.splits = most;
   p.cache_ctas = windows * p.splits;
   int64_t grid = p.cache_ctas;
   if (kRope != kNone) {
-    const int64_t items = a.cache.num_tokens * a.num_heads * (D / 16);
-    const int64_t ctas = (items + kThreads - 1) / kThreads, cap = 16 * static_cast<int64_t>(sms);
+    const int64_t ctas = (a.cache.num_tokens + kThreads / 32 - 1) / (kThreads / 32), cap = 8 * static_cast<int64_t>(sms);
     grid += ctas < cap ? ctas : cap;
   }
   return launch_programmatic(reshape_and_cache_fp8_kernel<T, D, kRope>, dim3(static_cast<unsigned>(grid)),

@@ -267,10 +267,10 @@ int64_t decode_fp8_slots(int sms, int num_kv_heads);
 // Split-KV decode over the 8-bit cache of the rows of requests with query length 1.
 cudaError_t launch_decode_fp8(const AttnArgs& a, const MxDecodeScratch& ws, int sms, cudaStream_t stream);
 
-// A rotary table's frequencies, in turns per position.
+// A rotary table's frequencies, in 2^-64 turns per position.
 constexpr int kMaxRotaryPairs = 256;
 struct RotaryFrequencies {
-  double turns[kMaxRotaryPairs];
+  uint64_t turns[kMaxRotaryPairs];
 };
 cudaError_t launch_rotary_table(const RotaryFrequencies& f, float* out, int64_t rows, int64_t start,
                                 int32_t rotary_dim, float factor, cudaStream_t stream);

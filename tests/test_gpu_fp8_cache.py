@@ -64,7 +64,7 @@ def _same(cache, pool, hkv, d):
     (7, 2, 128, F32, True, 2, "random"), (33, 3, 64, BF16, True, 3, "random"),
     (16, 5, 128, BF16, False, 0, "blocks"), (50, 1, 128, F32, False, 1, "blocks"),
     (40, 5, 64, F32, False, 0, "reversed"), (300, 1, 64, BF16, False, 5, "blocks"),
-    (700, 1, 64, BF16, True, 0, "random")])
+    (700, 1, 64, BF16, True, 0, "random"), (1300, 1, 64, BF16, False, 3, "woven"), (1900, 1, 64, F32, False, 0, "random")])
 def test_write_is_the_oracle_byte_for_byte(tokens, hkv, d, dtype, fused, pad, order):
     """Two calls into noise, the second behind the rows of the first: restarted blocks,
     blocks whose scale grows, blocks whose scale stays."""
@@ -82,6 +82,8 @@ def test_write_is_the_oracle_byte_for_byte(tokens, hkv, d, dtype, fused, pad, or
         slots = every[start + call * tokens:start + (call + 1) * tokens].astype(np.int64)
         if order == "reversed":
             slots = slots[::-1].copy()
+        if order == "woven":    # neighbours from two blocks in turn
+            slots = slots[np.argsort(np.arange(tokens) % 16 + np.arange(tokens) // 32 * 32, kind="stable")]
         if pad:
             slots[rng.permutation(tokens)[:pad]] = -1
         k, v = _rows(rng, tokens, hkv, d).to(dtype), _rows(rng, tokens, hkv, d).to(dtype)
