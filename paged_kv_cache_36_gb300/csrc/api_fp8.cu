@@ -233,7 +233,7 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
     ps.images = ws + w.images;
     ps.image_base = reinterpret_cast<int32_t*>(ws + w.image_base);
     ps.image_tiles = static_cast<int32_t>((std::min(workspace_bytes, w.total) - w.images) / w.tile);
-    e = launch_prefill_fp8(a, ps, max_query_len, sms, st);
+    e = launch_prefill_fp8(a, ps, sms, st);
   }
   if (e == cudaSuccess) e = launch_decode_fp8(a, ds, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_varlen_fp8 launch");

@@ -25,10 +25,11 @@
 //     [1, 2) by a power of two first, so that sums over codes are below 2^17 whatever q and
 //     the scale are; nothing of an element is lost above 2^-126 of the head's largest.
 //   - V's scale multiplies its codes, exactly, so weights and values go into the product as
-//     they are: weights are bfloat16 (8 bits) down to 2^-126, values have no other limit than
-//     that float32 sums hold: 2^8 sum_j |V_j| below 2^128.
-//   - The reference m of the weights is a score that was the largest and moves when one
-//     exceeds it by 2^8: the common block needs a vote, and no shuffle.
+//     they are: weights are bfloat16 (8 bits) over 102 binades below the largest, values have no
+//     other limit than that float32 sums hold.
+//   - The reference m of the weights lies 2^24 above a score that was the largest and moves when
+//     one exceeds that by 2^32: the common block needs a vote, and no shuffle, and the sums of
+//     flat scores stay finite for any values there are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,7 +44,9 @@ namespace pkv {
 namespace {
 
 constexpr int kMinUnits = 8;     // units in a range, nearly: at least 4
-constexpr float kMaxWeight = 8.f;
+// Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
+// one exceeds 2^kMost.
+constexpr float kLargest = -24.f, kMost = 8.f;
 constexpr int kMaxStages = 6;
 
 template <int NT>
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           mx[nt][cc] = fmaxf(s[nt][cc], s[nt][2 + cc]);
-          grow |= mx[nt][cc] > m[nt][cc] + kMaxWeight;
+          grow |= mx[nt][cc] > m[nt][cc] + kMost;
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[nt][cc], x);
+            const float mn = fmaxf(m[nt][cc], x - kLargest);
             const float alpha = mn == m[nt][cc] ? 1.f : exp2_approx(m[nt][cc] - mn);
             m[nt][cc] = mn;
             l[nt][cc] *= alpha;

@@ -8,8 +8,8 @@
 // P V as tcgen05 products, S and O in tensor memory, P (bfloat16) written over S.
 //
 // Where K and V tiles come from.
-//   - Requests with many query and key tiles have their key tiles converted once, by
-//     expand_fp8_kernel, to images in the workspace: K and V as the 128-byte swizzled rows
+//   - Requests with enough of them have their key tiles converted once, by expand_fp8_kernel,
+//     to images in the workspace: K and V as the 128-byte swizzled rows
 //     that the tensor core reads, so that a tile is one bulk copy of 16 or 32 KB from L2.
 //   - For the others eight warps convert as they go: a warp takes whole blocks, whose codes
 //     it reads as D / 32 coalesced vectors, and writes rows to the stage.
@@ -52,14 +52,31 @@ constexpr int kNanBufs = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = kSBufs * kKeys;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
+// one exceeds 2^kMost.  So O is rescaled once a row's maximum has grown by 2^32 (2^8, as for
+// bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134), sums of flat scores stay
+// finite for any values there are, and weights vanish (at 2^-126) 102 binades below the
+// largest.
+constexpr float kLargest = -24.f, kMost = 8.f;
 constexpr int kPrefixMax = 4096;           // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;       // a whole key tile more is still an int
 constexpr size_t kSmemLimit = 232448;
 constexpr int kNone = 0x7fffffff;          // no NaN
-// Query tiles (of a KV head) and key tiles from which on a request has images.
-constexpr int kImageQueryTiles = 4;
-constexpr int kImageKeyTiles = 8;
+// Which requests have images, by what both ways cost (see expand_fp8_kernel).  In a graph a
+// CTA takes some 2.0 us for a key tile of head_dim 128 that it converts and 1.1 over images, of
+// 64 1.0 and 0.6; images cost two kernels, 6 us, and for each key tile and KV head what they
+// write and read again.  us over images / converted as they go, 32 query and 8 KV heads of 128:
+//   tokens 4096 136 / 239, 2048 58 / 74, 1024 31 / 30, 512 behind 1223 29 / 31, behind 11539 84 /
+//   141, 128 behind 3874 35 / 41, 64 behind 2048 31 / 34, 4 behind 8000 66 / 98, 4 behind 1000 25 /
+//   22; 8 requests of 256 behind 1000 71 / 75; 16 of 4 behind 4000 130 / 82.
+//   16 query and 4 KV heads of 64: tokens 4096 67 / 78, 2048 31 / 28, 512 behind 1069 24 / 20, 64
+//   behind 4096 40 / 43.
+constexpr float kImageFixed = 6.f;
+template <int D>
+constexpr float image_gain() { return D == 128 ? 0.9f : 0.4f; }     // of a key tile, a CTA
+template <int D>
+constexpr float image_cost() { return D == 128 ? 0.024f : 0.012f; }  // of a key tile and KV head
+constexpr int kManyTiles = 4;  // query tiles from which on reading images often pays for writing them
 
 // Threads, and registers a thread by role (setmaxnreg), over images and without.
 template <bool kImages>
@@ -131,6 +148,7 @@ struct Params {
   int32_t* image_nan;
   int32_t* any;
   int32_t image_tiles;  // key tiles (of all KV heads) there is room for
+  int32_t sms;
 };
 
 struct Tile {
@@ -355,8 +373,9 @@ __device__ __forceinline__ void copy_role(const Params& p, uint8_t* smem, const 
     mbar_wait(&bars[kFull0 + (count - back) % kStages], ((count - back) / kStages) & 1, p.err);
 }
 
-// One row of Q, as it is (the scale's sign on it), zeros where there is no row.
-template <int D>
+// One row of Q, as it is (the scale's sign on it), zeros where there is no row.  kHalves of
+// the row are read before the wait for the buffer, the rest after.
+template <int D, int kHalves>
 __device__ __forceinline__ bool copy_q_row(const Params& p, const Tile& t, int row, uint8_t* smem, uint32_t tiles) {
   using L = Layout<D>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -369,15 +388,15 @@ __device__ __forceinline__ bool copy_q_row(const Params& p, const Tile& t, int r
       static_cast<int64_t>(t.h * G + (real ? row % G : 0)) * D);
   uint8_t* dst = smem + L::kQ + row * 128;
 #pragma unroll
-  for (int half = 0; half < L::NDH; ++half) {
-    uint4 x[8];
+  for (int half = 0; half < L::NDH; half += kHalves) {
+    uint4 x[8 * kHalves];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = real ? __ldg(src + 8 * half + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 8 * kHalves; ++i) x[i] = real ? __ldg(src + 8 * half + i) : make_uint4(0u, 0u, 0u, 0u);
     // the tile before is done with the buffer
     if (half == 0 && tiles > 0 && !held_warp_wait(&bars[kQEmpty], (tiles - 1) & 1, p.err, abort_flag)) return false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(dst + half * kRegion + ((i ^ (row & 7)) << 4)) =
+    for (int i = 0; i < 8 * kHalves; ++i)
+      *reinterpret_cast<uint4*>(dst + (half + i / 8) * kRegion + (((i & 7) ^ (row & 7)) << 4)) =
           make_uint4(x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign, x[i].w ^ sign);
   }
   fence_proxy_async_smem();
@@ -425,7 +444,7 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
     load(next, 0, load_id(0));
     int id = load_id(1);
     if constexpr (!kIsV) {
-      ok = copy_q_row<D>(p, t, cw * 32 + lane, smem, tiles);
+      ok = copy_q_row<D, 1>(p, t, cw * 32 + lane, smem, tiles);
       if (!ok) break;
     }
     for (int j = 0; j < t.nkt && ok; ++j, ++count) {
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
            ct = cta_tile(++it, cid, ncta, total), ++tiles) {
         if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
         const Tile t = find_tile<true>(ct, prefix, entries, p, tpt);
-        if (!copy_q_row<D>(p, t, (warp - 12) * 32 + lane, smem, tiles)) break;
+        if (!copy_q_row<D, L::NDH>(p, t, (warp - 12) * 32 + lane, smem, tiles)) break;
       }
     } else {
       if (warp < 16) convert_role<D, false>(p, smem, prefix, entries, total, tpt, warp - 12);
@@ -654,6 +673,12 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
       const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
       const int pos_min = t.nc + t.u0;
       float m_used = -INFINITY, l = 0.f;
+      // whether an image of these keys has a NaN in V (looked at when the tile is through)
+      int nan_images = 0;
+      if constexpr (kImages) {
+        const int32_t* at = p.image_nan + static_cast<int64_t>(__ldcg(p.image_base + t.r)) * p.hkv + t.h;
+        for (int j = lane; j < t.nkt; j += 32) nan_images |= __ldcg(at + static_cast<int64_t>(j) * p.hkv);
+      }
       bool ok = true;
       for (int j = 0; j < t.nkt && ok; ++j, ++count) {
         const int b = count % kSBufs;
@@ -683,9 +708,9 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], sv[60 + k]);
         const float m_mine = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * f;
         const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
-        if (j == 0) m_used = mx;  // key 0 is visible to every row
+        if (j == 0) m_used = mx - kLargest;  // key 0 is visible to every row
         // both warps of the quadrant see the same mx and m_used
-        const bool grow = mx > m_used + kRescaleThreshold;
+        const bool grow = mx > m_used + kMost;
         if (__any_sync(0xffffffffu, grow)) {
           // O must hold PV of the previous key tile before it is rescaled
           const uint32_t prev = count - 1;
@@ -694,8 +719,8 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
             break;
           }
           tc_fence_after();
-          const float alpha = grow ? exp2_approx(m_used - mx) : 1.f;
-          if (grow) m_used = mx;
+          const float alpha = grow ? exp2_approx(m_used - mx + kLargest) : 1.f;
+          if (grow) m_used = mx - kLargest;
           l *= alpha;
           rescale<D / 2>(o_cols, alpha);
         }
@@ -725,13 +750,12 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
       // dimensions of this warp's half in which the row sees a NaN
       uint64_t nan_dims = 0u;
       if constexpr (kImages) {
-        const int64_t first = static_cast<int64_t>(__ldcg(p.image_base + t.r)) * p.hkv + t.h;
-        for (int j0 = 0; j0 < t.nkt; j0 += 32) {
-          const int j = j0 + lane;
-          unsigned with = __ballot_sync(0xffffffffu, j < t.nkt && __ldcg(p.image_nan + first + static_cast<int64_t>(j) * p.hkv) != 0);
-          for (; with != 0u; with &= with - 1u) {
-            const int32_t* at = reinterpret_cast<const int32_t*>(
-                p.images + (first + static_cast<int64_t>(j0 + __ffs(with) - 1) * p.hkv) * image_bytes<D>() + 2 * L::kHalf) + half * (D / 2);
+        if (__any_sync(0xffffffffu, nan_images != 0)) {
+          const int64_t first = static_cast<int64_t>(__ldcg(p.image_base + t.r)) * p.hkv + t.h;
+          for (int j = 0; j < t.nkt; ++j) {
+            const int64_t i = first + static_cast<int64_t>(j) * p.hkv;
+            if (__ldcg(p.image_nan + i) == 0) continue;
+            const int32_t* at = reinterpret_cast<const int32_t*>(p.images + i * image_bytes<D>() + 2 * L::kHalf) + half * (D / 2);
             for (int d = 0; d < D / 2; ++d)
               if (__ldcg(at + d) <= pos) nan_dims |= 1ull << d;
           }
@@ -811,10 +835,50 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.num_reqs, tpt = kRows / p.group;
   bool bad = false;
+  // Requests of many query tiles, and of few: their most key tiles, all key tiles, and visits
+  // of query tiles to key tiles.  Each kind has images if that takes longer without.
+  float longest[2] = {0.f, 0.f}, all[2] = {0.f, 0.f}, visits[2] = {0.f, 0.f};
   for (int r = threadIdx.x; r < R; r += blockDim.x) {
     const int tiles = request_tiles(p, r, tpt, &bad) / p.hkv;
-    const int keys = tiles < kImageQueryTiles ? 0 : (__ldg(p.seq_lens + r) - 1) / kKeys + 1;
-    prefix[r + 1] = keys < kImageKeyTiles ? 0 : keys;
+    const int keys = tiles == 0 ? 0 : (__ldg(p.seq_lens + r) - 1) / kKeys + 1;
+    const int few = tiles < kManyTiles ? 1 : 0;
+    longest[few] = fmaxf(longest[few], static_cast<float>(keys));
+    all[few] += static_cast<float>(keys);
+    visits[few] += tiles * (static_cast<float>(__ldg(p.num_computed + r)) / kKeys + keys) * 0.5f;
+    prefix[r + 1] = few ? -keys : keys;
+  }
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      longest[k] = fmaxf(longest[k], __shfl_xor_sync(0xffffffffu, longest[k], x));
+      all[k] += __shfl_xor_sync(0xffffffffu, all[k], x);
+      visits[k] += __shfl_xor_sync(0xffffffffu, visits[k], x);
+    }
+  __shared__ float sums[8][2][3];
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      sums[warp][k][0] = longest[k];
+      sums[warp][k][1] = all[k];
+      sums[warp][k][2] = visits[k];
+    }
+  __syncthreads();
+  bool ahead[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float most = 0.f, n = 0.f, v = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      most = fmaxf(most, sums[w][k][0]);
+      n += sums[w][k][1];
+      v += sums[w][k][2];
+    }
+    most = fmaxf(most, v * p.hkv / p.sms);  // key tiles of the CTA that has most
+    ahead[k] = image_gain<D>() * most > kImageFixed + image_cost<D>() * n * p.hkv;
+  }
+  for (int r = threadIdx.x; r < R; r += blockDim.x) {
+    const int keys = prefix[r + 1];
+    prefix[r + 1] = keys < 0 ? (ahead[1] ? -keys : 0) : ahead[0] ? keys : 0;
   }
   if (threadIdx.x == 0) prefix[0] = 0;
   if (threadIdx.x < D) nans[threadIdx.x] = kNone;
@@ -917,8 +981,8 @@ int64_t prefill_fp8_image_bytes(int num_kv_heads, int head_dim) {
   return static_cast<int64_t>(num_kv_heads) * ((head_dim == 128 ? image_bytes<128>() : image_bytes<64>()) + 4);
 }
 
-cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, int max_query_len,
-                               int sms, cudaStream_t stream) {
+cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, int sms,
+                               cudaStream_t stream) {
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.q_stride = a.q_stride;
@@ -943,10 +1007,15 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, in
   p.images = nullptr;
   p.image_base = p.image_nan = p.any = nullptr;
   p.image_tiles = ws.image_tiles;
-  // where the longest query, the room or the table's width says that no request can have
+  p.sms = sms;
+  // where the room, the table's width or the number of tokens says that no request can have
   // images, nothing looks for them
-  if (ws.image_tiles >= kImageKeyTiles && p.bt_width > (kImageKeyTiles - 1) * kTileBlocks &&
-      (max_query_len == 0 || max_query_len > (kImageQueryTiles - 1) * (kRows / p.group))) {
+  const int tpt = kRows / p.group;
+  const float keys = static_cast<float>((a.bt_width + kTileBlocks - 1) / kTileBlocks);
+  const float tiles = static_cast<float>((a.num_tokens + tpt - 1) / tpt + a.num_reqs) * p.hkv / sms;
+  const float gain = a.head_dim == 128 ? image_gain<128>() : image_gain<64>();
+  const float cost = a.head_dim == 128 ? image_cost<128>() : image_cost<64>();
+  if (ws.image_tiles > 0 && gain * keys * (tiles > 1.f ? tiles : 1.f) > kImageFixed + cost * keys * p.hkv) {
     p.images = ws.images;
     p.image_nan = reinterpret_cast<int32_t*>(
         ws.images + static_cast<int64_t>(ws.image_tiles) * p.hkv * (a.head_dim == 128 ? image_bytes<128>() : image_bytes<64>()));

@@ -255,8 +255,8 @@ cudaError_t launch_gather_cache_fp8(const MxCacheArgs& a, cudaStream_t stream);
 
 // The same of the 8-bit prefill (images of bfloat16, see fp8_prefill.cu).
 int64_t prefill_fp8_image_bytes(int num_kv_heads, int head_dim);
-cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, int max_query_len,
-                               int sms, cudaStream_t stream);
+cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, int sms,
+                               cudaStream_t stream);
 
 // What the change to a request costs a warp of the 8-bit decode, in blocks.
 constexpr int kF8RequestCost = 2;

@@ -84,8 +84,10 @@ class Step:
         2^-24, S = scale sum |q||k| of a row's worst key and A = sum_j p_j |v_j| / sum_j p_j:
           score: each of D products and a few scalings rounds at u S at most, so a weight is
             off by 2 (D + 32) u S (log2 e folded in), numerator and denominator both;
-          weight: half a bfloat16 step, 2^-8 of A (and an exponential's 2^-21); where p_j is
-            below 2^-126 of the largest nothing is left of it: 2^-126 |v_j|;
+          weight: half a bfloat16 step, 2^-8 of A (and an exponential's 2^-21).  Weights are
+            formed as 2^(s - m) with m at most 24 above the row's largest score, and vanish below
+            2^-126 (the exponential flushes there): where p_j is below 2^-102 of the largest
+            nothing is left of it, 2^-102 |v_j|;
           sums: 2 n u of A for n keys, at worst;
           the result: half a bfloat16 step, 2^-8 |out|; below 2^-126 half of 2^-133.
         """
@@ -112,7 +114,7 @@ class Step:
                 ref[a:b, h] = out.masked_fill(nan, torch.nan)
                 tol[a:b, h] = (2.0 ** -8 * out.abs()
                                + mean * (2.0 ** -8 + 2.0 ** -20 + 4 * (self.d + 32) * u * worst + 2 * n * u)
-                               + 2.0 ** -126 * (seen.double() @ vh.abs()) + 2.0 ** -134)
+                               + 2.0 ** -102 * (seen.double() @ vh.abs()) + 2.0 ** -134)
         return ref, tol
 
 

@@ -91,6 +91,23 @@ def test_unlikely_keys_with_large_values():
     check(_run(step), *step.reference())
 
 
+def test_the_largest_values():
+    """All values 1.75 2^127 or their negative, flat scores: sums stay finite, and so does the result."""
+    step = Step(5, [(1, 3000), (1, 20), (300, 800), (40, 3)], 4, 2, 64)
+    step.q *= 2.0 ** -12
+    for pool, key in ((step.v, False),):
+        for r in range(4):
+            n = step.seq[r]
+            step.set(pool, key, r, np.arange(n)[:, None], 0, np.arange(64), 0x7E)
+            step.set(pool, key, r, np.arange(n)[:, None], 1, np.arange(64), 0xFE)
+            for b in range(-(-n // 16)):
+                for h in range(2):
+                    step.set_scale(pool, r, b, h, 246)
+    ref, tol = step.reference()
+    assert ref.abs().max() < 3e38
+    check(_run(step), ref, tol)
+
+
 def test_nan_counts_for_the_rows_that_see_it():
     """NaN in a key or a value at a position makes what sees it NaN: of a value one dimension
     of the rows behind, of a key all of them."""

@@ -1,5 +1,5 @@
-"""The 8-bit prefill of requests whose keys and values are converted ahead (four query
-tiles and eight key tiles or more), and where the room for that ends."""
+"""The 8-bit prefill of requests whose keys and values are converted ahead, and where the room
+for that ends."""
 
 import numpy as np
 import pytest
