@@ -10,27 +10,49 @@ from tests.fp8_support import Step, check
 pytestmark = pytest.mark.gpu
 
 
-def _run(step, workspace=None, **kw):
+def _tile_bytes(hkv, d):
+    return hkv * (2 * 256 * d + 4 * d + 4)
+
+
+def _run(step, workspace=None, images=True, **kw):
+    """(out, error word); `images`: whether some were made, which the workspace shows."""
     import paged_kv_cache_36_gb300 as pkv
     step.upload()
-    ws = pkv.new_workspace_fp8(step.H, step.hkv, step.d) if workspace is None else workspace
+    ws = workspace
+    if ws is None:
+        ws = torch.zeros_like(pkv.new_workspace_fp8(step.H, step.hkv, step.d))
     out = pkv.paged_attention_varlen_fp8(*step.args(), workspace=ws, **kw)
+    if workspace is None:
+        tile = _tile_bytes(step.hkv, step.d)
+        assert bool(ws[ws.numel() - (256 << 20) // tile * tile:][:1 << 16].any()) == images
     return out, pkv.read_error_word(ws)
 
 
 @pytest.mark.parametrize("heads, hkv, d", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (16, 1, 64), (10, 2, 64)])
 def test_parity(heads, hkv, d):
     """Beside rows without images and decode rows; odd lengths, ends inside blocks and tiles."""
-    reqs = [(1, 50), (600, 500), (33, 40), (5, 2000), (700, 403), (0, 900), (130, 1500), (1, 3)]
+    more = 0 if d == 128 else 2000
+    reqs = [(1, 50), (600, 500 + more), (33, 40), (5, 2000), (700, 403 + more), (0, 900), (130, 1500 + more), (1, 3)]
     step = Step(heads + d, reqs, heads, hkv, d, table_pad=2, stride_pad=1)
     out, err = _run(step)
     assert err == 0
     check(out, *step.reference())
 
 
+@pytest.mark.parametrize("reqs, images", [([(4, 2500)], True), ([(4, 600)], False), ([(4, 1200)] * 20, False),
+                                          ([(4, 600), (500, 700)], True), ([(900, 0)], True), ([(700, 0)], False)])
+def test_which_requests_have_them(reqs, images):
+    """Few query tiles: of long requests, unless there are many.  Many: where a CTA has enough (0.9 of
+    its key tiles, 8 for 900 tokens, above 6 + 0.024 for each there is)."""
+    step = Step(len(reqs), reqs, 8, 2, 128)
+    out, err = _run(step, images=images)
+    assert err == 0
+    check(out, *step.reference())
+
+
 @pytest.mark.parametrize("scale", [-0.2, 5.0])
 def test_scale(scale):
-    step = Step(3, [(520, 700)], 4, 1, 64)
+    step = Step(3, [(520, 700)], 4, 1, 128)
     step.scale = scale
     out, err = _run(step)
     assert err == 0
@@ -54,12 +76,12 @@ def test_nan():
 @pytest.mark.parametrize("tiles", [0, 9, 20, 27])
 def test_a_shorter_workspace(tiles):
     """Room for some of the requests' key tiles (9, 10 and 8 of them): the others are converted
-    as they are needed, the result is the same but for the order of nothing."""
+    as they are needed, with the same result."""
     import paged_kv_cache_36_gb300 as pkv
-    step = Step(5, [(520, 600), (600, 611), (1, 77), (530, 490)], 8, 2, 64)
-    ws = pkv.new_workspace_fp8(8, 2, 64)
+    step = Step(5, [(520, 600), (600, 611), (1, 77), (530, 490)], 8, 2, 128)
+    ws = pkv.new_workspace_fp8(8, 2, 128)
     whole, err = _run(step, ws)
-    tile = 2 * (2 * 16384 + 64 * 4 + 4)
+    tile = _tile_bytes(2, 128)
     need = ws.numel() - (256 << 20) // tile * tile
     got, err = _run(step, ws[:need + tiles * tile])
     assert err == 0 and torch.equal(got, whole)
@@ -70,7 +92,7 @@ def test_a_shorter_workspace(tiles):
 
 def test_block_ids_outside_the_pool_read_as_zeros():
     import paged_kv_cache_36_gb300 as pkv
-    step = Step(6, [(520, 600), (1, 5)], 4, 2, 64)
+    step = Step(6, [(520, 700), (1, 5)], 4, 2, 128)
     blk = step.table[0, 40]
     step.k[blk] = step.v[blk] = 0
     ref, tol = step.reference()
@@ -97,7 +119,7 @@ def test_a_workspace_used_again():
 def test_many_requests():
     """More requests than a plan in shared memory has entries, one of them with images."""
     reqs = [(2, i % 5) for i in range(4500)] + [(520, 600)] + [(1, 9)] * 300
-    step = Step(8, reqs, 2, 1, 64)
+    step = Step(8, reqs, 2, 1, 128)
     out, err = _run(step)
     assert err == 0
     check(out, *step.reference())
