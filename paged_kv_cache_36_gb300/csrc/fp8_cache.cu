@@ -28,8 +28,12 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWindow = 16;  // tokens of a window, at most
+constexpr int kThreads = 256;  // of a write's CTA, or a gather's
+constexpr int kWindow = 16;  // tokens of a gather's window, at most
+// Of a write's.  8192 tokens in order, 8 heads of 128: 19.9 us with 8, 20.7 with 4, 23.0 with
+// 16 (half of the windows of 8 have no block to begin, and end at once; those of 16 leave
+// some CTAs with twice the others' work).
+constexpr int kWriteWindow = 8;
 
 enum Rope { kNone, kHalf, kInterleaved };
 
@@ -95,7 +99,12 @@ struct Words<float> {
 };
 template <>
 struct Words<__nv_bfloat16> {  // two elements a word
-  __device__ __forceinline__ static void most(uint32_t w, uint32_t& m) { m = __vmaxu2(m, w & 0x7fff7fffu); }
+  // (a NaN does not count, and needs nothing done about it)
+  __device__ __forceinline__ static void most(uint32_t w, uint32_t& m) {
+    const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    m = *reinterpret_cast<const uint32_t*>(&x);
+  }
   __device__ __forceinline__ static uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
   __device__ __forceinline__ static uint32_t finite(uint32_t w, uint32_t& m) {
     uint32_t lo = 0u, hi = 0u;
@@ -351,9 +360,12 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
       uint4 o = make_uint4(0u, 0u, 0u, 0u);
       if (!anew && keep != 0u) o = *at;
       uint32_t w[4] = {o.x, o.y, o.z, o.w};
+      if (grown) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = e4m3x4_rescale(w[i], down);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (grown) w[i] = e4m3x4_rescale(w[i], down);
         const uint32_t n = f32x4_to_e4m3(raw[0].at(4 * j + i), raw[1].at(4 * j + i), raw[2].at(4 * j + i),
                                          raw[3].at(4 * j + i));
         w[i] = (w[i] & keep) | (n & ~keep);
@@ -451,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) reshape_and_
       return;
     }
   }
-  __shared__ int block_of[kWindow], first_of[kWindow], taken[kWindow];
-  __shared__ int rows[kWindow][kF8Block];
+  __shared__ int block_of[kWriteWindow], first_of[kWriteWindow], taken[kWriteWindow];
+  __shared__ int rows[kWriteWindow][kF8Block];
   __shared__ int found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int win = blockIdx.x / p.splits, split = blockIdx.x - win * p.splits;
@@ -498,32 +510,48 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) reshape_and_
     }
     if (lane == 0) found = __popc(leads);
   }
-  for (int i = threadIdx.x; i < kWindow * kF8Block; i += kThreads) rows[i / kF8Block][i % kF8Block] = -1;
+  for (int i = threadIdx.x; i < kWriteWindow * kF8Block; i += kThreads) rows[i / kF8Block][i % kF8Block] = -1;
   __syncthreads();
   const int leads = found;
   if (leads == 0) return;
   // ---- the other tokens of those blocks, two blocks at a time (in the order of the requests
   // a window has hardly more) ----
-  constexpr int kAhead = 8;
   for (int k = 0; k < leads; k += 2) {
     const uint32_t b0 = block_of[k], b1 = block_of[min(k + 1, leads - 1)];
-    for (int base = threadIdx.x; base < p.num_tokens; base += kThreads * kAhead) {
-      int64_t slot[kAhead];
+    auto look = [&](int64_t slot, int t) {
+      const uint32_t b = static_cast<uint32_t>(slot >> 4);
+      if (b != b0 && b != b1) return;
+      if (block_at(t, false) < 0) return;  // (a slot past 2^36 may look like another)
+      const int i = b == b0 ? k : k + 1;
+      if (t < first_of[i]) taken[i] = 1;
+      atomicMax(&rows[i][slot % kF8Block], t);
+    };
+    // eight slots a thread at a time, where there are as many and they are aligned
+    constexpr int kAhead = 4;
+    int t = 0;
+    if ((reinterpret_cast<uintptr_t>(p.slot_mapping) & 15u) == 0) {
+      const longlong2* pairs = reinterpret_cast<const longlong2*>(p.slot_mapping);
+      for (; t + 2 * kThreads * kAhead <= p.num_tokens; t += 2 * kThreads * kAhead) {
+        longlong2 s[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int t = base + u * kThreads;
-        slot[u] = t < p.num_tokens ? __ldg(p.slot_mapping + t) : -1;
-      }
+        for (int u = 0; u < kAhead; ++u) s[u] = __ldg(pairs + t / 2 + u * kThreads + threadIdx.x);
+        bool any = false;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const uint32_t b = static_cast<uint32_t>(slot[u] >> 4);
-        if (b != b0 && b != b1) continue;
-        const int t = base + u * kThreads, i = b == b0 ? k : k + 1;
-        if (block_at(t, false) < 0) continue;  // (a slot past 2^36 may look like another)
-        if (t < first_of[i]) taken[i] = 1;
-        atomicMax(&rows[i][slot[u] % kF8Block], t);
+        for (int u = 0; u < kAhead; ++u) {
+          const uint32_t x = static_cast<uint32_t>(s[u].x >> 4), y = static_cast<uint32_t>(s[u].y >> 4);
+          any |= x == b0 || x == b1 || y == b0 || y == b1;
+        }
+        if (any) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int at = t + 2 * (u * kThreads + static_cast<int>(threadIdx.x));
+            look(s[u].x, at);
+            look(s[u].y, at + 1);
+          }
+        }
       }
     }
+    for (t += threadIdx.x; t < p.num_tokens; t += kThreads) look(__ldg(p.slot_mapping + t), t);
   }
   __syncthreads();
   const int per = 2 * p.hkv;
@@ -550,44 +578,105 @@ __device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// One warp per token; every value is exact in either output type.  A lane takes 16 dimensions
-// of a key at a time (a vector of codes), and 4 of a value: the vector that holds them has
-// three other tokens' too, which the warps beside this one find in L1 if their tokens follow
-// one another.
+__device__ __forceinline__ float scale_of(const uint8_t* chunk, int d) {
+  return f8_pow2(f8_scale(__ldg(chunk + f8_code_bytes(d))) - 127);
+}
+
+struct GatherParams {
+  const uint8_t* key_cache;
+  const uint8_t* value_cache;
+  const int64_t* slot_mapping;
+  void* key_out;
+  void* value_out;
+  int64_t key_stride;    // elements
+  int64_t value_stride;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int32_t hkv;
+  int32_t window;        // tokens of a CTA at a time
+  uint32_t* err;
+};
+
+// One token, all heads, by a warp.  A lane takes 16 dimensions of a key at a time (a vector of
+// codes), and 4 of a value: the vector that holds them has three other tokens' too.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(
-    const uint8_t* __restrict__ key_cache, const uint8_t* __restrict__ value_cache,
-    const int64_t* __restrict__ slot_mapping, T* __restrict__ key_out, T* __restrict__ value_out,
-    int64_t key_stride, int64_t value_stride, int64_t num_tokens, int64_t num_slots, int32_t hkv,
-    uint32_t* __restrict__ err) {
-  grid_dependency_wait();  // the kernel before it may write the cache
-  if (threadIdx.x == 0) grid_launch_dependents();
+__device__ __forceinline__ void gather_token(const GatherParams& p, int64_t t, int64_t slot, bool in, int lane) {
   constexpr int P = D / 8, kAhead = 4;
-  const int lane = threadIdx.x & 31;
-  const int64_t wpb = kThreads / 32;
-  const int nk = hkv * D / 16, nv = hkv * D / 4;
-  for (int64_t t = blockIdx.x * wpb + (threadIdx.x >> 5); t < num_tokens; t += gridDim.x * wpb) {
-    const int64_t slot = __ldg(slot_mapping + t);
-    if (slot < 0) continue;
-    const bool in = slot < num_slots;
-    if (!in && lane == 0 && err) atomicOr(err, PKV_ERR_SLOT);
-    const int row = static_cast<int>(slot & (kF8Block - 1));
-    const int64_t blk = (in ? slot / kF8Block : 0) * hkv * f8_chunk_bytes(D);
-    const uint8_t* kblk = key_cache + blk + (row >> 3) * (D / 64) * 512 + (row & 7) * 64;
-    const uint8_t* vblk = value_cache + blk + ((row & 7) >> 1) * 16;
-    const int byte = (row >> 3) * 2 + (row & 1);  // of a V word
-    T* ko = key_out + t * key_stride;
-    T* vo = value_out + t * value_stride;
-    for (int i = lane; i < nk; i += 32) {
-      const int h = i / (D / 16), c = i % (D / 16);
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      float scale = 0.f;
-      if (in) {
-        const uint8_t* chunk = kblk + h * f8_chunk_bytes(D);
-        w = __ldg(reinterpret_cast<const uint4*>(chunk + (c >> 2) * 512 + (c & 3) * 16));
-        scale = f8_pow2(f8_scale(__ldg(key_cache + blk + h * f8_chunk_bytes(D) + f8_code_bytes(D))) - 127);
+  const int nk = p.hkv * D / 16, nv = p.hkv * D / 4;
+  const int row = static_cast<int>(slot & (kF8Block - 1));
+  const int64_t blk = (in ? slot / kF8Block : 0) * p.hkv * f8_chunk_bytes(D);
+  const uint8_t* kblk = p.key_cache + blk;
+  const uint8_t* vblk = p.value_cache + blk;
+  T* ko = static_cast<T*>(p.key_out) + t * p.key_stride;
+  T* vo = static_cast<T*>(p.value_out) + t * p.value_stride;
+  for (int i = lane; i < nk; i += 32) {
+    const int h = i / (D / 16), c = i % (D / 16);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    float scale = 0.f;
+    if (in) {
+      const uint8_t* chunk = kblk + h * f8_chunk_bytes(D);
+      w = __ldg(reinterpret_cast<const uint4*>(chunk + f8_key_at<D>(row, 16 * c)));
+      scale = scale_of(chunk, D);
+    }
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float a[4], b[4];
+      e4m3x4_to_f32(words[2 * k], a);
+      e4m3x4_to_f32(words[2 * k + 1], b);
+      const float x[8] = {a[0] * scale, a[1] * scale, a[2] * scale, a[3] * scale,
+                          b[0] * scale, b[1] * scale, b[2] * scale, b[3] * scale};
+      store8(ko + 16 * i + 8 * k, x);
+    }
+  }
+  const uint32_t low = 0x0040u + 0x0011u * ((row >> 3) * 2 + (row & 1));  // the token's bytes of two words, side by side
+  for (int base = lane; base < nv; base += 32 * kAhead) {
+    uint4 w[kAhead];
+    float scale[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = base + 32 * u;
+      const int h = i / (D / 4), c = i % (D / 4);  // dims 4 c .. + 3: lane group c / (P / 4), vector c % (P / 4)
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      scale[u] = 0.f;
+      if (in && i < nv) {
+        const uint8_t* chunk = vblk + h * f8_chunk_bytes(D);
+        w[u] = __ldg(reinterpret_cast<const uint4*>(chunk + c % (P / 4) * 512 + (c / (P / 4) * 4 + (row & 7) / 2) * 16));
+        scale[u] = scale_of(chunk, D);
       }
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = base + 32 * u;
+      if (i >= nv) break;
+      float x[4];
+      e4m3x4_to_f32(__byte_perm(__byte_perm(w[u].x, w[u].y, low), __byte_perm(w[u].z, w[u].w, low), 0x5410), x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= scale[u];
+      store4(vo + 4 * i, x);
+    }
+  }
+}
+
+// One block's keys, or values, of a head by a warp: row r goes to token rows[r], if any.
+template <typename T, int D, bool kIsV>
+__device__ __forceinline__ void gather_block(const GatherParams& p, int64_t blk, bool in, int h, const int64_t* rows, int lane) {
+  constexpr int NV = D / 32, P = D / 8;
+  const uint8_t* chunk = (kIsV ? p.value_cache : p.key_cache) + (blk * p.hkv + h) * f8_chunk_bytes(D);
+  uint4 w[NV];
+  float scale = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) w[j] = in ? __ldg(reinterpret_cast<const uint4*>(chunk + j * 512) + lane) : make_uint4(0u, 0u, 0u, 0u);
+  if (in) scale = scale_of(chunk, D);
+  T* out = static_cast<T*>(kIsV ? p.value_out : p.key_out) + static_cast<int64_t>(h) * D;
+  const int64_t stride = kIsV ? p.value_stride : p.key_stride;
+  if constexpr (!kIsV) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t t = rows[(lane >> 2) + 8 * (j / (D / 64))];
+      if (t < 0) continue;
+      T* to = out + t * stride + 64 * (j % (D / 64)) + 16 * (lane & 3);
+      const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float a[4], b[4];
@@ -595,37 +684,83 @@ __global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(
         e4m3x4_to_f32(words[2 * k + 1], b);
         const float x[8] = {a[0] * scale, a[1] * scale, a[2] * scale, a[3] * scale,
                             b[0] * scale, b[1] * scale, b[2] * scale, b[3] * scale};
-        store8(ko + 16 * i + 8 * k, x);
+        store8(to + 8 * k, x);
       }
     }
-    const uint32_t low = 0x0040u + 0x0011u * byte;  // bytes `byte` of two words, side by side
-    for (int base = lane; base < nv; base += 32 * kAhead) {
-      uint4 w[kAhead];
-      uint32_t e[kAhead];
+  } else {
+    int64_t t[4];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = base + 32 * u;
-        const int h = i / (D / 4), c = i % (D / 4);  // dims 4 c .. + 3: lane group c / (P / 4), vector c % (P / 4)
-        w[u] = make_uint4(0u, 0u, 0u, 0u);
-        e[u] = 127u;
-        if (in && i < nv) {
-          w[u] = __ldg(reinterpret_cast<const uint4*>(vblk + h * f8_chunk_bytes(D) + c % (P / 4) * 512 + c / (P / 4) * 64));
-          e[u] = __ldg(value_cache + blk + h * f8_chunk_bytes(D) + f8_code_bytes(D));
-        }
+    for (int i = 0; i < 4; ++i) t[i] = rows[2 * (lane & 3) + (i & 1) + 8 * (i >> 1)];
+#pragma unroll
+    for (int k = 0; k < P / 8; ++k) {  // eight dimensions
+      const uint32_t words[8] = {w[2 * k].x, w[2 * k].y, w[2 * k].z, w[2 * k].w,
+                                 w[2 * k + 1].x, w[2 * k + 1].y, w[2 * k + 1].z, w[2 * k + 1].w};
+      float x[4][8];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        float a[4];
+        e4m3x4_to_f32(words[d], a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i][d] = a[i] * scale;
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = base + 32 * u;
-        if (i >= nv) break;
-        const uint32_t four = __byte_perm(__byte_perm(w[u].x, w[u].y, low), __byte_perm(w[u].z, w[u].w, low), 0x5410);
-        const float scale = f8_pow2(f8_scale(e[u]) - 127);
-        float x[4];
-        e4m3x4_to_f32(four, x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] *= scale;
-        store4(vo + 4 * i, x);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (t[i] >= 0) store8(out + t[i] * stride + P * (lane >> 2) + 8 * k, x[i]);
     }
+  }
+}
+
+// Every value is exact in either output type.  A CTA takes a window of tokens.  Runs of them
+// that follow one another in a block are read by block, a warp a head and K or V; where the
+// window has more than a run in four tokens, a warp takes a token.  (8192 tokens in order, 8
+// heads of 128, bfloat16: by token 16.5 us.  7777 in random order, 5 heads of 64, float32: by
+// token 8.3.)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(const GatherParams p) {
+  grid_dependency_wait();  // the kernel before it may write the cache
+  if (threadIdx.x == 0) grid_launch_dependents();
+  __shared__ int64_t rows[kWindow][kF8Block];  // by run: the tokens of a block's rows
+  __shared__ int64_t slots[kWindow];
+  __shared__ int first[kWindow];               // tokens (of the window) that begin a run
+  __shared__ int count[2];                     // of runs, and of tokens
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t T0 = static_cast<int64_t>(blockIdx.x) * p.window; T0 < p.num_tokens;
+       T0 += static_cast<int64_t>(gridDim.x) * p.window) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.window), p.num_tokens - T0));
+    for (int i = threadIdx.x; i < kWindow * kF8Block; i += kThreads) rows[i / kF8Block][i % kF8Block] = -1;
+    __syncthreads();
+    if (warp == 0) {
+      const int64_t slot = lane < n ? __ldg(p.slot_mapping + T0 + lane) : -1;
+      const int64_t prev = __shfl_up_sync(0xffffffffu, slot, 1);
+      // (rows of a run ascend, so each is one token's)
+      const bool leads = slot >= 0 && (lane == 0 || prev < 0 || prev / kF8Block != slot / kF8Block || prev >= slot);
+      const unsigned lead = __ballot_sync(0xffffffffu, leads), live = __ballot_sync(0xffffffffu, slot >= 0);
+      const int k = __popc(lead & (0xffffffffu >> (31 - lane))) - 1;
+      if (lane < n) slots[lane] = slot;
+      if (slot >= 0) rows[k][slot % kF8Block] = T0 + lane;
+      if (leads) first[k] = lane;
+      if (lane == 0) {
+        count[0] = __popc(lead);
+        count[1] = __popc(live);
+      }
+      if (slot >= p.num_slots && p.err) atomicOr(p.err, PKV_ERR_SLOT);
+    }
+    __syncthreads();
+    const int runs = count[0], per = 2 * p.hkv;
+    if (4 * runs <= count[1]) {
+      for (int i = warp; i < runs * per; i += kThreads / 32) {
+        const int k = i / per, item = i - k * per;
+        const int64_t slot = slots[first[k]];
+        const bool in = slot < p.num_slots;
+        const int64_t blk = in ? slot / kF8Block : 0;
+        if (item & 1) gather_block<T, D, true>(p, blk, in, item >> 1, rows[k], lane);
+        else gather_block<T, D, false>(p, blk, in, item >> 1, rows[k], lane);
+      }
+    } else {
+      for (int i = warp; i < n; i += kThreads / 32)
+        if (slots[i] >= 0) gather_token<T, D>(p, T0 + i, slots[i], slots[i] < p.num_slots, lane);
+    }
+    __syncthreads();  // the tables are written again
   }
 }
 
@@ -653,13 +788,13 @@ cudaError_t write_t(const F8WriteArgs& a, cudaStream_t stream) {
   p.query_stride = a.query_stride;
   p.query_out_stride = a.query_out_stride;
   const int sms = current_sm_count();
-  // a token a window while there are SMs for them; 16 where a batch is long
+  // a token a window while there are SMs for them
   const int64_t want = (a.cache.num_tokens + 4 * sms - 1) / (4 * sms);
-  p.window = static_cast<int32_t>(want < kWindow ? want : kWindow);
+  p.window = static_cast<int32_t>(want < kWriteWindow ? want : kWriteWindow);
   const int windows = (p.num_tokens + p.window - 1) / p.window;
   p.splits = (2 * p.hkv + kThreads / 32 - 1) / (kThreads / 32);
-  const int most = (4 * sms + windows - 1) / windows;
-  if (p.splits > most) p.splits = most;
+  const int most = 4 * sms / windows;  // one wave
+  if (p.splits > most) p.splits = most > 1 ? most : 1;
   p.cache_ctas = windows * p.splits;
   int64_t grid = p.cache_ctas;
   if (kRope != kNone) {
@@ -678,13 +813,23 @@ cudaError_t write_d(const F8WriteArgs& a, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t gather_t(const MxCacheArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (a.num_tokens + 7) / 8, cap = static_cast<int64_t>(current_sm_count()) * 64;
-  return launch_programmatic(
-      gather_cache_fp8_kernel<T, D>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kThreads), 0,
-      stream, static_cast<const uint8_t*>(a.key_cache), static_cast<const uint8_t*>(a.value_cache),
-      a.slot_mapping, static_cast<T*>(const_cast<void*>(a.key)),
-      static_cast<T*>(const_cast<void*>(a.value)), a.key_stride, a.value_stride, a.num_tokens,
-      a.num_slots, a.num_kv_heads, a.err);
+  GatherParams p;
+  p.key_cache = a.key_cache;
+  p.value_cache = a.value_cache;
+  p.slot_mapping = a.slot_mapping;
+  p.key_out = const_cast<void*>(a.key);
+  p.value_out = const_cast<void*>(a.value);
+  p.key_stride = a.key_stride;
+  p.value_stride = a.value_stride;
+  p.num_tokens = a.num_tokens;
+  p.num_slots = a.num_slots;
+  p.hkv = a.num_kv_heads;
+  p.err = a.err;
+  const int64_t sms = current_sm_count(), want = (a.num_tokens + 4 * sms - 1) / (4 * sms);
+  p.window = static_cast<int32_t>(want < kWindow ? want : kWindow);
+  const int64_t windows = (a.num_tokens + p.window - 1) / p.window, cap = 64 * sms;
+  return launch_programmatic(gather_cache_fp8_kernel<T, D>, dim3(static_cast<unsigned>(windows < cap ? windows : cap)),
+                             dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace
