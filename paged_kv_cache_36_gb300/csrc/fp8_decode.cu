@@ -43,7 +43,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kMinUnits = 8;     // units in a range, nearly: at least 4
+constexpr int kMinUnits = 3;     // units in a range, nearly: at least 2, more than kF8RequestCost
 // Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
 // one exceeds 2^kMost.
 constexpr float kLargest = -24.f, kMost = 8.f;
@@ -273,6 +273,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
   }
   Cursor at = next;
   int ahead = 0;  // stages that are filled and not read
+  // the query heads of the request that the cursor has come to are wanted some stages on
+  auto want_queries = [&]() {
+    if (lane * 128 < 2 * G * D)
+      prefetch_l2(p.q + static_cast<int64_t>(__ldg(p.qsl + next.r)) * p.q_stride +
+                  static_cast<int64_t>(h * G) * D + lane * 64);
+  };
   auto fetch = [&]() {
     if (next.run <= 0) return;
     const bool in = id < num_blocks;
@@ -294,14 +300,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     if (--next.run == 0 && next.rest > 0) {
       next.next_run(prefix);
       row = p.block_table + static_cast<int64_t>(next.r) * p.bt_stride;
-      // its query heads are wanted some stages on
-      if (lane * 128 < 2 * G * D)
-        prefetch_l2(p.q + static_cast<int64_t>(__ldg(p.qsl + next.r)) * p.q_stride +
-                    static_cast<int64_t>(h * G) * D + lane * 64);
+      want_queries();
     }
     if (next.run > 0) id = static_cast<uint32_t>(__ldg(row));
   };
   id = static_cast<uint32_t>(__ldg(row));
+  want_queries();
   __syncwarp();
   for (int s = 0; s < stages - 1; ++s) fetch();
   if (h < kWarps) write_plan();  // with the first bytes on their way
@@ -569,20 +573,24 @@ __device__ __forceinline__ float range_weight(float2 ml) {
   return ml.x + static_cast<float>(static_cast<int>(__float_as_uint(ml.y) >> 23) - 127);
 }
 
-// Joins the partials of every request that crosses ranges.  kLanes lanes take 4
-// kLanes dimensions of one (request, query head); the groups of a warp take the
-// ranges in turn, kBatch loads of a lane in flight, and add up at the end.
-template <int D, int kLanes>
+// Joins the partials of every request that crosses ranges.  kLanes lanes take 4 kLanes
+// dimensions of one (request, query head); the groups of a warp, or with kTogether of all
+// warps of the CTA, take the ranges in turn, kBatch loads of a lane in flight, and add up at
+// the end.
+template <int D, int kLanes, bool kTogether>
 __global__ void __launch_bounds__(256, 4) join_fp8_kernel(const Params p) {
   grid_dependency_wait();  // the decode's partials
   if (threadIdx.x == 0) grid_launch_dependents();
-  constexpr int kBatch = 4, kParts = 32 / kLanes, kItems = D / (4 * kLanes);
+  constexpr int kBatch = 4, kItems = D / (4 * kLanes), kGroups = 32 / kLanes;
+  constexpr int kParts = kTogether ? 8 * kGroups : kGroups;
+  __shared__ float4 part_acc[kTogether ? 8 : 1][kLanes];
+  __shared__ float2 part_sum[kTogether ? 8 : 1];
   const int G = p.group, H = p.hkv * G;
-  const int lane = threadIdx.x & 31, part = lane / kLanes;
-  const int per_req = H * kItems;  // warps' items of a request
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = (kTogether ? warp * kGroups : 0) + lane / kLanes;
+  const int per_req = H * kItems;  // items of a request
   const int64_t total = static_cast<int64_t>(p.num_reqs) * per_req;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < total;
-       i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
+  const int64_t first = kTogether ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  for (int64_t i = first; i < total; i += static_cast<int64_t>(gridDim.x) * (kTogether ? 1 : 8)) {
     const int r = static_cast<int>(i / per_req);
     const int item = static_cast<int>(i - static_cast<int64_t>(r) * per_req);
     const int2 to_join = __ldcg(p.plan + r);
@@ -644,6 +652,30 @@ __global__ void __launch_bounds__(256, 4) join_fp8_kernel(const Params p) {
         a[c] += __shfl_xor_sync(0xffffffffu, a[c], x);
       }
     }
+    if constexpr (kTogether) {
+      __syncthreads();  // the item before is read
+      if (lane < kLanes) part_acc[warp][lane] = acc;
+      if (lane == 0) part_sum[warp] = make_float2(big, den);
+      __syncthreads();
+      if (warp == 0) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) mx = fmaxf(mx, part_sum[w].x);
+        den = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float2 sum = part_sum[w];
+          const float f = sum.x == mx ? 1.f : exp2_approx(sum.x - mx);
+          const float4 x = part_acc[w][lane & (kLanes - 1)];
+          den = fmaf(sum.y, f, den);
+          acc.x = fmaf(x.x, f, acc.x);
+          acc.y = fmaf(x.y, f, acc.y);
+          acc.z = fmaf(x.z, f, acc.z);
+          acc.w = fmaf(x.w, f, acc.w);
+        }
+      }
+    }
     if (part == 0) {
       const float inv = 1.f / den;
       const int64_t tok = __ldg(p.qsl + r);
@@ -669,16 +701,21 @@ cudaError_t launch_t(Params p, int sms, cudaStream_t stream) {
   e = launch_programmatic(decode_fp8_kernel<D, NT>, dim3(static_cast<unsigned>(sms)),
                           dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  // Few requests have many ranges each: eight lanes take 32 dimensions, four ranges at a
-  // time.  Where that is more than a wave of warps, more lanes and fewer ranges.
+  // Few requests have many ranges each: eight lanes take 32 dimensions, and the warps of a CTA
+  // an item together (one request of 30000 tokens, 16/4 heads of 64: 36 us with a warp an
+  // item) or, where that is more than a wave of warps, each its own, four ranges at a time;
+  // where that is too, more lanes and fewer ranges.
   const int64_t heads = static_cast<int64_t>(p.num_reqs) * p.hkv * p.group;
   const int64_t wave = 32 * static_cast<int64_t>(sms);
   constexpr int kWide = D / 4;
   const int lanes = heads * (D / 32) <= wave ? 8 : heads * (D / 64) <= wave ? 16 : kWide;
-  const int64_t grid = (heads * (D / (4 * lanes)) + 7) / 8;
-  return launch_programmatic(lanes == 8    ? join_fp8_kernel<D, 8>
-                             : lanes == 16 ? join_fp8_kernel<D, 16>
-                                           : join_fp8_kernel<D, kWide>,
+  const int64_t items = heads * (D / (4 * lanes));
+  const bool together = lanes == 8 && 8 * items <= wave;
+  const int64_t grid = together ? items : (items + 7) / 8;
+  return launch_programmatic(together      ? join_fp8_kernel<D, 8, true>
+                             : lanes == 8  ? join_fp8_kernel<D, 8, false>
+                             : lanes == 16 ? join_fp8_kernel<D, 16, false>
+                                           : join_fp8_kernel<D, kWide, false>,
                              dim3(static_cast<unsigned>(grid < wave / 4 ? grid : wave / 4)),
                              dim3(256), 0, stream, p);
 }

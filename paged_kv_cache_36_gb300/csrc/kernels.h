@@ -259,7 +259,7 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, in
                                cudaStream_t stream);
 
 // What the change to a request costs a warp of the 8-bit decode, in blocks.
-constexpr int kF8RequestCost = 2;
+constexpr int kF8RequestCost = 1;
 
 // Slots of the 8-bit decode on a device of `sms` SMs.
 int64_t decode_fp8_slots(int sms, int num_kv_heads);
