@@ -142,10 +142,11 @@ struct Params {
   // Key tiles converted ahead (null: none): request r's are images image_base[r] hkv on, its
   // key tiles in order, KV head fastest; -1: none, its rows are converted as they are needed.
   // any[0]: whether there are such; any[1]: whether there are images.  image_nan: by image,
-  // whether V has a NaN.
+  // whether V has a NaN; nan_seen: whether one of this call's has (zero between calls).
   uint8_t* images;
   int32_t* image_base;
   int32_t* image_nan;
+  uint32_t* nan_seen;
   int32_t* any;
   int32_t image_tiles;  // key tiles (of all KV heads) there is room for
   int32_t sms;
@@ -497,6 +498,8 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
   // the kernel before may write the images, q, the cache, out or the metadata
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
+  // (the kernel over images is through)
+  if (!kImages && p.images != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.nan_seen = 0u;
   if (kImages ? __ldcg(p.any + 1) == 0 : p.images != nullptr && __ldcg(p.any) == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.num_reqs;
@@ -655,6 +658,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
     uint64_t* pair_bar = &bars[kPair0 + quad];
     // never zero, for the masked scores' infinities; the scale's sign is on Q
     const float f = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+    const bool nan_seen = kImages && __ldcg(p.nan_seen) != 0u;
     uint32_t count = 0, pair_uses = 0, tiles_done = 0;
     auto exchange = [&](float mine) -> float {
       float* slot = xch + (pair_uses & 1) * 256;
@@ -665,20 +669,14 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
       ++pair_uses;
       return done ? slot[(half ^ 1) * 128 + row] : mine;
     };
-    for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0;
-         ct = cta_tile(++it, cid, ncta, total)) {
+    const int u = row / G;
+    int ct = cta_tile(0, cid, ncta, total);
+    Tile t = find_tile<kImages>(ct, prefix, entries, p, tpt);
+    for (int it = 0; ct >= 0;) {
       if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-      const Tile t = find_tile<kImages>(ct, prefix, entries, p, tpt);
-      const int u = row / G;
       const int pos = t.nc + t.u0 + (u < t.ntok ? u : t.ntok - 1);
       const int pos_min = t.nc + t.u0;
       float m_used = -INFINITY, l = 0.f;
-      // whether an image of these keys has a NaN in V (looked at when the tile is through)
-      int nan_images = 0;
-      if constexpr (kImages) {
-        const int32_t* at = p.image_nan + static_cast<int64_t>(__ldcg(p.image_base + t.r)) * p.hkv + t.h;
-        for (int j = lane; j < t.nkt; j += 32) nan_images |= __ldcg(at + static_cast<int64_t>(j) * p.hkv);
-      }
       bool ok = true;
       for (int j = 0; j < t.nkt && ok; ++j, ++count) {
         const int b = count % kSBufs;
@@ -743,6 +741,10 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         if (lane == 0) mbar_arrive(&bars[kPFull0 + b]);
       }
       if (!ok) break;
+      // (the next query tile is looked up while P V ends)
+      ct = cta_tile(++it, cid, ncta, total);
+      Tile next = t;
+      if (ct >= 0) next = find_tile<kImages>(ct, prefix, entries, p, tpt);
       // ---- epilogue: O / (l_0 + l_1) -> out ----
       if (!warp_wait(&bars[kOFinal], tiles_done & 1, p.err, abort_flag)) break;
       tc_fence_after();
@@ -750,7 +752,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
       // dimensions of this warp's half in which the row sees a NaN
       uint64_t nan_dims = 0u;
       if constexpr (kImages) {
-        if (__any_sync(0xffffffffu, nan_images != 0)) {
+        if (nan_seen) {
           const int64_t first = static_cast<int64_t>(__ldcg(p.image_base + t.r)) * p.hkv + t.h;
           for (int j = 0; j < t.nkt; ++j) {
             const int64_t i = first + static_cast<int64_t>(j) * p.hkv;
@@ -813,6 +815,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         }
       }
       tc_fence_before();
+      t = next;
     }
   }
 
@@ -934,7 +937,10 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
     store_keys<D>(image, warp, k, lane);
     store_values<D>(image + kHalf, warp, v, lane);
     const bool any = __syncthreads_or(nan);
-    if (threadIdx.x == 0) p.image_nan[i] = any ? 1 : 0;
+    if (threadIdx.x == 0) {
+      p.image_nan[i] = any ? 1 : 0;
+      if (any) atomicOr(p.nan_seen, 1u);
+    }
     if (any) {
       if (threadIdx.x < D) {
         reinterpret_cast<int32_t*>(image + 2 * kHalf)[threadIdx.x] = nans[threadIdx.x];
@@ -1003,6 +1009,7 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, in
   p.group = a.num_heads / a.num_kv_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
+  p.nan_seen = a.err + 1;
   p.entry_shift = 0;
   p.images = nullptr;
   p.image_base = p.image_nan = p.any = nullptr;
