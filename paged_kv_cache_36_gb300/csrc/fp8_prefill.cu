@@ -825,8 +825,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Makes the images: a CTA takes one at a time, a block's keys and values each of its eight
-// warps.  Also decides which requests have images, and reports bad metadata.
+// Makes the images: a CTA takes the K or the V of one at a time, a block each of its eight warps.  Also decides which requests have images, and reports bad metadata.
 template <int D>
 __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
   constexpr uint32_t kHalf = Layout<D>::kHalf;
@@ -905,8 +904,9 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
     }
   }
   const uint64_t block_bytes = static_cast<uint64_t>(p.hkv) * f8_chunk_bytes(D);
-  for (int64_t i = blockIdx.x;; i += gridDim.x) {
-    const int64_t tile = i / p.hkv;
+  for (int64_t x = blockIdx.x;; x += gridDim.x) {
+    const int64_t i = x >> 1, tile = i / p.hkv;
+    const bool is_v = x & 1;
     if (tile >= prefix[R]) break;
     const int h = static_cast<int>(i - tile * p.hkv);
     int lo = 0, hi = R;  // prefix[lo] <= tile < prefix[hi]
@@ -917,25 +917,25 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
     if (prefix[lo + 1] > p.image_tiles) break;  // and so are the requests after it
     const int at = static_cast<int>(tile - prefix[lo]) * kKeys + warp * kF8Block;
     const int seq = __ldg(p.seq_lens + lo);
-    Codes<D> k, v;
-    k.zero();
-    v.zero();
+    Codes<D> c;
+    c.zero();
     if (at < seq) {
       const int id = __ldg(p.block_table + static_cast<int64_t>(lo) * p.bt_stride + at / kF8Block);
-      if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.num_blocks)) {
-        const uint64_t off = static_cast<uint32_t>(id) * block_bytes + static_cast<uint64_t>(h) * f8_chunk_bytes(D);
-        k.load(p.key_cache + off, lane);
-        v.load(p.value_cache + off, lane);
-      } else if (lane == 0) {
+      if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.num_blocks))
+        c.load((is_v ? p.value_cache : p.key_cache) + static_cast<uint32_t>(id) * block_bytes +
+                   static_cast<uint64_t>(h) * f8_chunk_bytes(D), lane);
+      else if (lane == 0)
         atomicOr(p.err, PKV_ERR_BLOCK_ID);
-      }
-      if (at + kF8Block > seq) keep_codes<D>(v, keep_tokens(seq - at, lane));
     }
-    const bool nan = has_nan<D>(v);
-    if (nan) note_nan<D>(v, nans, at, lane);
     uint8_t* image = p.images + i * static_cast<int64_t>(image_bytes<D>());
-    store_keys<D>(image, warp, k, lane);
-    store_values<D>(image + kHalf, warp, v, lane);
+    if (!is_v) {
+      store_keys<D>(image, warp, c, lane);
+      continue;
+    }
+    if (at + kF8Block > seq) keep_codes<D>(c, keep_tokens(seq - at, lane));
+    const bool nan = has_nan<D>(c);
+    if (nan) note_nan<D>(c, nans, at, lane);
+    store_values<D>(image + kHalf, warp, c, lane);
     const bool any = __syncthreads_or(nan);
     if (threadIdx.x == 0) {
       p.image_nan[i] = any ? 1 : 0;
