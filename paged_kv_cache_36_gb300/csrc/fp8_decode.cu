@@ -485,10 +485,12 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
         float e[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) e[c] = exp2_approx(s[nt][c] - m[nt][c & 1]);
-        l[nt][0] += e[0] + e[2];
-        l[nt][1] += e[1] + e[3];
-        pt[nt][0] = transpose_8x8(pack_bf16(e[0], e[1]));
-        pt[nt][1] = transpose_8x8(pack_bf16(e[2], e[3]));
+        const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
+        // (the rounded ones: what rounding does to all of a row's weights cancels)
+        l[nt][0] += __uint_as_float(w0 << 16) + __uint_as_float(w1 << 16);
+        l[nt][1] += __uint_as_float(w0 & 0xffff0000u) + __uint_as_float(w1 & 0xffff0000u);
+        pt[nt][0] = transpose_8x8(w0);
+        pt[nt][1] = transpose_8x8(w1);
       }
       // ---- O^T += V^T P^T ----
       const uint32_t vs = static_cast<uint32_t>(ve << 7) * 0x00010001u;  // 2^(ve - 127)

@@ -730,8 +730,10 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         for (int e = 0; e < 32; ++e) {
           const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), f2, c2);
           const float2 pe = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-          l2[e & 1] = __fadd2_rn(l2[e & 1], pe);
           w[e] = pack_bf16(pe.x, pe.y);
+          // (the rounded ones, so that what rounding does to all of a row's weights cancels: errors of
+          // 1.1 of the result's own rounding instead of 1.4, for 4 % of the time)
+          l2[e & 1] = __fadd2_rn(l2[e & 1], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)));
         }
         tmem_st32(s_cols, w);
         l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);

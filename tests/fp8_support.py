@@ -84,8 +84,9 @@ class Step:
         2^-24, S = scale sum |q||k| of a row's worst key and A = sum_j p_j |v_j| / sum_j p_j:
           score: each of D products and a few scalings rounds at u S at most, so a weight is
             off by 2 (D + 32) u S (log2 e folded in), numerator and denominator both;
-          weight: half a bfloat16 step, 2^-8 of A (and an exponential's 2^-21).  Weights are
-            formed as 2^(s - m) with m at most 24 above the row's largest score, and vanish below
+          weight: half a bfloat16 step, 2^-8 of A in the numerator, and (the denominator sums the
+            rounded weights) 2^-8 |out|: sum_j p_j d_j (v_j - out) with |d_j| <= 2^-8 is at most
+            2^-8 (A + |out|).  (And an exponential's 2^-21.)  Weights are formed as 2^(s - m) with m at most 24 above the row's largest score, and vanish below
             2^-126 (the exponential flushes there): where p_j is below 2^-102 of the largest
             nothing is left of it, 2^-102 |v_j|;
           sums: 2 n u of A for n keys, at worst;
@@ -112,7 +113,7 @@ class Step:
                 worst = (q[:, h].abs() @ kh.abs().T * abs(self.scale)).masked_fill(~seen, 0).amax(1, keepdim=True)
                 mean = p @ vh.abs()
                 ref[a:b, h] = out.masked_fill(nan, torch.nan)
-                tol[a:b, h] = (2.0 ** -8 * out.abs()
+                tol[a:b, h] = (2.0 ** -7 * out.abs()
                                + mean * (2.0 ** -8 + 2.0 ** -20 + 4 * (self.d + 32) * u * worst + 2 * n * u)
                                + 2.0 ** -102 * (seen.double() @ vh.abs()) + 2.0 ** -134)
         return ref, tol
