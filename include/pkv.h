@@ -538,8 +538,13 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
  * request, are left as they were; a block id outside the pool reads as zeros
  * (PKV_ERR_BLOCK_ID).  A request with several query tokens has 2^31 - 256 keys at most.
- * Bytes of tokens past a request's end may hold anything; a NaN in a key or value counts
- * for the rows that see it, and for no others.
+ * Bytes of tokens past a request's end may hold anything; a NaN in a key counts for the rows
+ * that see it, a NaN in a value for that dimension of those rows, and for no others.
+ *
+ * Both products take bfloat16 with float32 sums.  Keys, values and queries are exact in it (of
+ * a decode row's query nothing is kept that is 2^126 times below the head's largest element).
+ * Weights are rounded to 8 bits, numerator and denominator alike, and vanish 2^-102 below the
+ * row's largest; scores (scale <q, k>) and their sums are float32.  scale must be finite.
  *
  * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch, its first
  * 256 bytes zero before its first use, word 0 the error word; two calls that overlap on the

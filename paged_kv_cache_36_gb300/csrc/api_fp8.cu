@@ -170,6 +170,8 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   const char* where = "pkv_paged_attention_varlen_fp8";
   if (num_tokens < 0 || num_reqs < 0 || num_heads <= 0 || max_query_len < 0)
     return fail(PKV_E_INVALID, "%s: bad sizes", where);
+  if (!std::isfinite(static_cast<float>(scale * 1.4426950408889634)))
+    return fail(PKV_E_INVALID, "%s: scale must be finite", where);
   const int rc = check_cache_shape(where, num_blocks, block_size, num_kv_heads, head_dim);
   if (rc != PKV_OK) return rc;
   if (num_heads % num_kv_heads) return fail(PKV_E_INVALID, "%s: num_heads %% num_kv_heads != 0", where);

@@ -70,13 +70,14 @@ def test_rope(pkv, change, code):
     (dict(d=80), -2), (dict(H=5), -1), (dict(H=34, hkv=2), -2), (dict(ws=None), -3),
     (dict(wsb=16), -3), (dict(q=None), -1), (dict(bt=None), -1), (dict(q=P + 2), -1),
     (dict(qs=4 * 64 + 4), -1), (dict(qs=64), -1), (dict(width=0), -1), (dict(width=9), -1),
-    (dict(mql=-1), -1), (dict(nb=0), -1)])
+    (dict(mql=-1), -1), (dict(nb=0), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1),
+    (dict(scale=3e38), -1)])
 def test_attention(pkv, change, code):
     a = dict(T=3, R=2, nb=4, bs=16, H=4, hkv=2, d=64, q=P, bt=P, ws=P, wsb=1 << 40, qs=256, width=8,
-             stride=8, mql=0)
+             stride=8, mql=0, scale=0.125)
     a.update(change)
     rc = pkv.lib().pkv_paged_attention_varlen_fp8(
-        a["q"], a["qs"], P, P, a["bt"], a["stride"], a["width"], P, P, P, 0.125, P, a["qs"], a["T"],
+        a["q"], a["qs"], P, P, a["bt"], a["stride"], a["width"], P, P, P, a["scale"], P, a["qs"], a["T"],
         a["R"], a["nb"], a["bs"], a["H"], a["hkv"], a["d"], a["mql"], a["ws"], a["wsb"], None)
     assert rc == code
     if code:
