@@ -22,6 +22,17 @@
 // warps 2 and 3 copy K and V; warps 4-11 run the softmax and the epilogue, two per 32-lane
 // quadrant of tensor memory, each with half of the key tile's columns; warps 12-15 bring the
 // query rows in, and without images they convert K and warps 16-19 V.
+//
+// What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 133 us,
+// 1033 TFLOP/s, 54 % of the bf16 rate; of 16384 tokens about 1490 us, 1476 TFLOP/s, 78 %.  At 4096
+// the kernel over images has the tensor core busy 49 % of the time, 48 % of the issue slots taken
+// and 50 MB read: neither the products nor memory bound it, but the chain from S to P.
+// Measured and not kept, with what it was measured against (us, a prompt of 4096): two softmax
+// groups with key tiles in turn and an S and an O each 150 (136), with P in halves 142 (136);
+// rows written by the warps that bring Q 130 (129), with two O and two S 137 (129); two S
+// instead of three 137 (129); spinning instead of suspended waits in the issuing warps 147.5
+// (146); copies split in 4 KB 150 (146).
+//
 // Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that stops all
 // roles.
 #include <cuda_bf16.h>
@@ -95,7 +106,7 @@ enum Bar {
   kVFull0 = kKEmpty0 + kKStages, kVEmpty0 = kVFull0 + kVStages,
   kSFull0 = kVEmpty0 + kVStages, kSFree0 = kSFull0 + kSBufs,
   kPFull0 = kSFree0 + kSBufs, kODone0 = kPFull0 + kSBufs,
-  kOFinal = kODone0 + kSBufs, kPair0,
+  kOFinal = kODone0 + kSBufs, kNanRead, kPair0,
   kNumBars = kPair0 + 4
 };
 
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
       if (b == kQFull) n = 4;  // the warps that bring Q
       if (!kImages && ((b >= kKFull0 && b < kKFull0 + kKStages) || (b >= kVFull0 && b < kVFull0 + kVStages)))
         n = 4;  // the warps that convert
-      if (b >= kPFull0 && b < kPFull0 + kSBufs) n = 8;  // softmax warps
+      if ((b >= kPFull0 && b < kPFull0 + kSBufs) || b == kNanRead) n = 8;  // softmax warps
       if (b >= kPair0 && b < kPair0 + 4) n = 2;         // the two warps sharing a quadrant
       mbar_init(&bars[b], n);
     }
@@ -659,7 +670,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
     // never zero, for the masked scores' infinities; the scale's sign is on Q
     const float f = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
     const bool nan_seen = kImages && __ldcg(p.nan_seen) != 0u;
-    uint32_t count = 0, pair_uses = 0, tiles_done = 0;
+    uint32_t count = 0, pair_uses = 0, tiles_done = 0, nan_tiles = 0;
     auto exchange = [&](float mine) -> float {
       float* slot = xch + (pair_uses & 1) * 256;
       slot[half * 128 + row] = mine;
@@ -768,13 +779,15 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         const int32_t* at = nans + tiles_done % kNanBufs * D + half * (D / 2);
         for (int d = 0; d < D / 2; ++d)
           if (at[d] <= pos) nan_dims |= 1ull << d;
-        // every softmax warp has read them: ready for another query tile
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        // once every softmax warp has read them they are ready for another query tile
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kNanRead]);
         if (warp == 4) {
+          if (!warp_wait(&bars[kNanRead], nan_tiles & 1, p.err, abort_flag)) break;
           for (int d = lane; d < D; d += 32) nans[tiles_done % kNanBufs * D + d] = kNone;
           if (lane == 0) any_nan[tiles_done % kNanBufs] = 0;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ++nan_tiles;
       }
       ++tiles_done;
       // This warp holds output dims [half * D/2, half * D/2 + D/2) of its 32
