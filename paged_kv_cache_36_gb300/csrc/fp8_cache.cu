@@ -16,6 +16,11 @@
 // second pass, the result depends on no order, and of a slot given twice the last token
 // counts.  A batch in the order of its requests has one search per 16 tokens; in the worst
 // order there is one per token, T^2 / 32 steps of a warp.
+//
+// What bounds it.  8192 tokens, 8 KV heads of 128, bfloat16, nothing in L2: 19.9 us for 50 MB,
+// of them about 3 for the search; issue slots and warps 41 % busy, so latency: a warp's rows, their maximum, the codes and the stores follow one
+// another.  With RoPE of 32 query heads 35.5 us for 184 MB, 5.2 TB/s.  64 tokens 5.5 us, with
+// RoPE 5.6.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -713,8 +718,8 @@ __device__ __forceinline__ void gather_block(const GatherParams& p, int64_t blk,
 // Every value is exact in either output type.  A CTA takes a window of tokens.  Runs of them
 // that follow one another in a block are read by block, a warp a head and K or V; where the
 // window has more than a run in four tokens, a warp takes a token.  (8192 tokens in order, 8
-// heads of 128, bfloat16: by token 16.5 us.  7777 in random order, 5 heads of 64, float32: by
-// token 8.3.)
+// heads of 128, bfloat16: by token 16.5 us, by block 14.2.  7777 in random order, 5 heads of 64,
+// float32: by token 8.3.)
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(const GatherParams p) {
   grid_dependency_wait();  // the kernel before it may write the cache
