@@ -76,12 +76,16 @@ constexpr int kNone = 0x7fffffff;          // no NaN
 // Which requests have images, by what both ways cost (see expand_fp8_kernel).  In a graph a
 // CTA takes some 2.0 us for a key tile of head_dim 128 that it converts and 1.1 over images, of
 // 64 1.0 and 0.6; images cost two kernels, 6 us, and for each key tile and KV head what they
-// write and read again.  us over images / converted as they go, 32 query and 8 KV heads of 128:
-//   tokens 4096 136 / 239, 2048 58 / 74, 1024 31 / 30, 512 behind 1223 29 / 31, behind 11539 84 /
-//   141, 128 behind 3874 35 / 41, 64 behind 2048 31 / 34, 4 behind 8000 66 / 98, 4 behind 1000 25 /
-//   22; 8 requests of 256 behind 1000 71 / 75; 16 of 4 behind 4000 130 / 82.
-//   16 query and 4 KV heads of 64: tokens 4096 67 / 78, 2048 31 / 28, 512 behind 1069 24 / 20, 64
-//   behind 4096 40 / 43.
+// write and read again.  us over images / converted as they go, without those kernels, 32 query
+// and 8 KV heads of 128:
+//   tokens 4096 134 / 264, 2048 57 / 81, 1024 31.3 / 31.0, 512 behind 1223 30 / 33, behind 11539
+//   82 / 148, 128 behind 3874 35 / 42, 64 behind 2048 32 / 35, 4 behind 8000 69 / 104, 4 behind
+//   1000 25 / 23; 8 requests of 256 behind 1000 67 / 80; 16 of 4 behind 4000 124 / 87.
+//   16 query and 4 KV heads of 64: tokens 4096 67 / 80, 2048 31 / 29, 512 behind 1069 24 / 21, 64
+//   behind 4096 42 / 45.
+// The host weighs the two kernels, by the most that the batch may be; once they are launched the
+// device compares the rest (1024 tokens: 31 us, with the two weighed again 37; 2048 of 16/4
+// heads of 64 31 and 35).
 constexpr float kImageFixed = 6.f;
 template <int D>
 constexpr float image_gain() { return D == 128 ? 0.9f : 0.4f; }     // of a key tile, a CTA
@@ -840,7 +844,8 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Makes the images: a CTA takes the K or the V of one at a time, a block each of its eight warps.  Also decides which requests have images, and reports bad metadata.
+// Makes the images: a CTA takes the K or the V of one at a time, a block each of its eight
+// warps.  Also decides which requests have images, and reports bad metadata.
 template <int D>
 __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
   constexpr uint32_t kHalf = Layout<D>::kHalf;
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
       v += sums[w][k][2];
     }
     most = fmaxf(most, v * p.hkv / p.sms);  // key tiles of the CTA that has most
-    ahead[k] = image_gain<D>() * most > kImageFixed + image_cost<D>() * n * p.hkv;
+    ahead[k] = image_gain<D>() * most > image_cost<D>() * n * p.hkv;
   }
   for (int r = threadIdx.x; r < R; r += blockDim.x) {
     const int keys = prefix[r + 1];

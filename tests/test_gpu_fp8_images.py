@@ -43,7 +43,8 @@ def test_parity(heads, hkv, d):
                                           ([(4, 600), (500, 700)], True), ([(900, 0)], True), ([(700, 0)], False)])
 def test_which_requests_have_them(reqs, images):
     """Few query tiles: of long requests, unless there are many.  Many: where a CTA has enough (0.9 of
-    its key tiles, 8 for 900 tokens, above 6 + 0.024 for each there is)."""
+    its key tiles, 8 for 900 tokens, above 6 + 0.024 for each there is; without the 6 where
+    other requests have them)."""
     step = Step(len(reqs), reqs, 8, 2, 128)
     out, err = _run(step, images=images)
     assert err == 0
