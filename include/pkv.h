@@ -497,7 +497,7 @@ int64_t pkv_fp8_block_bytes(int32_t block_size, int32_t num_kv_heads, int32_t he
  * become zero.  (Blocks fill from row 0, so a recycled one forgets its old scale.)
  * Of a slot given twice the last of its tokens counts; the result does not depend on the
  * order of the others.  A call whose tokens are not in the order of their blocks costs a
- * search of all slots for each token: num_tokens^2 / 32 steps of a warp. */
+ * search of all slots for each token: num_tokens^2 / 32 steps of a warp.  At most 2^30 tokens. */
 int pkv_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_stride,
                               int64_t value_stride, void* key_cache, void* value_cache,
                               const int64_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
@@ -532,10 +532,11 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
 
 /* pkv_paged_attention_varlen over 8-bit caches: the same definition with K and V the
  * values the caches stand for, sums and softmax in float32.  q and out are bfloat16;
- * num_heads / num_kv_heads may be any integer up to 16; at most 8192 requests.  A
- * block_table row has max_blocks_per_req <= block_table_stride entries.  max_query_len as
- * there (1: every row is a decode row; longer ones are then not computed).  Rows of a
- * request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
+ * num_heads / num_kv_heads may be any integer G up to 16; at most 8192 requests and 2^30
+ * tokens, and unless max_query_len is 1, num_reqs * num_kv_heads * ceil(num_tokens / n) must
+ * be below 2^31, n = floor(128 / G).  A block_table row has max_blocks_per_req <=
+ * block_table_stride entries.  max_query_len as there (1: every row is a decode row; longer
+ * ones are then not computed).  Rows of a request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
  * request, are left as they were; a block id outside the pool reads as zeros
  * (PKV_ERR_BLOCK_ID).  A request with several query tokens has 2^31 - 256 keys at most.
  * Bytes of tokens past a request's end may hold anything; a NaN in a key counts for the rows

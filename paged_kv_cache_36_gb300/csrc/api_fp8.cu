@@ -15,6 +15,7 @@ namespace pkv {
 namespace {
 
 constexpr int kMaxGroup = 16;
+constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of a call: the kernels count on from them in 32 bits
 constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's angles are good to 2^-25 below it
 
 // Whether some of T rows of na bytes, sa apart, share a byte with rows of nb bytes, sb apart.
@@ -76,7 +77,7 @@ int pkv_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_st
                             slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads,
                             head_dim, dtype, error_word, &a.cache);
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  if (num_tokens > 0x7fffffffLL) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^31 - 1 tokens", where);
+  if (num_tokens > kMaxTokens) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^30 tokens", where);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_write_fp8(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "reshape_and_cache_fp8 launch");
@@ -98,7 +99,7 @@ int pkv_rope_reshape_and_cache_fp8(const int64_t* positions, const void* query, 
                             slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads,
                             head_dim, dtype, error_word, &a.cache);
   if (rc != PKV_OK) return rc;
-  if (num_tokens > 0x7fffffffLL) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^31 - 1 tokens", where);
+  if (num_tokens > kMaxTokens) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^30 tokens", where);
   if (num_heads <= 0 || num_heads > (1 << 20) || max_position < 0)
     return fail(PKV_E_INVALID, "%s: bad sizes", where);
   const int64_t es = dtype == PKV_F32 ? 4 : 2;
@@ -177,8 +178,8 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   if (num_heads % num_kv_heads) return fail(PKV_E_INVALID, "%s: num_heads %% num_kv_heads != 0", where);
   if (num_heads / num_kv_heads > kMaxGroup)
     return fail(PKV_E_UNSUPPORTED, "%s: more than %d query heads per KV head", where, kMaxGroup);
-  if (num_reqs > step_metadata_max_reqs() || num_tokens > 0x7fffffffLL)
-    return fail(PKV_E_UNSUPPORTED, "%s: at most %d requests and 2^31 - 1 tokens", where,
+  if (num_reqs > step_metadata_max_reqs() || num_tokens > kMaxTokens)
+    return fail(PKV_E_UNSUPPORTED, "%s: at most %d requests and 2^30 tokens", where,
                 step_metadata_max_reqs());
   if (!workspace) return fail(PKV_E_WORKSPACE, "%s: workspace is required", where);
   const int sms = current_sm_count();
@@ -201,6 +202,11 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
                 max_blocks_per_req, block_table_stride);
   if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kF8RequestCost) > 0x7fffffffLL)
     return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
+  // (offsets that are garbage may give every request the same rows)
+  const int64_t tile = 128 / (num_heads / num_kv_heads);
+  if (max_query_len != 1 && (num_tokens + tile - 1) / tile * num_kv_heads > 0x7fffffffLL / num_reqs)
+    return fail(PKV_E_UNSUPPORTED, "%s: %d requests of %lld tokens may have 2^31 query tiles", where, num_reqs,
+                static_cast<long long>(num_tokens));
   AttnArgs a;
   a.q = q;
   a.q_stride = q_stride;

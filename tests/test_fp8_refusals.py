@@ -43,7 +43,7 @@ def test_cache_write_and_gather(pkv, name, change, code):
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(T=0), 0), (dict(T=-1), -1), (dict(T=1 << 31), -2), (dict(H=0), -1), (dict(rd=0), -2),
+    (dict(T=0), 0), (dict(T=-1), -1), (dict(T=1 << 31), -2), (dict(T=(1 << 30) + 1), -2), (dict(H=0), -1), (dict(rd=0), -2),
     (dict(rd=72), -2), (dict(rd=24), -2), (dict(rd=8, neox=0, dtype=1), 1), (dict(rd=8), -2),
     (dict(rd=8, dtype=0), 1), (dict(maxp=-1), -1), (dict(pos=None), -1), (dict(q=None), -1),
     (dict(qo=None), -1), (dict(table=None), -1), (dict(table=P + 8), -1), (dict(qs=64), -1),
@@ -66,12 +66,14 @@ def test_rope(pkv, change, code):
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(T=0), 0), (dict(R=0), 0), (dict(T=-1), -1), (dict(R=9000), -2), (dict(bs=8), -2),
+    (dict(T=0), 0), (dict(R=0), 0), (dict(T=-1), -1), (dict(T=(1 << 30) + 1), -2), (dict(R=9000), -2), (dict(bs=8), -2),
     (dict(d=80), -2), (dict(H=5), -1), (dict(H=34, hkv=2), -2), (dict(ws=None), -3),
     (dict(wsb=16), -3), (dict(q=None), -1), (dict(bt=None), -1), (dict(q=P + 2), -1),
     (dict(qs=4 * 64 + 4), -1), (dict(qs=64), -1), (dict(width=0), -1), (dict(width=9), -1),
     (dict(mql=-1), -1), (dict(nb=0), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1),
-    (dict(scale=3e38), -1)])
+    (dict(scale=3e38), -1),
+    # 4096 requests that might share 2^19 rows of 8 KV heads: 2^31 tiles of 8 tokens
+    (dict(R=4096, T=1 << 19, H=128, hkv=8, qs=8192), -2)])
 def test_attention(pkv, change, code):
     a = dict(T=3, R=2, nb=4, bs=16, H=4, hkv=2, d=64, q=P, bt=P, ws=P, wsb=1 << 40, qs=256, width=8,
              stride=8, mql=0, scale=0.125)
