@@ -23,15 +23,16 @@
 // quadrant of tensor memory, each with half of the key tile's columns; warps 12-15 bring the
 // query rows in, and without images they convert K and warps 16-19 V.
 //
-// What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 133 us,
-// 1033 TFLOP/s, 54 % of the bf16 rate; of 16384 tokens about 1490 us, 1476 TFLOP/s, 78 %.  At 4096
-// the kernel over images has the tensor core busy 49 % of the time, 48 % of the issue slots taken
-// and 50 MB read: neither the products nor memory bound it, but the chain from S to P.
+// What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 129 us,
+// 1065 TFLOP/s, 56 % of the bf16 rate; of 16384 tokens 1400 us, 1571 TFLOP/s, 83 %.  Neither the
+// products nor memory bound it, but the chain from S to P: without exponentials 16384 tokens
+// take 7 % less, without maxima 10, with an eighth of Q K^T 6, with a quarter of P V 5.
 // Measured and not kept, with what it was measured against (us, a prompt of 4096): two softmax
 // groups with key tiles in turn and an S and an O each 150 (136), with P in halves 142 (136);
 // rows written by the warps that bring Q 130 (129), with two O and two S 137 (129); two S
 // instead of three 137 (129); spinning instead of suspended waits in the issuing warps 147.5
-// (146); copies split in 4 KB 150 (146).
+// (146); copies split in 4 KB 150 (146); weights made before the maxima are exchanged 139
+// (134); a query tile ended after the next one's first scores 130.6 (128.4).
 //
 // Every wait is bounded; a timeout sets PKV_ERR_TIMEOUT and an abort flag that stops all
 // roles.
@@ -64,11 +65,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = kSBufs * kKeys;
 // Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
-// one exceeds 2^kMost.  So O is rescaled once a row's maximum has grown by 2^32 (2^8, as for
-// bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134), sums of flat scores stay
-// finite for any values there are, and weights vanish (at 2^-126) 102 binades below the
-// largest.
-constexpr float kLargest = -24.f, kMost = 8.f;
+// 64 of a row add up to more than kMost.  So O is rescaled once a row's maximum has grown by
+// 2^26 to 2^32 (2^8, as for bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134),
+// sums of flat scores stay finite for any values there are, and weights vanish (at 2^-126) 102
+// binades below the largest.  Only a row's first key tile, and one that moves m, needs the
+// maximum itself (found in every tile: a prompt of 16384 tokens 1475 us instead of 1430).
+constexpr float kLargest = -24.f, kMost = 256.f;
 constexpr int kPrefixMax = 4096;           // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;       // a whole key tile more is still an int
 constexpr size_t kSmemLimit = 232448;
@@ -98,7 +100,7 @@ template <bool kImages>
 struct Shape {
   static constexpr int kThreads = kImages ? 512 : 640;
   static constexpr int kLaunch = kImages ? 128 : 96;
-  static constexpr int kIssue = kImages ? 40 : 32, kSoftmax = kImages ? 184 : 152, kConvert = kImages ? 96 : 72;
+  static constexpr int kIssue = kImages ? 40 : 32, kSoftmax = kImages ? 192 : 152, kConvert = kImages ? 88 : 72;
   static_assert(kIssue + 2 * kSoftmax + (kImages ? 1 : 2) * kConvert <= kThreads / 128 * kLaunch,
                 "the roles' registers fit in what the block is launched with");
   static_assert(kThreads * kLaunch <= 65536, "and those in an SM");
@@ -240,6 +242,18 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 // The power of two of a scale byte as a bfloat16 pair.
 __device__ __forceinline__ uint32_t scale_pair(int e) { return static_cast<uint32_t>(e << 7) * 0x00010001u; }
+
+// The two of a bfloat16 pair to two sums.  (The rounded weights, so that what rounding does to
+// all of a row's cancels: errors of 1.1 of the result's own rounding instead of 1.4.  Adding
+// them as they are instead of as two floats: a prompt of 16384 tokens 1406 us instead of 1430.)
+__device__ __forceinline__ void add_pair(float2& sum, uint32_t w) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "add.rn.f32.bf16 %0, a, %0;\n\t"
+      "add.rn.f32.bf16 %1, b, %1;\n\t}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "r"(w));
+}
 
 // Eight codes times their scale.
 __device__ __forceinline__ uint4 eight_values(uint32_t w0, uint32_t w1, uint32_t scale) {
@@ -704,6 +718,29 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         // causal mask (only tiles reaching past the tile's first row)
         const int key0 = j * kKeys + half * 64;
         if (key0 + 63 > pos_min) mask_scores(s_cols, pos_min + 1 - key0, pos + 1 - key0);
+        // the largest of the row's scores in the key tile
+        auto row_max = [&]() -> float {
+          float mine = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            float sv[32];
+            tmem_ld32(s_cols + c, *reinterpret_cast<uint32_t(*)[32]>(&sv));
+            tmem_wait_ld();
+            float m4[4] = {sv[0], sv[1], sv[2], sv[3]};  // four chains of three-input maxima
+#pragma unroll
+            for (int i = 4; i < 28; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], sv[i + k], sv[i + 4 + k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], sv[28 + k]);
+            mine = fmax3(mine, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+          mine *= f;
+          return fmaxf(mine, exchange(mine));
+        };
+        if (j == 0) m_used = row_max() - kLargest;  // key 0 is visible to every row
+        // P = 2^(s f - m_used) as bf16 pairs over the first 32 of this warp's 64 S columns
+        uint32_t w[32];
         float sv[64];
         {
           uint32_t (&r)[64] = *reinterpret_cast<uint32_t(*)[64]>(&sv);
@@ -711,20 +748,24 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
           tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
           tmem_wait_ld();
         }
-        // row max: four chains of three-input maxima
-        float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+        const float2 f2 = make_float2(f, f), c2 = make_float2(-m_used, -m_used);
+        float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 4; c < 60; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], sv[c + k], sv[c + 4 + k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], sv[60 + k]);
-        const float m_mine = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * f;
-        const float mx = fmaxf(m_mine, exchange(m_mine));  // row max of the key tile
-        if (j == 0) m_used = mx - kLargest;  // key 0 is visible to every row
-        // both warps of the quadrant see the same mx and m_used
-        const bool grow = mx > m_used + kMost;
-        if (__any_sync(0xffffffffu, grow)) {
+        for (int e = 0; e < 32; ++e) {
+          const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), f2, c2);
+          w[e] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
+          add_pair(l2, w[e]);
+        }
+        // Whether the reference has to move the sums tell; both warps of the quadrant see the
+        // same.  (Not in the first key tile: 64 weights of 2^kLargest at most.)
+        const float sum = l2.x + l2.y;
+        const bool grow = j > 0 && fmaxf(sum, exchange(sum)) > kMost;
+        if (!__any_sync(0xffffffffu, grow)) {
+          l += sum;
+          tmem_st32(s_cols, w);
+        } else {
+          // (rare: in short loops, from S once more)
+          const float mx = row_max();
           // O must hold PV of the previous key tile before it is rescaled
           const uint32_t prev = count - 1;
           if (!warp_wait(&bars[kODone0 + prev % kSBufs], (prev / kSBufs) & 1, p.err, abort_flag)) {
@@ -736,22 +777,23 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
           if (grow) m_used = mx - kLargest;
           l *= alpha;
           rescale<D / 2>(o_cols, alpha);
-        }
-        // P = 2^(s f - m_used) as bf16 pairs over the first 32 of this warp's 64 S columns
-        const float2 f2 = make_float2(f, f), c2 = make_float2(-m_used, -m_used);
-        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t w[32];
+          l2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16], y[8];
+            tmem_ld8(s_cols + 16 * c, *reinterpret_cast<uint32_t(*)[8]>(&r[0]));
+            tmem_ld8(s_cols + 16 * c + 8, *reinterpret_cast<uint32_t(*)[8]>(&r[8]));
+            tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), f2, c2);
-          const float2 pe = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-          w[e] = pack_bf16(pe.x, pe.y);
-          // (the rounded ones, so that what rounding does to all of a row's weights cancels: errors of
-          // 1.1 of the result's own rounding instead of 1.4, for 4 % of the time)
-          l2[e & 1] = __fadd2_rn(l2[e & 1], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)));
+            for (int e = 0; e < 8; ++e) {
+              y[e] = pack_bf16(exp2_approx(fmaf(__uint_as_float(r[2 * e]), f, -m_used)),
+                               exp2_approx(fmaf(__uint_as_float(r[2 * e + 1]), f, -m_used)));
+              add_pair(l2, y[e]);
+            }
+            tmem_st8(s_cols + 8 * c, y);
+          }
+          l += l2.x + l2.y;
         }
-        tmem_st32(s_cols, w);
-        l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

@@ -124,3 +124,42 @@ def test_many_requests():
     out, err = _run(step)
     assert err == 0
     check(out, *step.reference())
+
+
+@pytest.mark.parametrize("room", [True, False])
+@pytest.mark.parametrize("heads, hkv, d, more", [(8, 2, 128, 0), (4, 1, 64, 0), (4, 1, 64, 1000)])
+def test_scores_that_rise(heads, hkv, d, more, room):
+    """Scores of a key tile together 16 to 336 above the one before, or below it, in all rows,
+    in some of a tile's and in a tile's half: the weights' reference moves, from weights that
+    float32 holds and from others."""
+    import paged_kv_cache_36_gb300 as pkv
+    step = Step(heads + d, [(520, 800 + more), (300, 900 + more)], heads, hkv, d)
+    step.scale = 1.0
+    step.q.fill_(1.0)
+    step.q[::3] = 0.5            # (rows that rise by half as much)
+    step.q[5::7] = -1.0          # (and that fall)
+    codes = {0: 0x00, 16: None, 40: None, 24: None, 240: None, 576: None}
+    value = lambda c: next(x for x in range(0x7F) if (x & 7 | (8 if x >> 3 else 0)) * 2.0 ** (max(x >> 3, 1) - 10) == c / d)  # noqa: E731
+    for c in codes:
+        codes[c] = value(c)
+    rises = [0, 16, 40, 24, 24, 240, 40, 240, 576, 576, 240]
+    for r in range(2):
+        n = step.seq[r]
+        for h in range(hkv):
+            for b in range(-(-n // 16)):
+                step.set_scale(step.k, r, b, h, 127)
+            for pos in range(n):
+                c = rises[min(pos // 128, len(rises) - 1)]
+                if pos % 128 >= 64 and pos // 128 == 3:
+                    c = 40               # one half of a tile alone
+                step.set(step.k, True, r, pos, h, np.arange(d), codes[c])
+            step.set(step.k, True, r, np.arange(n), h, 7, step.rng.integers(0, 0x39, n).astype(np.uint8))
+    ws = None
+    if not room:
+        ws = torch.zeros_like(pkv.new_workspace_fp8(heads, hkv, d))
+        tile = _tile_bytes(hkv, d)
+        ws = ws[:ws.numel() - (256 << 20) // tile * tile]
+    # (11 key tiles of head_dim 64 are not worth the kernels)
+    out, err = _run(step, ws, images=d == 128 or more > 0)
+    assert err == 0
+    check(out, *step.reference())
