@@ -17,10 +17,11 @@
 // counts.  A batch in the order of its requests has one search per 16 tokens; in the worst
 // order there is one per token, T^2 / 32 steps of a warp.
 //
-// What bounds it.  8192 tokens, 8 KV heads of 128, bfloat16, nothing in L2: 19.9 us for 50 MB,
-// of them about 3 for the search; issue slots and warps 41 % busy, so latency: a warp's rows, their maximum, the codes and the stores follow one
-// another.  With RoPE of 32 query heads 35.5 us for 184 MB, 5.2 TB/s.  64 tokens 5.5 us, with
-// RoPE 5.6.
+// What bounds it.  8192 tokens that begin inside blocks, 8 KV heads of 128, bfloat16, nothing in
+// L2: 17.4 us for 50 MB.  By its clocks (whole blocks, CTAs of 256 threads) a CTA has its leaders
+// 2 us after its start, the other tokens 1.4 later, and a warp takes 2 to 2.7 us for each of its
+// two items: latency of rows that follow from slots, of their maximum and of the stores.  With
+// RoPE of 32 query heads 35.4 us for 184 MB, 5.2 TB/s.  64 tokens 5.5 us with RoPE or without.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -33,14 +34,19 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;  // of a write's CTA, or a gather's
+constexpr int kThreads = 256;  // of a gather's CTA
 constexpr int kWindow = 16;  // tokens of a gather's window, at most
-// Of a write's.  8192 tokens in order, 8 heads of 128: 19.9 us with 8, 20.7 with 4, 23.0 with
-// 16 (half of the windows of 8 have no block to begin, and end at once; those of 16 leave
+// Of a write's.  8192 tokens in order, 8 heads of 128 (and CTAs of 256 threads): 19.9 us with 8,
+// 20.7 with 4, 23.0 with 16 (half of the windows of 8 have no block to begin, and end at once; those of 16 leave
 // some CTAs with twice the others' work).
 constexpr int kWriteWindow = 8;
 
 enum Rope { kNone, kHalf, kInterleaved };
+// Threads of a write's CTA.  A window in which one block ends and another begins has twice the
+// work.  8192 tokens, 8 heads of 128, that begin inside blocks: 17.4 us, with 256 threads
+// 18.4; of whole blocks 16.5 and 15.6; with RoPE 39.0 and 35.4.
+template <Rope kRope>
+constexpr int write_threads() { return kRope == kNone ? 512 : 256; }
 
 // N consecutive elements of a row.
 template <typename T, int N>
@@ -202,16 +208,11 @@ __device__ __forceinline__ void rotated(const T* row, int d, const float* cs, in
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// The scale of a chunk that gets rows of magnitude `amax`; *grown: by how much the rows
-// that stay have to come down (0 where there are none).  One warp.
-__device__ __forceinline__ int new_scale(const uint8_t* head, bool anew, uint32_t amax, int* grown) {
+// The scale of a chunk with scale `e_old` (0 if it begins anew) that gets rows of magnitude
+// `amax`; *grown: by how much the rows that stay have to come down.
+__device__ __forceinline__ int new_scale(int e_old, uint32_t amax, int* grown) {
   const int e_new = f8_scale_of(amax);
-  if (anew) {
-    *grown = 0;
-    return e_new;
-  }
-  const int e_old = f8_scale(*head);
-  *grown = max(e_new - e_old, 0);
+  *grown = e_old == 0 ? 0 : max(e_new - e_old, 0);
   return max(e_new, e_old);
 }
 
@@ -241,6 +242,7 @@ __device__ __forceinline__ void write_keys(const WriteParams& p, int64_t blk, in
   const T* key = static_cast<const T*>(p.key) + static_cast<int64_t>(h) * D;
   const int tok[2] = {rows[lane >> 2], rows[(lane >> 2) + 8]};
   const bool anew = rows[0] >= 0;
+  const int e_old = anew ? 0 : f8_scale(chunk[f8_code_bytes(D)]);
   uint32_t amax = 0u;
   // without RoPE the rows stay in registers; with it they are rotated twice, for the scale
   // and for the codes (64 more registers would halve the warps of an SM)
@@ -291,7 +293,7 @@ __device__ __forceinline__ void write_keys(const WriteParams& p, int64_t blk, in
     }
   }
   int grown;
-  const int e = new_scale(chunk + f8_code_bytes(D), anew, amax, &grown);
+  const int e = new_scale(e_old, amax, &grown);
   const float inv = f8_pow2(127 - e);
   const float down = f8_pow2(max(-grown, -126));
 #pragma unroll
@@ -339,6 +341,7 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
   uint8_t* chunk = p.value_cache + (blk * p.hkv + h) * f8_chunk_bytes(D);
   const T* value = static_cast<const T*>(p.value) + static_cast<int64_t>(h) * D + (lane >> 2) * P;
   const bool anew = rows[0] >= 0;
+  const int e_old = anew ? 0 : f8_scale(chunk[f8_code_bytes(D)]);
   Piece<T, P> raw[4];
   uint32_t keep = 0u;  // bytes of a word that stay
 #pragma unroll
@@ -353,7 +356,7 @@ __device__ __forceinline__ void write_values(const WriteParams& p, int64_t blk, 
   }
   const uint32_t amax = most_of<T>(raw);
   int grown;
-  const int e = new_scale(chunk + f8_code_bytes(D), anew, amax, &grown);
+  const int e = new_scale(e_old, amax, &grown);
   const float inv = f8_pow2(127 - e);
   const float down = f8_pow2(max(-grown, -126));
   if (anew || grown || keep != 0xffffffffu) {
@@ -455,7 +458,9 @@ __device__ __forceinline__ void rotate_queries(const WriteParams& p, int64_t fir
 }
 
 template <typename T, int D, Rope kRope>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) reshape_and_cache_fp8_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(write_threads<kRope>(), (sizeof(T) == 2 ? 1024 : 512) / write_threads<kRope>())
+    reshape_and_cache_fp8_kernel(const WriteParams p) {
+  constexpr int kThreads = write_threads<kRope>();
   // a programmatic dependent of the kernel before it, which may still read the cache or
   // write the new rows
   grid_dependency_wait();
@@ -519,6 +524,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) reshape_and_
   __syncthreads();
   const int leads = found;
   if (leads == 0) return;
+  // so are the scales and codes of blocks that have rows already
+  // (8192 tokens 19.3 us without, 18.4 with; of 64 tokens with RoPE 5.5 and 6.2)
+  for (int k = 0; k < leads && p.window > 1; ++k) {
+    if (__ldg(p.slot_mapping + first_of[k]) % kF8Block == 0) continue;
+    constexpr int kLines = f8_chunk_bytes(D) / 128 + 1;
+    const int64_t blk = static_cast<int64_t>(block_of[k]) * p.hkv * f8_chunk_bytes(D);
+    for (int i = threadIdx.x; i < 2 * p.hkv * kLines; i += kThreads) {
+      const int item = i / kLines, at = (item >> 1) * f8_chunk_bytes(D) + min((i - item * kLines) * 128, f8_code_bytes(D));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(((item & 1) ? p.value_cache : p.key_cache) + blk + at));
+    }
+  }
   // ---- the other tokens of those blocks, two blocks at a time (in the order of the requests
   // a window has hardly more) ----
   for (int k = 0; k < leads; k += 2) {
@@ -771,6 +787,7 @@ __global__ void __launch_bounds__(kThreads) gather_cache_fp8_kernel(const Gather
 
 template <typename T, int D, Rope kRope>
 cudaError_t write_t(const F8WriteArgs& a, cudaStream_t stream) {
+  constexpr int kThreads = write_threads<kRope>();
   WriteParams p;
   p.key = a.cache.key;
   p.value = a.cache.value;
