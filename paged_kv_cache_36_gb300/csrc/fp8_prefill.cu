@@ -77,22 +77,23 @@ constexpr size_t kSmemLimit = 232448;
 constexpr int kNone = 0x7fffffff;          // no NaN
 // Which requests have images, by what both ways cost (see expand_fp8_kernel).  In a graph a
 // CTA takes some 2.0 us for a key tile of head_dim 128 that it converts and 1.1 over images, of
-// 64 1.0 and 0.6; images cost two kernels, 6 us, and for each key tile and KV head what they
+// 64 1.0 and 0.6; images cost two kernels, 6 to 7 us, and for each key tile and KV head what they
 // write and read again.  us over images / converted as they go, without those kernels, 32 query
 // and 8 KV heads of 128:
-//   tokens 4096 134 / 264, 2048 57 / 81, 1024 31.3 / 31.0, 512 behind 1223 30 / 33, behind 11539
-//   82 / 148, 128 behind 3874 35 / 42, 64 behind 2048 32 / 35, 4 behind 8000 69 / 104, 4 behind
-//   1000 25 / 23; 8 requests of 256 behind 1000 67 / 80; 16 of 4 behind 4000 124 / 87.
-//   16 query and 4 KV heads of 64: tokens 4096 67 / 80, 2048 31 / 29, 512 behind 1069 24 / 21, 64
-//   behind 4096 42 / 45.
+//   tokens 4096 130 / 256, 2048 56 / 79, 1024 30.8 / 31.1, 512 behind 1223 30 / 32, behind 11539
+//   80 / 145, 128 behind 3874 34 / 43, 64 behind 2048 31 / 35, 4 behind 8000 65 / 108, 4 behind
+//   1000 25 / 23; 8 requests of 256 behind 1000 66 / 80, of 256 40 / 42; 16 of 4 behind 4000 125 /
+//   87, 64 of 4 behind 2000 227 / 160 (so 0.014 a key tile and KV head).
+//   16 query and 4 KV heads of 64: tokens 4096 61 / 81, 2048 30 / 29, 512 behind 1069 24 / 21, 64
+//   behind 4096 38 / 45.
 // The host weighs the two kernels, by the most that the batch may be; once they are launched the
 // device compares the rest (1024 tokens: 31 us, with the two weighed again 37; 2048 of 16/4
 // heads of 64 31 and 35).
-constexpr float kImageFixed = 6.f;
+constexpr float kImageFixed = 6.5f;
 template <int D>
 constexpr float image_gain() { return D == 128 ? 0.9f : 0.4f; }     // of a key tile, a CTA
 template <int D>
-constexpr float image_cost() { return D == 128 ? 0.024f : 0.012f; }  // of a key tile and KV head
+constexpr float image_cost() { return D == 128 ? 0.014f : 0.012f; }  // of a key tile and KV head
 constexpr int kManyTiles = 4;  // query tiles from which on reading images often pays for writing them
 
 // Threads, and registers a thread by role (setmaxnreg), over images and without.
