@@ -25,8 +25,9 @@
 //
 // What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 129 us,
 // 1065 TFLOP/s, 56 % of the bf16 rate; of 16384 tokens 1400 us, 1571 TFLOP/s, 83 %.  Neither the
-// products nor memory bound it, but the chain from S to P: without exponentials 16384 tokens
-// take 7 % less, without maxima 10, with an eighth of Q K^T 6, with a quarter of P V 5.
+// products nor memory bound it, but the chain from S to P: when 16384 tokens took 1489 us they
+// took 7 % less without exponentials, 9 without maxima, 6 with an eighth of Q K^T, 5 with a
+// quarter of P V.
 // Measured and not kept, with what it was measured against (us, a prompt of 4096): two softmax
 // groups with key tiles in turn and an S and an O each 150 (136), with P in halves 142 (136);
 // rows written by the warps that bring Q 130 (129), with two O and two S 137 (129); two S
