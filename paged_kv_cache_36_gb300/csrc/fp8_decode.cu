@@ -23,7 +23,8 @@
 // bfloat16.
 //   - K's scale multiplies the scores in float32.  The queries of a head are brought to
 //     [1, 2) by a power of two first, so that sums over codes are below 2^17 whatever q and
-//     the scale are; nothing of an element is lost above 2^-126 of the head's largest.
+//     the scale are; nothing of an element is lost above 2^-126 of the head's largest.  The
+//     exponents of q, of K's scale and of the softmax's are added up before they multiply.
 //   - V's scale multiplies its codes, exactly, so weights and values go into the product as
 //     they are: weights are bfloat16 (8 bits) over 102 binades below the largest, values have no
 //     other limit than that float32 sums hold.
@@ -43,6 +44,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "fp8.cuh"
@@ -86,7 +88,8 @@ struct Params {
   int32_t num_blocks;
   int32_t hkv;
   int32_t group;
-  float scale_log2;
+  float scale_m;       // scale log2(e) = scale_m 2^scale_e, scale_m zero or of magnitude [1, 2]
+  int32_t scale_e;
   uint32_t* err;
   int2* plan;        // [num_reqs]: what there is to join (see slot_of)
   float2* part_ml;   // [2 * ranges][hkv][group]
@@ -347,7 +350,8 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     // B fragments of Q^T: k-step 4 a + i of lane tid holds dims 64 a + 16 tid + 4 i .. + 3, the
     // order of the K codes
     uint32_t qb[NT][KS][2];
-    float qs[NT][2];  // what undoes the powers of two, times scale log2(e), of heads 2 tid, + 1
+    int qe[NT][2];  // of heads 2 tid, + 1: the exponent that undoes the power of two, and the scale's
+    bool far = false;  // whether with some scale of K 2^qe may be no normal float32
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int head = nt * 8 + gid;
@@ -375,10 +379,11 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) qb[nt][k][i] = mul_bf16x2(qb[nt][k][i], up * 0x00010001u);
-      // (a product of the two may be outside float32's range where the scores are not: see `factor`)
-      qs[nt][0] = __int_as_float(__shfl_sync(0xffffffffu, ex - 127, 8 * tid));
-      qs[nt][1] = __int_as_float(__shfl_sync(0xffffffffu, ex - 127, 8 * tid + 4));
+      qe[nt][0] = __shfl_sync(0xffffffffu, ex - 127, 8 * tid) + p.scale_e;
+      qe[nt][1] = __shfl_sync(0xffffffffu, ex - 127, 8 * tid + 4) + p.scale_e;
+      far |= max(qe[nt][0], qe[nt][1]) > 253 - kF8MaxScale || min(qe[nt][0], qe[nt][1]) < 1 - kF8MinScale;
     }
+    far = __any_sync(0xffffffffu, far);
 
     float o[KS][NT][4];
     float m[NT][2], l[NT][2];
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
       for (int j = 0; j < NV; ++j) kw[j] = *reinterpret_cast<const uint4*>(st + j * 512 + lane * 16);
 #pragma unroll
       for (int j = 0; j < NV; ++j) vw[j] = *reinterpret_cast<const uint4*>(st + kChunk + j * 512 + lane * 16);
-      const int ke = f8_scale(st[f8_code_bytes(D)]) - 127;
+      const int ke = f8_scale(st[f8_code_bytes(D)]);
       const int ve = f8_scale(st[kChunk + f8_code_bytes(D)]);
       if (zeros) {
 #pragma unroll
@@ -449,11 +454,21 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][c] += s2[nt][c];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          // within float32, and not zero, for the masked scores' infinities
-          const int e = min(max(__float_as_int(qs[nt][cc]) + ke, -126), 110);
-          f[nt][cc] = f8_pow2(e) * p.scale_log2;
-        }
+        for (int cc = 0; cc < 2; ++cc) f[nt][cc] = __uint_as_float(static_cast<uint32_t>(qe[nt][cc] + ke) << 23) * p.scale_m;
+      }
+      if (far) {
+        // of q, K and the scale maybe only the product is within float32: the sums take what one
+        // power of two does not hold, so what they become lies between them and the scores
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int e = qe[nt][cc] + ke - 127, last = min(max(e, -126), 126);
+            const int first = min(max(e - last, -126), 126), then = min(max(e - last - first, -126), 126);
+            f[nt][cc] = f8_pow2(last) * p.scale_m;
+            s[nt][cc] = s[nt][cc] * f8_pow2(first) * f8_pow2(then);
+            s[nt][2 + cc] = s[nt][2 + cc] * f8_pow2(first) * f8_pow2(then);
+          }
       }
       if (tokens < kF8Block) {
 #pragma unroll
@@ -779,7 +794,9 @@ cudaError_t launch_decode_fp8(const AttnArgs& a, const MxDecodeScratch& ws, int 
   p.num_blocks = static_cast<int32_t>(a.num_blocks);
   p.hkv = a.num_kv_heads;
   p.group = a.num_heads / a.num_kv_heads;
-  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  int e;
+  p.scale_m = static_cast<float>(2.0 * std::frexp(static_cast<double>(a.scale) * 1.4426950408889634, &e));
+  p.scale_e = e - 1;
   p.err = a.err;
   p.plan = reinterpret_cast<int2*>(ws.plan);
   p.part_ml = reinterpret_cast<float2*>(ws.part_ml);

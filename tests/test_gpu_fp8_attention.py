@@ -73,6 +73,24 @@ def test_scales_far_apart(lo, hi, which):
     check(_run(step), *step.reference())
 
 
+@pytest.mark.parametrize("q_exp, lo, hi, scale_exp, prefill", [
+    (120, -9, -5, -124, False),    # query times K's scale past 2^111, where the scores are ordinary
+    (50, 80, 84, -143, False), (10, 115, 119, -138, False), (100, -20, -9, -100, True),
+    (-120, -9, -5, 116, True),     # below 2^-126
+    (-60, -80, -74, 125, False), (-100, -30, -24, 115, True)])
+def test_exponents_that_cancel(q_exp, lo, hi, scale_exp, prefill):
+    """Queries, K's scales and the softmax's scale far from 1, their product not: scores of a few
+    units in single rows, and in those of several tokens too where <q, k> itself is a float32."""
+    step = Step(300 + q_exp, [(1, 400), (1, 33)] + [(20, 100)] * prefill, 8, 2, 64)
+    k = step.k.reshape(len(step.k), 2, -1)
+    k[:, :, 16 * 64] = step.rng.integers(127 + lo, 128 + hi, k.shape[:2])
+    step.q *= 2.0 ** q_exp
+    step.scale = 2.0 ** scale_exp
+    ref, tol = step.reference()
+    assert step.q.isfinite().all() and (tol <= 2.0 ** -5 * ref.abs().max()).all()
+    check(_run(step), ref, tol)
+
+
 def test_unlikely_keys_with_large_values():
     """A key e^-60 as likely as the others holds the only values that are not zero."""
     step = Step(3, [(1, 299), (40, 260)], 4, 2, 128)
