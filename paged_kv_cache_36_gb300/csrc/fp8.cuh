@@ -30,6 +30,7 @@ namespace pkv {
 constexpr int kF8Block = 16;                 // tokens per cache block
 constexpr int kF8MinScale = 10;              // 2^-9 2^(10 - 127) is bfloat16's smallest normal number
 constexpr int kF8MaxScale = 246;             // 448 2^(246 - 127) = 1.75 2^127 is finite
+constexpr int kF8Loud = 207;                 // up to here 2^31 values (below 2^89) times 2^8 add up to less than 2^128
 
 __host__ __device__ constexpr int f8_code_bytes(int d) { return kF8Block * d; }
 __host__ __device__ constexpr int f8_chunk_bytes(int d) { return kF8Block * d + 16; }

@@ -33,8 +33,8 @@
 //     the unrounded sums 0.0022; weights of two bfloat16 reach 0.0016, but took 337 us for 8
 //     requests of 131072 tokens where these took 326).
 //   - The reference m of the weights lies 2^24 above a score that was the largest and moves when
-//     one exceeds that by 2^32: the common block needs a vote, and no shuffle, and the sums of
-//     flat scores stay finite for any values there are.
+//     one exceeds that by 2^32 (by 2 where the block's values are large, kF8Loud): the common
+//     block needs a vote, and no shuffle, and sums stay finite for any values there are.
 //
 // What bounds it.  8 requests of 131072 tokens with 64 query and 8 KV heads of 128 take 326 to 330
 // us, 6.6 TB/s, 97 to 98 % of the copy rate.  64 requests of 128 to 4096 tokens (32/8 heads of
@@ -57,8 +57,9 @@ namespace {
 
 constexpr int kMinUnits = 3;     // units in a range, nearly: at least 2, more than kF8RequestCost
 // Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
-// one exceeds 2^kMost.
-constexpr float kLargest = -24.f, kMost = 8.f;
+// one exceeds 2^kMost, or in a block of large values 2^kMostLoud: sums over 2^22 keys of those
+// stay finite, over the others' always.
+constexpr float kLargest = -24.f, kMost = 8.f, kMostLoud = -23.f;
 constexpr int kMaxStages = 6;
 constexpr int kWarpPlan = 128;   // requests up to which a warp makes the plan for itself
 
@@ -424,8 +425,9 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) vw[j] = *reinterpret_cast<const uint4*>(st + kChunk + j * 512 + lane * 16);
       const int ke = f8_scale(st[f8_code_bytes(D)]);
-      const int ve = f8_scale(st[kChunk + f8_code_bytes(D)]);
+      int ve = f8_scale(st[kChunk + f8_code_bytes(D)]);
       if (zeros) {
+        ve = 127;
 #pragma unroll
         for (int j = 0; j < NV; ++j) kw[j] = vw[j] = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 
       // ---- online softmax per head column ----
       float mx[NT][2];
+      const float most = ve > kF8Loud ? kMostLoud : kMost;
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           mx[nt][cc] = fmaxf(s[nt][cc], s[nt][2 + cc]);
-          grow |= mx[nt][cc] > m[nt][cc] + kMost;
+          grow |= mx[nt][cc] > m[nt][cc] + most;
         }
       }
       if (__any_sync(0xffffffffu, grow)) {

@@ -126,6 +126,38 @@ def test_the_largest_values():
     check(_run(step), ref, tol)
 
 
+def rising_over_the_largest_values(reqs, heads, hkv, d, mixed, seed=0):
+    """Scores that rise by 16 to 24 (2^23 to 2^35) every so many keys of a request, in halves of
+    blocks too, and fall again; values 1.75 2^127 (of odd KV heads the negative), or where mixed
+    some blocks of them between ordinary ones."""
+    step = Step(seed + heads + d, reqs, heads, hkv, d)
+    step.scale = 1.0
+    step.q.fill_(1.0)
+    scores = {0: 0x00, 16: 0x58, 18: 0x59, 36: 0x61, 40: 0x62, 56: 0x66, 72: 0x69, 80: 0x6A}
+    rises = [0, 18, 18, 36, 56, 72, 40, 80, 16, 0]
+    for r, n in enumerate(step.seq):
+        each = max(n // 9, 8)
+        for h in range(hkv):
+            step.set(step.k, True, r, np.arange(n)[:, None], h, np.arange(d), 0)
+            for i in range(0, n, each):
+                step.set(step.k, True, r, np.arange(i, min(n, i + each)), h, 5, scores[rises[i // each % 10]])
+            for b in range(-(-n // 16)):
+                step.set_scale(step.k, r, b, h, 127)
+                if not mixed or b % 3 == 1:
+                    at = np.arange(16 * b, min(n, 16 * b + 16))
+                    step.set(step.v, False, r, at[:, None], h, np.arange(d), 0xFE if h % 2 else 0x7E)
+                    step.set_scale(step.v, r, b, h, 246)
+    return step
+
+
+@pytest.mark.parametrize("heads, hkv, d, mixed", [(4, 2, 64, False), (8, 2, 128, True), (16, 1, 64, True)])
+def test_decode_of_scores_that_rise_over_the_largest_values(heads, hkv, d, mixed):
+    step = rising_over_the_largest_values([(1, 3000), (1, 100), (1, 39), (1, 700)], heads, hkv, d, mixed)
+    ref, tol = step.reference()
+    assert 1e38 < ref.abs().max() < 3e38
+    check(_run(step, max_query_len=1), ref, tol)
+
+
 def test_nan_counts_for_the_rows_that_see_it():
     """NaN in a key or a value at a position makes what sees it NaN: of a value one dimension
     of the rows behind, of a key all of them."""
