@@ -546,6 +546,7 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * a decode row's query nothing is kept that is 2^126 times below the head's largest element).
  * Weights are rounded to 8 bits, numerator and denominator alike, and vanish 2^-102 below the
  * row's largest; scores (scale <q, k>) and their sums are float32.  scale must be finite.
+ * Sums of values are finite whatever the values and the scores, for up to 2^22 keys.
  *
  * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch, its first
  * 256 bytes zero before its first use, word 0 the error word; two calls that overlap on the

@@ -14,6 +14,11 @@
 //   - For the others eight warps convert as they go: a warp takes whole blocks, whose codes
 //     it reads as D / 32 coalesced vectors, and writes rows to the stage.
 //
+// Large values.  The reference of a row's weights moves at once in key tiles that hold some
+// (kF8Loud), so that sums stay finite; without images a warp notes which.  Over images it
+// does in all key tiles if one of the call's holds some (a word read for each: a prompt of 16384
+// tokens 1434 us where without it took 1407).
+//
 // NaN.  Zero times NaN would poison rows that do not see a NaN in V, so one is stored as
 // zero and its position noted by dimension; a row at or behind it gets NaN there.  (In a tile
 // that every row sees it is left in V.)
@@ -21,7 +26,7 @@
 // Warp roles: warp 0 owns the tensor memory and issues Q K^T, warp 1 issues P V; over images
 // warps 2 and 3 copy K and V; warps 4-11 run the softmax and the epilogue, two per 32-lane
 // quadrant of tensor memory, each with half of the key tile's columns; warps 12-15 bring the
-// query rows in, and without images they convert K and warps 16-19 V.
+// query rows in, and without images they convert K, warps 16-19 V, and warp 2 notes large values.
 //
 // What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 129 us,
 // 1065 TFLOP/s, 56 % of the bf16 rate; of 16384 tokens 1400 us, 1571 TFLOP/s, 83 %.  Neither the
@@ -62,16 +67,20 @@ constexpr int kSBufs = 3;
 // Query tiles whose NaN positions are in shared memory (no images).  V of query tile n + 4 is
 // converted after P V of n + 2, and so after the epilogue of n + 1.
 constexpr int kNanBufs = 4;
+// Key tiles of which shared memory says whether they hold large values (no images).  It does of
+// tile n after the Q K^T of n - 3, and so after the P V of n - 6.
+constexpr int kLoudBufs = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = kSBufs * kKeys;
 // Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
-// 64 of a row add up to more than kMost.  So O is rescaled once a row's maximum has grown by
+// 64 of a row add up to more than kMost, or in a key tile of large values (kF8Loud) kMostLoud:
+// sums over 2^22 keys of those stay finite, over the others' always.  So O is rescaled once a row's maximum has grown by
 // 2^26 to 2^32 (2^8, as for bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134),
 // sums of flat scores stay finite for any values there are, and weights vanish (at 2^-126) 102
 // binades below the largest.  Only a row's first key tile, and one that moves m, needs the
 // maximum itself (found in every tile: a prompt of 16384 tokens 1475 us instead of 1430).
-constexpr float kLargest = -24.f, kMost = 256.f;
+constexpr float kLargest = -24.f, kMost = 256.f, kMostLoud = 1.f / 131072;  // (64 equal ones 2^-18)
 constexpr int kPrefixMax = 4096;           // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;       // a whole key tile more is still an int
 constexpr size_t kSmemLimit = 232448;
@@ -128,7 +137,8 @@ struct Layout {
   static constexpr uint32_t kBars = kV + kVStages * kHalf;
   static constexpr uint32_t kXch = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [2 parity][2 half][128 rows] floats
   static constexpr uint32_t kNan = kXch + 2 * 2 * 128 * 4;                 // [kNanBufs][D] positions, [kNanBufs] any
-  static constexpr uint32_t kMisc = kNan + kNanBufs * (D + 1) * 4;         // tensor memory slot, abort flag
+  static constexpr uint32_t kLoud = kNan + kNanBufs * (D + 1) * 4;         // [kLoudBufs]
+  static constexpr uint32_t kMisc = kLoud + kLoudBufs * 4;                 // tensor memory slot, abort flag
   static constexpr uint32_t kPrefix = kMisc + 16;
   static_assert(kBars % 8 == 0 && kMisc % 4 == 0, "barriers, and words");
 };
@@ -161,11 +171,12 @@ struct Params {
   // Key tiles converted ahead (null: none): request r's are images image_base[r] hkv on, its
   // key tiles in order, KV head fastest; -1: none, its rows are converted as they are needed.
   // any[0]: whether there are such; any[1]: whether there are images.  image_nan: by image,
-  // whether V has a NaN; nan_seen: whether one of this call's has (zero between calls).
+  // whether V has a NaN; flags_seen: whether one of this call's has (1), and whether one has
+  // large values (2) (zero between calls).
   uint8_t* images;
   int32_t* image_base;
   int32_t* image_nan;
-  uint32_t* nan_seen;
+  uint32_t* flags_seen;
   int32_t* any;
   int32_t image_tiles;  // key tiles (of all KV heads) there is room for
   int32_t sms;
@@ -511,6 +522,45 @@ __device__ __forceinline__ void convert_role(const Params& p, uint8_t* smem, con
   }
 }
 
+// Notes which key tiles hold large values (a warp; no images), with the stages of K.
+template <int D>
+__device__ __forceinline__ void loud_role(const Params& p, uint8_t* smem, const int32_t* prefix, int entries,
+                                          int total, int tpt) {
+  using L = Layout<D>;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  volatile uint32_t* loud = reinterpret_cast<volatile uint32_t*>(smem + L::kLoud);
+  const int lane = threadIdx.x & 31, cid = blockIdx.x, ncta = gridDim.x;
+  const uint64_t block_bytes = static_cast<uint64_t>(p.hkv) * f8_chunk_bytes(D);
+  uint32_t count = 0;
+  bool ok = true;
+  for (int it = 0, ct = cta_tile(0, cid, ncta, total); ct >= 0 && ok; ct = cta_tile(++it, cid, ncta, total)) {
+    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+    const Tile t = find_tile<false>(ct, prefix, entries, p, tpt);
+    const int nblk = (t.nkeys - 1) / kF8Block + 1;
+    const int32_t* ids = p.block_table + static_cast<int64_t>(t.r) * p.bt_stride;
+    const uint8_t* scale = p.value_cache + static_cast<uint64_t>(t.h) * f8_chunk_bytes(D) + f8_code_bytes(D);
+    auto load = [&](int j) -> uint32_t {  // a block a lane
+      const int b = j * kTileBlocks + lane;
+      if (lane >= kTileBlocks || b >= nblk) return 0u;
+      const uint32_t id = static_cast<uint32_t>(__ldg(ids + b));
+      return id < static_cast<uint32_t>(p.num_blocks) ? __ldg(scale + id * block_bytes) : 0u;
+    };
+    uint32_t next = 0u;  // (of a row's first key tile nothing asks)
+    for (int j = 0; j < t.nkt; ++j, ++count) {
+      const int st = count % kKStages;
+      ok = count < kKStages || held_warp_wait(&bars[kKEmpty0 + st], (count / kKStages - 1) & 1, p.err, abort_flag);
+      if (!ok) break;
+      const bool any = __any_sync(0xffffffffu, next > kF8Loud);
+      if (lane == 0) {
+        loud[count % kLoudBufs] = any ? 1u : 0u;
+        mbar_arrive(&bars[kKFull0 + st]);
+      }
+      if (j + 1 < t.nkt) next = load(j + 1);
+    }
+  }
+}
+
 template <int D, bool kImages>
 __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kernel(const Params p) {
   using L = Layout<D>;
@@ -530,7 +580,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   // (the kernel over images is through)
-  if (!kImages && p.images != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.nan_seen = 0u;
+  if (!kImages && p.images != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.flags_seen = 0u;
   if (kImages ? __ldcg(p.any + 1) == 0 : p.images != nullptr && __ldcg(p.any) == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.num_reqs;
@@ -547,8 +597,9 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
     for (int b = 0; b < kNumBars; ++b) {
       uint32_t n = 1;
       if (b == kQFull) n = 4;  // the warps that bring Q
-      if (!kImages && ((b >= kKFull0 && b < kKFull0 + kKStages) || (b >= kVFull0 && b < kVFull0 + kVStages)))
-        n = 4;  // the warps that convert
+      // the warps that convert, and with K the one that notes large values
+      if (!kImages && b >= kKFull0 && b < kKFull0 + kKStages) n = 5;
+      if (!kImages && b >= kVFull0 && b < kVFull0 + kVStages) n = 4;
       if ((b >= kPFull0 && b < kPFull0 + kSBufs) || b == kNanRead) n = 8;  // softmax warps
       if (b >= kPair0 && b < kPair0 + 4) n = 2;         // the two warps sharing a quadrant
       mbar_init(&bars[b], n);
@@ -660,6 +711,8 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         if (warp == 2) copy_role<D, false>(p, smem, prefix, entries, total, tpt);
         else copy_role<D, true>(p, smem, prefix, entries, total, tpt);
       }
+    } else if (warp == 2) {
+      loud_role<D>(p, smem, prefix, entries, total, tpt);
     }
   } else if (warp >= 12) {
     set_registers<S::kConvert, false>();
@@ -689,7 +742,10 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
     uint64_t* pair_bar = &bars[kPair0 + quad];
     // never zero, for the masked scores' infinities; the scale's sign is on Q
     const float f = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-    const bool nan_seen = kImages && __ldcg(p.nan_seen) != 0u;
+    const uint32_t flags_seen = kImages ? __ldcg(p.flags_seen) : 0u;
+    const bool nan_seen = (flags_seen & 1u) != 0u;
+    const volatile uint32_t* loud = reinterpret_cast<volatile uint32_t*>(smem + L::kLoud);
+    float most = (flags_seen & 2u) ? kMostLoud : kMost;
     uint32_t count = 0, pair_uses = 0, tiles_done = 0, nan_tiles = 0;
     auto exchange = [&](float mine) -> float {
       float* slot = xch + (pair_uses & 1) * 256;
@@ -717,6 +773,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         }
         tc_fence_after();
         const uint32_t s_cols = lane_addr + kColS + b * kKeys + half * 64;
+        if (!kImages) most = loud[count % kLoudBufs] != 0u ? kMostLoud : kMost;
         // causal mask (only tiles reaching past the tile's first row)
         const int key0 = j * kKeys + half * 64;
         if (key0 + 63 > pos_min) mask_scores(s_cols, pos_min + 1 - key0, pos + 1 - key0);
@@ -761,7 +818,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
         // Whether the reference has to move the sums tell; both warps of the quadrant see the
         // same.  (Not in the first key tile: 64 weights of 2^kLargest at most.)
         const float sum = l2.x + l2.y;
-        const bool grow = j > 0 && fmaxf(sum, exchange(sum)) > kMost;
+        const bool grow = j > 0 && fmaxf(sum, exchange(sum)) > most;
         if (!__any_sync(0xffffffffu, grow)) {
           l += sum;
           tmem_st32(s_cols, w);
@@ -891,7 +948,7 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
 // Makes the images: a CTA takes the K or the V of one at a time, a block each of its eight
 // warps.  Also decides which requests have images, and reports bad metadata.
 template <int D>
-__global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
+__global__ void __launch_bounds__(256, 4) expand_fp8_kernel(const Params p) {
   constexpr uint32_t kHalf = Layout<D>::kHalf;
   extern __shared__ int32_t prefix[];  // [R + 1]: key tiles; then the scan's
   __shared__ int32_t nans[D];
@@ -1000,12 +1057,15 @@ __global__ void __launch_bounds__(256) expand_fp8_kernel(const Params p) {
     const bool nan = has_nan<D>(c);
     if (nan) note_nan<D>(c, nans, at, lane);
     store_values<D>(image + kHalf, warp, c, lane);
-    const bool any = __syncthreads_or(nan);
-    if (threadIdx.x == 0) {
-      p.image_nan[i] = any ? 1 : 0;
-      if (any) atomicOr(p.nan_seen, 1u);
-    }
-    if (any) {
+    const bool loud = c.e > kF8Loud;
+    if (!__syncthreads_or(nan || loud)) {
+      if (threadIdx.x == 0) p.image_nan[i] = 0;
+    } else {
+      const bool nan_here = __syncthreads_or(nan), loud_here = __syncthreads_or(loud);
+      if (threadIdx.x == 0) {
+        p.image_nan[i] = nan_here ? 1 : 0;
+        atomicOr(p.flags_seen, (nan_here ? 1u : 0u) | (loud_here ? 2u : 0u));
+      }
       if (threadIdx.x < D) {
         reinterpret_cast<int32_t*>(image + 2 * kHalf)[threadIdx.x] = nans[threadIdx.x];
         nans[threadIdx.x] = kNone;
@@ -1073,7 +1133,7 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, const MxPrefillScratch& ws, in
   p.group = a.num_heads / a.num_kv_heads;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
-  p.nan_seen = a.err + 1;
+  p.flags_seen = a.err + 1;
   p.entry_shift = 0;
   p.images = nullptr;
   p.image_base = p.image_nan = p.any = nullptr;

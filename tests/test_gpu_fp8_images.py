@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests.fp8_support import Step, check
+from tests.test_gpu_fp8_attention import rising_over_the_largest_values
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +164,29 @@ def test_scores_that_rise(heads, hkv, d, more, room):
     out, err = _run(step, ws, images=d == 128 or more > 0)
     assert err == 0
     check(out, *step.reference())
+
+
+@pytest.mark.parametrize("room", [True, False])
+@pytest.mark.parametrize("heads, hkv, d, mixed", [(4, 2, 128, False), (8, 2, 128, True), (4, 1, 64, True)])
+def test_scores_that_rise_over_the_largest_values(heads, hkv, d, mixed, room):
+    """Of requests over images and without (and of one that has no such values, beside them)."""
+    import paged_kv_cache_36_gb300 as pkv
+    more = 0 if d == 128 else 2000
+    reqs = [(520, 800 + more), (300, 900 + more), (3, 700), (1, 500)]
+    step = rising_over_the_largest_values(reqs, heads, hkv, d, mixed, seed=int(room))
+    n = step.seq[1]
+    for h in range(hkv):
+        step.set(step.v, False, 1, np.arange(n)[:, None], h, np.arange(d),
+                 step.rng.integers(0, 0x7F, (n, d)).astype(np.uint8))
+        for b in range(-(-n // 16)):
+            step.set_scale(step.v, 1, b, h, 120)
+    ws = None
+    if not room:
+        ws = torch.zeros_like(pkv.new_workspace_fp8(heads, hkv, d))
+        tile = _tile_bytes(hkv, d)
+        ws = ws[:ws.numel() - (256 << 20) // tile * tile]
+    out, err = _run(step, ws)
+    assert err == 0
+    ref, tol = step.reference()
+    assert 1e38 < ref.abs().max() < 3e38
+    check(out, ref, tol)
