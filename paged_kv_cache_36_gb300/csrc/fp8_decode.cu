@@ -680,8 +680,9 @@ __global__ void __launch_bounds__(256, 4) join_fp8_kernel(const Params p) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (k0 + kParts * k >= splits) break;
-        // 2^-9 at most: some hundred values near float32's end may be added up
-        const float w = exp2_approx(ml[k].x - mx - 10.f) * ml[k].y;
+        // 2^-13 at most: values near float32's end of as many ranges as there are, 16 an SM, may
+        // be added up
+        const float w = exp2_approx(ml[k].x - mx - 14.f) * ml[k].y;
         den += w;
         acc.x = fmaf(x[k].x, w, acc.x);
         acc.y = fmaf(x[k].y, w, acc.y);

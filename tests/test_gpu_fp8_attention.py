@@ -126,6 +126,18 @@ def test_the_largest_values():
     check(_run(step), ref, tol)
 
 
+def test_the_largest_values_in_more_than_a_thousand_ranges():
+    """Flat scores over 120000 keys of one KV head: ranges join to a finite result."""
+    step = Step(6, [(1, 119999)], 2, 1, 64)
+    step.q *= 2.0 ** -12
+    n = step.seq[0]
+    step.set(step.v, False, 0, np.arange(n)[:, None], 0, np.arange(64), 0x7E)
+    step.v[:, 16 * 64] = 246
+    ref, tol = step.reference()
+    assert 2.9e38 < ref.abs().min() and ref.abs().max() < 3e38
+    check(_run(step, max_query_len=1), ref, tol)
+
+
 def rising_over_the_largest_values(reqs, heads, hkv, d, mixed, seed=0):
     """Scores that rise by 16 to 24 (2^23 to 2^35) every so many keys of a request, in halves of
     blocks too, and fall again; values 1.75 2^127 (of odd KV heads the negative), or where mixed
