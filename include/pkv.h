@@ -545,7 +545,8 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * Both products take bfloat16 with float32 sums.  Keys, values and queries are exact in it (of
  * a decode row's query nothing is kept that is 2^126 times below the head's largest element).
  * Weights are rounded to 8 bits, numerator and denominator alike, and vanish 2^-102 below the
- * row's largest; scores (scale <q, k>) and their sums are float32.  scale must be finite.
+ * row's largest; scores (scale <q, k>) and their sums are float32, and so, for requests with
+ * several query tokens, is <q, k> itself: it must be below 2^128.  scale must be finite.
  * Sums of values are finite whatever the values and the scores, for up to 2^22 keys.
  *
  * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch, its first

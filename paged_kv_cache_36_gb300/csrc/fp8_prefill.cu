@@ -740,8 +740,9 @@ __global__ void __launch_bounds__(Shape<kImages>::kThreads, 1) prefill_fp8_kerne
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t o_cols = lane_addr + kColO + half * (D / 2);
     uint64_t* pair_bar = &bars[kPair0 + quad];
-    // never zero, for the masked scores' infinities; the scale's sign is on Q
-    const float f = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+    // never zero, for the masked scores' infinities (2^-149 leaves 2^-21 of the largest sums);
+    // the scale's sign is on Q
+    const float f = fmaxf(fabsf(p.scale_log2), 1.4e-45f);
     const uint32_t flags_seen = kImages ? __ldcg(p.flags_seen) : 0u;
     const bool nan_seen = (flags_seen & 1u) != 0u;
     const volatile uint32_t* loud = reinterpret_cast<volatile uint32_t*>(smem + L::kLoud);

@@ -195,6 +195,20 @@ def test_scores_at_the_ends():
         check(_run(step), *step.reference())
 
 
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, -2.0 ** -130, 2.0 ** -126])
+def test_the_smallest_scales_over_the_largest_sums(scale):
+    """<q, k> up to 2^127 or near, in single rows and in those of several tokens: scores of a few units
+    at most, of none at all with a scale of zero."""
+    step = Step(12, [(1, 200), (70, 65), (3, 0)], 8, 4, 128, lo=0, hi=0)
+    step.q.fill_(2.0 ** 114)
+    step.q[::2] *= -1
+    step.scale = scale
+    ref, tol = step.reference()
+    k = step.history(1)[0].sum(-1).abs().max() * 2.0 ** 114
+    assert 2.0 ** 125 < k < 2.0 ** 127 and (tol <= 2.0 ** -5 * ref.abs().max()).all()
+    check(_run(step), ref, tol)
+
+
 def test_rows_left_alone_and_bad_metadata():
     pkv = _pkv()
     step = Step(4, [(1, 20), (1, 40), (6, 3), (7, 40), (1, 9)], 4, 2, 64).upload()
