@@ -535,7 +535,7 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * num_heads / num_kv_heads may be any integer G up to 16; at most 8192 requests and 2^30
  * tokens, and unless max_query_len is 1, num_reqs * num_kv_heads * ceil(num_tokens / n) must
  * be below 2^31, n = floor(128 / G).  A block_table row has max_blocks_per_req <=
- * block_table_stride entries.  max_query_len as there (1: every row is a decode row; longer
+ * block_table_stride entries, all rows with one more each at most 2^31 - 16.  max_query_len as there (1: every row is a decode row; longer
  * ones are then not computed).  Rows of a request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
  * request, are left as they were; a block id outside the pool reads as zeros
  * (PKV_ERR_BLOCK_ID).  A request with several query tokens has 2^31 - 256 keys at most.

@@ -200,8 +200,9 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
   if (max_blocks_per_req <= 0 || (num_reqs > 1 && block_table_stride < max_blocks_per_req))
     return fail(PKV_E_INVALID, "%s: block_table rows of %d entries, %d apart", where,
                 max_blocks_per_req, block_table_stride);
-  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kF8RequestCost) > 0x7fffffffLL)
-    return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
+  // (the decode counts these units in 32 bits, and some more)
+  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kF8RequestCost) > 0x7fffffffLL - 15)
+    return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 16 entries, with one for each request", where);
   // (offsets that are garbage may give every request the same rows)
   const int64_t tile = 128 / (num_heads / num_kv_heads);
   if (max_query_len != 1 && (num_tokens + tile - 1) / tile * num_kv_heads > 0x7fffffffLL / num_reqs)

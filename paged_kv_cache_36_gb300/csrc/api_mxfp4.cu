@@ -135,8 +135,10 @@ int pkv_paged_attention_varlen_mxfp4(const void* q, int64_t q_stride, const void
   if (max_blocks_per_req <= 0 || (num_reqs > 1 && block_table_stride < max_blocks_per_req))
     return fail(PKV_E_INVALID, "%s: block_table rows of %d entries, %d apart", where,
                 max_blocks_per_req, block_table_stride);
-  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kMxRequestCost) > 0x7fffffffLL)
-    return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 1 entries", where);
+  // (the decode counts these units in 32 bits, and some more)
+  if (num_reqs * (static_cast<int64_t>(max_blocks_per_req) + kMxRequestCost) > 0x7fffffffLL - 15)
+    return fail(PKV_E_UNSUPPORTED, "%s: a block table of more than 2^31 - 16 entries, with %d for each request",
+                where, kMxRequestCost);
   AttnArgs a;
   a.q = q;
   a.q_stride = q_stride;

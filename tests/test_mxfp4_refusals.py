@@ -57,6 +57,12 @@ def test_attention(pkv, change, code):
     if code:
         assert b"pkv_paged_attention_varlen_mxfp4" in pkv.lib().pkv_last_error()
 
+@pytest.mark.parametrize("R, width", [(1, 0x7fffffff - 1), (1, 0x7fffffff - 15), (2, 1 << 30), (8192, 1 << 18)])
+def test_block_tables_that_32_bits_do_not_count(pkv, R, width):
+    """With what a request and a rounded division add to their entries."""
+    assert pkv.lib().pkv_paged_attention_varlen_mxfp4(
+        P, 256, P, P, P, width, width, P, P, P, 0.125, P, 256, 3, R, 4, 16, 4, 2, 64, 1, P, 1 << 40, None) == -2
+
 
 @pytest.mark.parametrize("H, hkv, d", [(4, 3, 64), (34, 2, 64), (0, 1, 64), (8, 8, 96)])
 def test_workspace_of_unsupported_heads(pkv, H, hkv, d):
