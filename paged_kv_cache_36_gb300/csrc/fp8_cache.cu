@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(write_threads<kRope>(), (sizeof(T) == 2 ? 1024
     constexpr int kLines = f8_chunk_bytes(D) / 128 + 1;
     const int64_t blk = static_cast<int64_t>(block_of[k]) * p.hkv * f8_chunk_bytes(D);
     for (int i = threadIdx.x; i < 2 * p.hkv * kLines; i += kThreads) {
-      const int item = i / kLines, at = (item >> 1) * f8_chunk_bytes(D) + min((i - item * kLines) * 128, f8_code_bytes(D));
+      const int item = i / kLines;
+      const int64_t at = static_cast<int64_t>(item >> 1) * f8_chunk_bytes(D) + min((i - item * kLines) * 128, f8_code_bytes(D));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(((item & 1) ? p.value_cache : p.key_cache) + blk + at));
     }
   }
@@ -635,7 +636,7 @@ __device__ __forceinline__ void gather_token(const GatherParams& p, int64_t t, i
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     float scale = 0.f;
     if (in) {
-      const uint8_t* chunk = kblk + h * f8_chunk_bytes(D);
+      const uint8_t* chunk = kblk + static_cast<int64_t>(h) * f8_chunk_bytes(D);
       w = __ldg(reinterpret_cast<const uint4*>(chunk + f8_key_at<D>(row, 16 * c)));
       scale = scale_of(chunk, D);
     }
@@ -661,7 +662,7 @@ __device__ __forceinline__ void gather_token(const GatherParams& p, int64_t t, i
       w[u] = make_uint4(0u, 0u, 0u, 0u);
       scale[u] = 0.f;
       if (in && i < nv) {
-        const uint8_t* chunk = vblk + h * f8_chunk_bytes(D);
+        const uint8_t* chunk = vblk + static_cast<int64_t>(h) * f8_chunk_bytes(D);
         w[u] = __ldg(reinterpret_cast<const uint4*>(chunk + c % (P / 4) * 512 + (c / (P / 4) * 4 + (row & 7) / 2) * 16));
         scale[u] = scale_of(chunk, D);
       }

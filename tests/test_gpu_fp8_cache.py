@@ -259,3 +259,23 @@ def test_other_stream_and_copied_blocks():
     s.synchronize()
     for a, b, x in zip(*outs, (k, v)):
         assert torch.equal(a, b) and ((a - x).abs() <= x.abs() * 2.0 ** -4 + 2.0 ** -12).all()
+
+
+def test_blocks_of_more_than_two_to_the_31_bytes():
+    """As many KV heads as are allowed: offsets inside a block pass 2^31."""
+    pkv = _pkv()
+    hkv, d = 1 << 20, 128
+    kc, vc = pkv.new_cache_fp8(1, hkv, d)
+    assert kc.shape[1] > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(2, hkv, d, generator=gen, device="cuda").to(BF16) for _ in "kv")
+    for slots in ([0, 5], [9, 2]):      # (the second call's rows join the first's)
+        slots = torch.tensor(slots, device="cuda")
+        pkv.reshape_and_cache_fp8(k, v, kc, vc, slots)
+        outs = [torch.empty_like(k) for _ in "kv"]
+        pkv.gather_cache_fp8(kc, vc, slots, *outs)
+        for out, x in zip(outs, (k, v)):
+            for h in range(0, hkv, 1 << 17):
+                a, b = out[:, h:h + (1 << 17)].float(), x[:, h:h + (1 << 17)].float()
+                # half a code's step, 2^-10 of a scale of at most 2^-5 below the codes' normal range
+                assert ((a - b).abs() <= b.abs() * 2.0 ** -4 + 2.0 ** -15).all()
