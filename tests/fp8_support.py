@@ -9,6 +9,49 @@ import torch
 from oracle import fp8
 
 
+def codes_of(x, e):
+    """e4m3 codes of float64 numbers at scale bytes e: oracle.fp8.code of whole arrays."""
+    grid = fp8.TABLE[:fp8.NAN]
+    y = np.abs(np.where(np.isfinite(x), x, 0.0)) * np.exp2(127.0 - e)
+    mids = (grid[1:] + grid[:-1]) / 2
+    i = np.searchsorted(mids, y)        # mids[i - 1] < y <= mids[i]
+    tie = (i < len(mids)) & (y == mids[np.minimum(i, len(mids) - 1)])
+    i += tie & (i % 2 == 1)
+    return np.where(np.isfinite(x), i + 128 * np.signbit(x), fp8.NAN).astype(np.uint8)
+
+
+def write_many(pool, slots, rows, is_key):
+    """oracle.fp8.write, block by block at once."""
+    _, hkv, d = rows.shape
+    slots = np.asarray(slots)
+    at = np.array([[fp8.place(t, i, d, is_key) for i in range(d)] for t in range(16)])
+    live, first = np.unique(slots[::-1], return_index=True)     # (the last of equal ones)
+    token = len(slots) - 1 - first
+    token, live = token[live >= 0], live[live >= 0]
+    blocks, of = np.unique(live // 16, return_inverse=True)
+    x = rows[token]
+    amax = np.zeros((len(blocks), hkv))
+    np.maximum.at(amax, of, np.abs(np.where(np.isfinite(x), x, 0.0)).max(-1))
+    m, ex = np.frexp(amax)
+    e = np.where(amax > 0, np.clip(127 + ex - 9 + (m > 0.875), fp8.LOW, fp8.HIGH), fp8.LOW)
+    chunks = pool.reshape(len(pool), hkv, -1)[blocks]
+    old = np.clip(chunks[..., 16 * d].astype(int), fp8.LOW, fp8.HIGH)
+    anew = np.zeros(len(blocks), bool)
+    anew[of[live % 16 == 0]] = True
+    e = np.where(anew[:, None], e, np.maximum(e, old))
+    codes = chunks[..., at]                                     # [blocks, hkv, 16, d]
+    down = codes_of(fp8.TABLE[codes & 127] * np.exp2(np.minimum(old - e, 0).astype(float))[..., None, None],
+                    np.full(codes.shape, 127))
+    down = np.where(down == fp8.NAN, fp8.NAN, down | codes & 128)
+    codes = np.where((e > old)[..., None, None], down, codes)
+    codes[anew] = 0
+    codes[of[:, None], np.arange(hkv), (live % 16)[:, None]] = codes_of(x, e[of][..., None])
+    chunks[..., at] = codes
+    chunks[..., 16 * d:] = 0
+    chunks[..., 16 * d] = e
+    pool.reshape(len(pool), hkv, -1)[blocks] = chunks
+
+
 class Step:
     """A flattened step of requests (query_len, past) over pools of random codes: those of the
     requests' tokens are numbers with scales 2^lo .. 2^hi, everything else is noise (NaN

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import fp8
+from tests.fp8_support import write_many
 
 
 @pytest.mark.parametrize("xs, e", [
@@ -64,3 +65,20 @@ def test_tables():
     w = fp8.frequencies(64, 1e4, "none", 1.0, 0, 0, 0)
     assert f[0] == w[0] == p[0] and f[-1] == w[-1] / 8 and p[-1] == w[-1] / 8
     assert np.isclose(fp8.frequencies(64, 1e4, "ntk", 8.0, 0, 0, 0)[-1], w[-1] / 8)
+
+
+@pytest.mark.parametrize("is_key", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_writes_of_whole_arrays_are_those_of_single_values(d, is_key):
+    rng = np.random.default_rng(d)
+    pools = [rng.integers(0, 256, (6, 2 * fp8.chunk_bytes(d)), dtype=np.uint8)]
+    pools.append(pools[0].copy())
+    for call in range(3):
+        slots = rng.integers(-1, 96, 30)
+        rows = rng.standard_normal((30, 2, d)) * np.exp2(rng.integers(-30, 30, (30, 2, 1)))
+        rows[3] = 0.0
+        rows[4, 0, :5] = np.nan, np.inf, -np.inf, -0.0, 464.0
+        rows[5] = rng.choice(np.concatenate([fp8.TABLE[:127], (fp8.TABLE[1:127] + fp8.TABLE[:126]) / 2]), (2, d))
+        fp8.write(pools[0], slots, rows, is_key)
+        write_many(pools[1], slots, rows, is_key)
+        assert np.array_equal(*pools)
