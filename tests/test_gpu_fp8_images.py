@@ -190,3 +190,30 @@ def test_scores_that_rise_over_the_largest_values(heads, hkv, d, mixed, room):
     ref, tol = step.reference()
     assert 1e38 < ref.abs().max() < 3e38
     check(out, ref, tol)
+
+
+@pytest.mark.parametrize("heads, hkv, d", [(32, 2, 64), (16, 1, 128)])
+def test_nan_of_one_query_tile_after_the_other(heads, hkv, d):
+    """Without room for images, ten and more query tiles a CTA: NaN that some rows of a tile see, in
+    some tiles, in several of a CTA in a row, and none in those between."""
+    import paged_kv_cache_36_gb300 as pkv
+    R = 160 // hkv + 40
+    rng = np.random.default_rng(d)
+    reqs = [(int(rng.integers(50, 65)) * 2 // hkv, int(rng.integers(0, 200))) for _ in range(R)]
+    tpt = 128 // (heads // hkv)
+    tiles = sum(-(-n // tpt) for n, _ in reqs) * hkv
+    assert tiles > 1600
+    step = Step(d, reqs, heads, hkv, d)
+    for r, (n, past) in enumerate(reqs):
+        if r // 7 % 3 == 0:     # (clean requests side by side)
+            continue
+        for pos in range(past, past + n, int(rng.integers(3, 20))):
+            step.set(step.v, False, r, pos, int(rng.integers(hkv)), int(rng.integers(d)), 0x7F if pos % 2 else 0xFF)
+    ref, tol = step.reference()
+    seen = ref.isnan().any(-1)
+    assert 0.05 < seen.double().mean() < 0.95
+    ws = torch.zeros_like(pkv.new_workspace_fp8(heads, hkv, d))
+    tile = _tile_bytes(hkv, d)
+    out, err = _run(step, ws[:ws.numel() - (256 << 20) // tile * tile])
+    assert err == 0
+    check(out, ref, tol)
