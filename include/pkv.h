@@ -581,8 +581,9 @@ int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* 
  *                    pairs: a = floor(c(high)), 0 at least, b = ceil(c(low)), rotary_dim - 1
  *                    at most, c(n) = rotary_dim log(L / 2 pi n) / (2 log base), the pair
  *                    that makes n turns.
- * Frequencies, angles and their remainders are 64-bit; entries are off by 2^-23 of
- * attention_factor at most.  base > 1; factor >= 1 (but for PKV_ROPE_NONE); 0 < low < high and L > 0
+ * f_i is 64-bit floating point, angles and their remainders from there on 64-bit fixed point;
+ * entries are off by 2^-23 of attention_factor at most, which is a finite float32 (below 2^-126
+ * by 2^-149 more).  base > 1; factor >= 1 (but for PKV_ROPE_NONE); 0 < low < high and L > 0
  * (PARTS and YARN); rotary_dim even, 512 at most (NTK: 4 at least); start + num_positions <= 2^26.
  * ---------------------------------------------------------------------- */
 #define PKV_ROPE_NONE 0

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kMaxGroup = 16;
 constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of a call: the kernels count on from them in 32 bits
-constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's angles are good to 2^-25 below it
+constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's frequencies are good to 2^-26 of a radian below it
 
 // Whether some of T rows of na bytes, sa apart, share a byte with rows of nb bytes, sb apart.
 // (Of rows whose strides differ, whether their extents overlap.)
@@ -26,6 +26,37 @@ bool rows_overlap(const void* a, int64_t sa, int64_t na, const void* b, int64_t 
   const int64_t d = static_cast<const char*>(b) - static_cast<const char*>(a);
   const int64_t m = (d % sa + sa) % sa;  // where b's rows begin between a's
   return m < na || m + nb > sa;
+}
+
+constexpr double kTau = 6.283185307179586476925;
+constexpr double kTauLow = 2.4492935982947064e-16;  // what kTau lacks of 2 pi
+
+// w radians, w in [0, 1], as turns of 64 bits behind the point, to the nearest.
+uint64_t turns_of(double w) {
+  const double q = w / kTau;
+  const double q_low = (std::fma(-q, kTau, w) - q * kTauLow) / kTau;
+  const double whole = std::floor(std::ldexp(q, 64));
+  const double rest = std::ldexp(q, 64) - whole + std::ldexp(q_low, 64);
+  return static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(rest)));
+}
+
+// The series of a finite float32's factor (Taylor's).
+RotarySeries series_of(double factor) {
+  int e;
+  const double f = 2.0 * std::frexp(factor, &e);
+  RotarySeries s;
+  s.unit = static_cast<float>(std::ldexp(1.0, e - 1));
+  double term = f;  // f (2 pi)^k / k!
+  for (int k = 0; k <= 10; ++k) {
+    const double x = (k & 2) ? -term : term;
+    float& to = k % 2 ? s.s[k / 2] : s.c[k / 2];
+    to = static_cast<float>(x);
+    if (k == 0) s.c_low = static_cast<float>(x - to);
+    if (k == 1) s.s_low = static_cast<float>(x - to);
+    if (k == 2) s.c1_low = static_cast<float>(x - to);
+    term *= kTau / (k + 1);
+  }
+  return s;
 }
 
 struct F8Workspace {
@@ -260,8 +291,8 @@ int pkv_build_cos_sin_cache(float* out, int64_t num_positions, int64_t start, in
     return fail(PKV_E_UNSUPPORTED, "%s: rotary_dim of at most %d", where, 2 * kMaxRotaryPairs);
   if (num_positions > kMaxPosition || start > kMaxPosition - num_positions)
     return fail(PKV_E_UNSUPPORTED, "%s: positions past 2^26", where);
-  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(attention_factor))
-    return fail(PKV_E_INVALID, "%s: base must be above 1, and attention_factor finite", where);
+  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(static_cast<float>(attention_factor)))
+    return fail(PKV_E_INVALID, "%s: base must be above 1, and attention_factor a finite float32", where);
   if (scaling < PKV_ROPE_NONE || scaling > PKV_ROPE_YARN)
     return fail(PKV_E_INVALID, "%s: scaling %d", where, scaling);
   if (scaling != PKV_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
@@ -273,11 +304,11 @@ int pkv_build_cos_sin_cache(float* out, int64_t num_positions, int64_t start, in
     return fail(PKV_E_INVALID, "%s: original_max_position must be positive, and 0 < low < high", where);
   if (num_positions == 0) return PKV_OK;
   if (!out || !aligned16(out)) return fail(PKV_E_INVALID, "%s: the table must be 16-byte aligned", where);
-  const double tau = 6.283185307179586476925, rd = rotary_dim;
+  const double rd = rotary_dim;
   const double b = scaling == PKV_ROPE_NTK ? base * std::pow(factor, rd / (rd - 2)) : base;
   // the pair that makes `turns` turns within the original length
   auto pair = [&](double turns) {
-    return rd * std::log(static_cast<double>(original_max_position) / (tau * turns)) / (2 * std::log(base));
+    return rd * std::log(static_cast<double>(original_max_position) / (kTau * turns)) / (2 * std::log(base));
   };
   const double first = banded ? std::max(std::floor(pair(high)), 0.0) : 0.0;
   const double last = banded ? std::min(std::ceil(pair(low)), rd - 1) : 0.0;
@@ -286,14 +317,14 @@ int pkv_build_cos_sin_cache(float* out, int64_t num_positions, int64_t start, in
     double w = std::pow(b, -2.0 * i / rd), keep = 1.0;
     if (scaling == PKV_ROPE_LINEAR) keep = 0.0;
     if (scaling == PKV_ROPE_PARTS)
-      keep = (static_cast<double>(original_max_position) * w / tau - low) / (high - low);
+      keep = (static_cast<double>(original_max_position) * w / kTau - low) / (high - low);
     if (scaling == PKV_ROPE_YARN) keep = 1.0 - (i - first) / std::max(last - first, 0.001);
     keep = std::min(std::max(keep, 0.0), 1.0);
     w = keep == 1.0 ? w : keep * w + (1.0 - keep) * w / factor;
-    f.turns[i] = static_cast<uint64_t>(std::ldexp(w / tau, 64));  // (below a sixth of a turn)
+    f.turns[i] = turns_of(w);  // (below a sixth of a turn)
   }
   const cudaError_t e = launch_rotary_table(f, out, num_positions, start, rotary_dim,
-                                            static_cast<float>(attention_factor), static_cast<cudaStream_t>(stream));
+                                            series_of(attention_factor), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "build_cos_sin_cache launch");
   return PKV_OK;
 }

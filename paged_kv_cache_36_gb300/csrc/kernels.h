@@ -272,8 +272,15 @@ constexpr int kMaxRotaryPairs = 256;
 struct RotaryFrequencies {
   uint64_t turns[kMaxRotaryPairs];
 };
+// factor cos(2 pi r) / unit = c[0] + c[1] r^2 + c[2] r^4 ..., factor sin(2 pi r) / unit = s[0] r +
+// s[1] r^3 ...; with what c[0], c[1] and s[0] lose in float32.
+struct RotarySeries {
+  float c[6], c_low, c1_low;
+  float s[5], s_low;
+  float unit;  // a power of two
+};
 cudaError_t launch_rotary_table(const RotaryFrequencies& f, float* out, int64_t rows, int64_t start,
-                                int32_t rotary_dim, float factor, cudaStream_t stream);
+                                int32_t rotary_dim, const RotarySeries& series, cudaStream_t stream);
 
 // A step's metadata built on the device.
 struct StepMetadataArgs {

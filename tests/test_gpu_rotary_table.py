@@ -1,6 +1,9 @@
 """The table of rotary angles against float64: an entry is the float32 nearest to its value,
 but for the errors of the float32 sine and cosine (2^-23 of the factor in all)."""
 
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -27,6 +30,34 @@ def test_table(n, rd, start, base, scaling, factor, length, low, high, attention
     assert got.shape == (n, rd) and got.dtype is torch.float32
     # 2^-23 of the factor (documented), and what a 64-bit angle of 2^26 is off by itself
     assert np.abs(got.double().cpu().numpy() - want).max() <= attention * (2.0 ** -23 + (start + n) * 2.0 ** -51)
+
+
+TAU = Fraction("6.28318530717958647692528676655900576839433879875021164194989")
+
+
+def _exact(n, rd, start, freqs, attention):
+    """float64 [n, rd] from angles in turns, 64 bits behind the point (of 2^26 positions 2^-39)."""
+    turns = np.array([round(Fraction(f) / TAU * 2 ** 64) % 2 ** 64 for f in freqs], np.uint64)
+    with np.errstate(over="ignore"):
+        rest = (np.arange(start, start + n, dtype=np.uint64)[:, None] * turns).view(np.int64)
+    angle = rest.astype(np.float64) * (2.0 ** -64 * 2 * math.pi)
+    return attention * np.concatenate([np.cos(angle), np.sin(angle)], 1)
+
+
+@pytest.mark.parametrize("scaling, factor, attention, start", [
+    ("yarn", 8.0, None, 0), ("yarn", 32.0, None, 100000), ("yarn", 40.0, None, 0), ("linear", 4.0, 0.7, 1 << 20),
+    ("none", 1.0, 1.069, 0), ("parts", 8.0, -1.45, (1 << 26) - 40000), ("none", 1.0, 1.0, 3), ("ntk", 4.0, 1e-30, 0),
+    ("none", 1.0, 3.4e38, 0)])
+def test_the_documented_bound(scaling, factor, attention, start):
+    """2^-23 of the factor, over 5 million entries."""
+    import paged_kv_cache_36_gb300 as pkv
+    n, rd = 40000, 128
+    got = pkv.build_cos_sin_cache(n, rd, scaling=scaling, factor=factor, original_max_position=4096,
+                                  attention_factor=attention, start=start)
+    if attention is None:
+        attention = 0.1 * np.log(factor) + 1.0
+    want = _exact(n, rd, start, fp8.frequencies(rd, 1e4, scaling, factor, 4096, 1.0, 32.0), attention)
+    assert np.abs(got.double().cpu().numpy() - want).max() <= abs(attention) * 2.0 ** -23
 
 
 def test_extending_and_rotating_with_it():
