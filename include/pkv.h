@@ -496,8 +496,11 @@ int64_t pkv_fp8_block_bytes(int32_t block_size, int32_t num_kv_heads, int32_t he
  * begins it anew: the block's own e does not count, and rows that the call does not write
  * become zero.  (Blocks fill from row 0, so a recycled one forgets its old scale.)
  * Of a slot given twice the last of its tokens counts; the result does not depend on the
- * order of the others.  A call whose tokens are not in the order of their blocks costs a
- * search of all slots for each token: num_tokens^2 / 32 steps of a warp.  At most 2^30 tokens. */
+ * order of the others.  The search for a block's tokens reads all slots of the call, so the
+ * cost has a part that grows with num_tokens^2: once for each 16 tokens in the order of their
+ * blocks, for each two in the worst order.  Of 8 KV heads of 128 in bfloat16 32768 tokens take
+ * 0.08 ms in order and 0.28 in none, 131072 0.5 and 2.9, 2^20 24 and 183.  At most 2^20 tokens
+ * (more in several calls, each of whole blocks). */
 int pkv_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_stride,
                               int64_t value_stride, void* key_cache, void* value_cache,
                               const int64_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,

@@ -15,7 +15,8 @@ namespace pkv {
 namespace {
 
 constexpr int kMaxGroup = 16;
-constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of a call: the kernels count on from them in 32 bits
+constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of an attention: the kernels count on from them in 32 bits
+constexpr int64_t kMaxWritten = int64_t{1} << 20;  // of a write, whose search takes their square
 constexpr int64_t kMaxPosition = int64_t{1} << 26;  // the table's frequencies are good to 2^-26 of a radian below it
 
 // Whether some of T rows of na bytes, sa apart, share a byte with rows of nb bytes, sb apart.
@@ -108,7 +109,7 @@ int pkv_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_st
                             slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads,
                             head_dim, dtype, error_word, &a.cache);
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  if (num_tokens > kMaxTokens) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^30 tokens", where);
+  if (num_tokens > kMaxWritten) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^20 tokens", where);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_write_fp8(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "reshape_and_cache_fp8 launch");
@@ -130,7 +131,7 @@ int pkv_rope_reshape_and_cache_fp8(const int64_t* positions, const void* query, 
                             slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads,
                             head_dim, dtype, error_word, &a.cache);
   if (rc != PKV_OK) return rc;
-  if (num_tokens > kMaxTokens) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^30 tokens", where);
+  if (num_tokens > kMaxWritten) return fail(PKV_E_UNSUPPORTED, "%s: more than 2^20 tokens", where);
   if (num_heads <= 0 || num_heads > (1 << 20) || max_position < 0)
     return fail(PKV_E_INVALID, "%s: bad sizes", where);
   const int64_t es = dtype == PKV_F32 ? 4 : 2;

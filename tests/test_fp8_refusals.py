@@ -42,6 +42,16 @@ def test_cache_write_and_gather(pkv, name, change, code):
     assert getattr(pkv.lib(), name)(*args) == code
 
 
+@pytest.mark.parametrize("T, code", [((1 << 20) + 1, -2), (1 << 30, -2), (1 << 20, -1)])
+def test_writes_that_would_search_for_long(pkv, T, code):
+    """Tokens past 2^20 are refused (and 2^20 by another check: a null table, rows off 16 bytes)."""
+    tail = [T, 1 << 20, 16, 2, 64, 1, None, None]
+    assert pkv.lib().pkv_rope_reshape_and_cache_fp8(P, 4 * P, 256, 6 * P, 256, 4, P, 128, 2 * P, 128, 3 * P, 3 * P, P,
+                                                    None, 10, 64, 1, *tail) == code
+    rows = P if code == -2 else P + 8
+    assert pkv.lib().pkv_reshape_and_cache_fp8(rows, rows, 128, 128, P, P, P, *tail) == code
+
+
 @pytest.mark.parametrize("change, code", [
     (dict(T=0), 0), (dict(T=-1), -1), (dict(T=1 << 31), -2), (dict(T=(1 << 30) + 1), -2), (dict(H=0), -1), (dict(rd=0), -2),
     (dict(rd=72), -2), (dict(rd=24), -2), (dict(rd=8, neox=0, dtype=1), 1), (dict(rd=8), -2),
