@@ -538,11 +538,11 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * num_heads / num_kv_heads may be any integer G up to 16; at most 8192 requests and 2^30
  * tokens, and unless max_query_len is 1, num_reqs * num_kv_heads * ceil(num_tokens / n) must
  * be below 2^31, n = floor(128 / G).  A block_table row has max_blocks_per_req <=
- * block_table_stride entries, all rows with one more each at most 2^31 - 16.  max_query_len as there (1: every row is a decode row; longer
- * ones are then not computed).  Rows of a request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last
- * request, are left as they were; a block id outside the pool reads as zeros
- * (PKV_ERR_BLOCK_ID).  A request with several query tokens has 2^31 - 256 keys at most.
- * Bytes of tokens past a request's end may hold anything; a NaN in a key counts for the rows
+ * block_table_stride entries, all rows with one more each at most 2^31 - 16.  max_query_len
+ * as there (1: every row is a decode row; longer ones are then not computed).  Rows of a
+ * request whose metadata fails the checks (PKV_ERR_METADATA), and rows behind the last request,
+ * are left as they were; a block id outside the pool reads as zeros (PKV_ERR_BLOCK_ID).  A
+ * request with several query tokens has 2^31 - 256 keys at most.  Bytes of tokens past a request's end may hold anything; a NaN in a key counts for the rows
  * that see it, a NaN in a value for that dimension of those rows, and for no others.
  *
  * Both products take bfloat16 with float32 sums.  Keys, values and queries are exact in it (of
@@ -552,10 +552,15 @@ int pkv_gather_cache_fp8(const void* key_cache, const void* value_cache,
  * several query tokens, is <q, k> itself: it must be below 2^128.  scale must be finite.
  * Sums of values are finite whatever the values and the scores, for up to 2^22 keys.
  *
- * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch, its first
- * 256 bytes zero before its first use, word 0 the error word; two calls that overlap on the
- * GPU must not share one.  All arguments, the metadata among them, are read only after the
- * work before the call on `stream`. */
+ * Requests whose keys are read often enough have them and their values converted to bfloat16
+ * once, in the workspace's last 256 MiB; what finds no room there (some 65000 tokens of 8 KV
+ * heads of 128) is converted again for every 128 / G query tokens.
+ *
+ * The workspace is pkv_fp8_attention_workspace_bytes() bytes whatever the batch (all but its
+ * last 256 MiB are needed, and decode rows use no more), its first 256 bytes zero before its
+ * first use, word 0 the error word; two calls that overlap on the GPU must not share one.  All
+ * arguments, the metadata among them, are read only after the work before the call on
+ * `stream`. */
 size_t pkv_fp8_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
 int pkv_paged_attention_varlen_fp8(const void* q, int64_t q_stride, const void* key_cache,
                                    const void* value_cache, const int32_t* block_table,

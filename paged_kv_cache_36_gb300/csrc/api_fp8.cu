@@ -64,7 +64,7 @@ struct F8Workspace {
   size_t plan, ml, o, image_base, images, tile, total;
 };
 
-// Room for the prefill's converted key tiles: 511 of 8 KV heads of 128, 65408 tokens.
+// Room for the prefill's converted key tiles: 508 of 8 KV heads of 128, 65024 tokens.
 constexpr size_t kImageRoom = 256u << 20;
 
 // The error word's 256 bytes, then the decode's plan (for the largest batch) and partials,

@@ -817,7 +817,7 @@ cudaError_t write_t(const F8WriteArgs& a, cudaStream_t stream) {
   p.window = static_cast<int32_t>(want < kWriteWindow ? want : kWriteWindow);
   const int windows = (p.num_tokens + p.window - 1) / p.window;
   p.splits = (2 * p.hkv + kThreads / 32 - 1) / (kThreads / 32);
-  const int most = 4 * sms / windows;  // one wave
+  const int most = 4 * sms / windows;  // (bfloat16: one wave, of CTAs of 512 threads two)
   if (p.splits > most) p.splits = most > 1 ? most : 1;
   p.cache_ctas = windows * p.splits;
   int64_t grid = p.cache_ctas;
