@@ -61,7 +61,7 @@ constexpr int kMinUnits = 3;     // units in a range, nearly: at least 2, more t
 // stay finite, over the others' always.
 constexpr float kLargest = -24.f, kMost = 8.f, kMostLoud = -23.f;
 constexpr int kMaxStages = 6;
-constexpr int kWarpPlan = 128;   // requests up to which a warp makes the plan for itself
+constexpr int kWarpPlan = 32;     // requests up to which a warp makes the plan for itself
 
 template <int NT>
 constexpr int warps_per_cta() { return NT == 1 ? 16 : 8; }
@@ -197,25 +197,17 @@ __global__ void __launch_bounds__(warps_per_cta<NT>() * 32, 1)
     return nb > 0 ? nb + kF8RequestCost : 0;
   };
   if (R <= kWarpPlan) {
-    // every warp makes all of it (and writes what the others write), so none waits for another:
-    // one request of 1000 tokens 8.9 -> 8.6 us, 8 of 300 to 500 11.7 -> 11.0, 16 of 8000 34.9 ->
-    // 34.4, 64 of 128 to 4096 55.4 -> 55.6
-    int carry = 0, units[kWarpPlan / 32];
+    // every warp makes all of it (and writes what the others write), so none waits for another.
+    // Requests of 100 to 300 tokens, 32/8 heads of 128, each way and by the CTA together: 1 10.3
+    // and 10.6 us, 16 11.5 and 12.3, 32 11.7 and 13.0; with up to 128 to a warp, four a lane, 33
+    // 14.0 and 13.9, 64 17.1 and 16.5, 128 23.2 and 20.6.
+    int inc = lane < R ? units_of(lane, warp == 0) : 0;
 #pragma unroll
-    for (int k = 0; k < kWarpPlan / 32; ++k)
-      units[k] = 32 * k + lane < R ? units_of(32 * k + lane, warp == 0) : 0;
-#pragma unroll
-    for (int k = 0; k < kWarpPlan / 32; ++k) {
-      if (32 * k >= R) break;
-      int inc = units[k];
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, x);
-        if (lane >= x) inc += y;
-      }
-      if (32 * k + lane < R) prefix[32 * k + lane + 1] = carry + inc;
-      carry += __shfl_sync(0xffffffffu, inc, 31);
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += y;
     }
+    if (lane < R) prefix[lane + 1] = inc;
     if (lane == 0) prefix[0] = 0;
     __syncwarp();
   } else {
