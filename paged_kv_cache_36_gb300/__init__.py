@@ -626,7 +626,8 @@ def fp8_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: i
 
 
 def new_workspace_fp8(num_heads: int, num_kv_heads: int, head_dim: int, device="cuda"):
-    """A workspace of paged_attention_varlen_fp8, for any batch."""
+    """A workspace of paged_attention_varlen_fp8, for any batch.  All but its last 256 MiB are
+    needed: a shorter slice serves, with less room for what long prompts convert ahead."""
     import torch
     ws = torch.empty(fp8_attention_workspace_bytes(num_heads, num_kv_heads, head_dim),
                      dtype=torch.uint8, device=device)

@@ -36,9 +36,9 @@
 //     one exceeds that by 2^32 (by 2 where the block's values are large, kF8Loud): the common
 //     block needs a vote, and no shuffle, and sums stay finite for any values there are.
 //
-// What bounds it.  8 requests of 131072 tokens with 64 query and 8 KV heads of 128 take 326 to 330
+// What bounds it.  8 requests of 131072 tokens with 64 query and 8 KV heads of 128 take 325
 // us, 6.6 TB/s, 97 to 98 % of the copy rate.  64 requests of 128 to 4096 tokens (32/8 heads of
-// 128, 284 MB) take 55.6 us.  By the kernel's clocks (when blocks still made the plan together)
+// 128, 284 MB) take 55.3 us.  By the kernel's clocks (when blocks still made the plan together)
 // the plan was there at 2.0 us, the first data at 6.9, the last block at 41 to 50.4, median 47.4:
 // 7.0 TB/s in between; the start and the join are the rest.
 #include <cuda_bf16.h>
