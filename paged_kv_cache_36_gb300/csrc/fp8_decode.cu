@@ -61,7 +61,7 @@ constexpr int kMinUnits = 3;     // units in a range, nearly: at least 2, more t
 // stay finite, over the others' always.
 constexpr float kLargest = -24.f, kMost = 8.f, kMostLoud = -23.f;
 constexpr int kMaxStages = 6;
-constexpr int kWarpPlan = 32;     // requests up to which a warp makes the plan for itself
+constexpr int kWarpPlan = 32;    // requests up to which a warp makes the plan for itself
 
 template <int NT>
 constexpr int warps_per_cta() { return NT == 1 ? 16 : 8; }

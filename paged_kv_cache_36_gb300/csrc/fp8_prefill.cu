@@ -15,9 +15,9 @@
 //     it reads as D / 32 coalesced vectors, and writes rows to the stage.
 //
 // Large values.  The reference of a row's weights moves at once in key tiles that hold some
-// (kF8Loud), so that sums stay finite; without images a warp notes which.  Over images it
-// does in all key tiles if one of the call's holds some (a word read for each: a prompt of 16384
-// tokens 1434 us where without it took 1407).
+// (kF8Loud), so that sums stay finite; without images a warp notes which.  Over images it does
+// so in all key tiles if one of the call's holds some (with a word read for each of them a
+// prompt of 16384 tokens took 1434 us instead of 1407).
 //
 // NaN.  Zero times NaN would poison rows that do not see a NaN in V, so one is stored as
 // zero and its position noted by dimension; a row at or behind it gets NaN there.  (In a tile
@@ -26,7 +26,8 @@
 // Warp roles: warp 0 owns the tensor memory and issues Q K^T, warp 1 issues P V; over images
 // warps 2 and 3 copy K and V; warps 4-11 run the softmax and the epilogue, two per 32-lane
 // quadrant of tensor memory, each with half of the key tile's columns; warps 12-15 bring the
-// query rows in, and without images they convert K, warps 16-19 V, and warp 2 notes large values.
+// query rows in, and without images they convert K, warps 16-19 V, and warp 2 notes large
+// values.
 //
 // What bounds it.  A prompt of 4096 tokens with 32 query and 8 KV heads of 128 takes 129 us,
 // 1065 TFLOP/s, 56 % of the bf16 rate; of 16384 tokens 1400 us, 1571 TFLOP/s, 83 %.  Neither the
@@ -74,13 +75,13 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = kSBufs * kKeys;
 // Weights are 2^(score - m): a new reference m puts the largest at 2^kLargest, and m moves when
-// 64 of a row add up to more than kMost, or in a key tile of large values (kF8Loud) kMostLoud:
-// sums over 2^22 keys of those stay finite, over the others' always.  So O is rescaled once a row's maximum has grown by
-// 2^26 to 2^32 (2^8, as for bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134),
-// sums of flat scores stay finite for any values there are, and weights vanish (at 2^-126) 102
-// binades below the largest.  Only a row's first key tile, and one that moves m, needs the
-// maximum itself (found in every tile: a prompt of 16384 tokens 1475 us instead of 1430).
-constexpr float kLargest = -24.f, kMost = 256.f, kMostLoud = 1.f / 131072;  // (64 equal ones 2^-18)
+// 64 of a row add up to more than kMost.  So O is rescaled once a row's maximum has grown by
+// 2^26 to 2^32 (2^8, as for bfloat16 caches: a prompt of 4096 tokens 146 us instead of 134), and
+// weights vanish (at 2^-126) 102 binades below the largest.  In a key tile of large values
+// (kF8Loud) the sum may be kMostLoud, twice that of 64 of the largest: sums over 2^22 of those
+// keys stay finite, and over others always.  Only a row's first key tile, and one that moves m,
+// needs the maximum itself (found in every tile: a prompt of 16384 tokens 1475 us instead of 1430).
+constexpr float kLargest = -24.f, kMost = 256.f, kMostLoud = 1.f / 131072;
 constexpr int kPrefixMax = 4096;           // entries of the plan in shared memory
 constexpr int kMaxKeys = 0x7fffff00;       // a whole key tile more is still an int
 constexpr size_t kSmemLimit = 232448;
